@@ -6,6 +6,7 @@ is missing (build it with ``python allreduce_schedule_algorithms_amd/build_lib.p
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import enum
 import os
@@ -16,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("AR_LIBRARY") or os.path.join(_HERE, "libar_mi355x.so")
 
 AR_MAX_RANKS = 256
+AR_MAX_GRADS = 65536
 
 
 class Status(enum.IntEnum):
@@ -90,6 +92,12 @@ class Exec(enum.IntEnum):
     AR_EXEC_DAG = 3
 
 
+class Norm(enum.IntEnum):
+    AR_NORM_L2 = 0
+    AR_NORM_MAX = 1
+
+
+NORMS = {"l2": Norm.AR_NORM_L2, "max": Norm.AR_NORM_MAX}
 DTYPES = {"int32": Dtype.AR_INT32, "fp32": Dtype.AR_FP32, "bf16": Dtype.AR_BF16}
 OPS = {"sum": Op.AR_SUM, "max": Op.AR_MAX, "avg": Op.AR_AVG}
 COLLECTIVES = {"allreduce": Collective.AR_ALLREDUCE, "reduce_scatter": Collective.AR_REDUCE_SCATTER,
@@ -146,6 +154,17 @@ class ar_cost_model(C.Structure):
                 ("reserved", C.c_int32)]
 
 
+class ar_grad(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64), ("dtype", C.c_int32),
+                ("out_dtype", C.c_int32)]
+
+
+class ar_clip(C.Structure):
+    _fields_ = [("norm", C.c_int32), ("max_norm", C.c_float), ("eps", C.c_float), ("total", C.c_void_p),
+                ("each", C.c_void_p), ("known", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_size_t), ("start_event", C.c_void_p), ("stop_event", C.c_void_p)]
+
+
 # exported symbol -> (restype, argtypes)
 SIGNATURES = {
     "ar_allreduce": (C.c_int, [C.POINTER(C.c_void_p), C.c_int32, C.c_int64, C.c_int32, C.c_int32, C.c_int32,
@@ -179,6 +198,13 @@ SIGNATURES = {
     "ar_get_cost_model": (C.c_int, [C.POINTER(ar_cost_model)]),
     "ar_select": (C.c_int, [C.POINTER(ar_call), C.POINTER(C.c_int32), C.POINTER(C.c_int32),
                             C.POINTER(C.c_double)]),
+    "ar_grad_norm": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(ar_clip), C.c_void_p]),
+    "ar_grad_clip": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(ar_clip), C.c_void_p]),
+    "ar_grad_workspace_bytes": (C.c_int, [C.c_void_p, C.c_int32, C.POINTER(ar_clip), C.POINTER(C.c_size_t)]),
+    "ar_allreduce_clip": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                    C.POINTER(ar_clip), C.c_void_p]),
+    "ar_allreduce_clip_workspace_bytes": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
+                                                    C.POINTER(ar_clip), C.POINTER(C.c_size_t)]),
     "ar_status_string": (C.c_char_p, [C.c_int]),
     "ar_last_hip_error": (C.c_int32, []),
     "ar_last_error_message": (C.c_char_p, []),
@@ -331,6 +357,67 @@ def ar_set_launch_blocks(max_blocks: int) -> int:
     prev = C.c_int64(0)
     _check(lib.ar_set_launch_blocks(int(max_blocks), C.byref(prev)))
     return prev.value
+
+
+# ---- gradient norms and clipping ----
+class GradList:
+    """Host table of ar_grad records. It holds addresses, so what owns the tensors' memory has to outlive its use."""
+
+    def __init__(self, words, count):
+        self.words = array.array("Q", words)  # a record is four words: data, out, n, dtype | out_dtype << 32
+        self.count = count
+        self.address = self.words.buffer_info()[0]
+
+
+def marshal_grads(records) -> GradList:
+    """GradList of (data, out, n, dtype, out_dtype) records: addresses as integers (out 0: in place), types by name
+    or value. Built once, a caller that repeats calls on the same tensors passes it again."""
+    words = []
+    count = 0
+    for data, out, n, dtype, out_dtype in records:
+        if n < 0:
+            raise ArError(Status.AR_INVALID_ARGUMENT, f"tensor {count}: n must be >= 0")
+        words += (data, out, n, _enum(DTYPES, dtype) | _enum(DTYPES, out_dtype) << 32)
+        count += 1
+    return GradList(words, count)
+
+
+def make_clip(norm="l2", max_norm=0.0, eps=1e-6, total=None, each=None, known=None, workspace=None, workspace_bytes=0,
+              start_event=None, stop_event=None) -> ar_clip:
+    def ptr(t):
+        return t if t is None or isinstance(t, int) else t.data_ptr()
+    return ar_clip(_enum(NORMS, norm), float(max_norm), float(eps), ptr(total), ptr(each), ptr(known), ptr(workspace),
+                   int(workspace_bytes), _event(start_event), _event(stop_event))
+
+
+def ar_grad_norm(grads: GradList, clip: ar_clip, stream=None):
+    _check(lib.ar_grad_norm(grads.address, grads.count, C.byref(clip), _stream(stream)))
+
+
+def ar_grad_clip(grads: GradList, clip: ar_clip, stream=None):
+    _check(lib.ar_grad_clip(grads.address, grads.count, C.byref(clip), _stream(stream)))
+
+
+def ar_grad_workspace_bytes(grads: GradList, clip: ar_clip) -> int:
+    out = C.c_size_t(0)
+    _check(lib.ar_grad_workspace_bytes(grads.address, grads.count, C.byref(clip), C.byref(out)))
+    return out.value
+
+
+def ar_allreduce_clip(bufs, n, P, dtype, op, collective, clip: ar_clip, stream=None):
+    """bufs: buckets * P pointers or tensors, bucket by bucket; n: the buckets' elements."""
+    sizes = array.array("q", n)
+    _check(lib.ar_allreduce_clip(_ptrs(bufs), sizes.buffer_info()[0], len(sizes), int(P), _enum(DTYPES, dtype),
+                                 _enum(OPS, op), _enum(COLLECTIVES, collective), C.byref(clip), _stream(stream)))
+
+
+def ar_allreduce_clip_workspace_bytes(n, P, dtype, op, collective, clip: ar_clip) -> int:
+    sizes = array.array("q", n)
+    out = C.c_size_t(0)
+    _check(lib.ar_allreduce_clip_workspace_bytes(sizes.buffer_info()[0], len(sizes), int(P), _enum(DTYPES, dtype),
+                                                 _enum(OPS, op), _enum(COLLECTIVES, collective), C.byref(clip),
+                                                 C.byref(out)))
+    return out.value
 
 
 def ar_schedule_build(call: ar_call) -> "Schedule":

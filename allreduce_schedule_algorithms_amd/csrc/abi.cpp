@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "exec.h"
+#include "grad.h"
 #include "sched.h"
 
 static_assert(sizeof(ar_oprec) == sizeof(ar::OpRec), "ar_oprec layout");
@@ -104,6 +105,152 @@ ar_status check_bufs(void* const* bufs, int P) {
   for (int p = 1; p < P; ++p)
     if (v[p] == v[p - 1]) return fail(AR_INVALID_ARGUMENT, "two ranks share one buffer");
   return AR_OK;
+}
+
+bool is_float(int32_t dtype) { return dtype == AR_FP32 || dtype == AR_BF16; }
+int64_t float_bytes(int32_t dtype) { return dtype == AR_BF16 ? 2 : 4; }
+constexpr int64_t kMaxElements = int64_t(1) << 48;
+
+ar_status check_clip(const ar_clip* c, bool scale, ar::Clip* out) {
+  if (!c) return fail(AR_INVALID_ARGUMENT, "clip is NULL");
+  if (c->norm != AR_NORM_L2 && c->norm != AR_NORM_MAX) return fail(AR_INVALID_ARGUMENT, "unknown norm");
+  if (scale) {
+    if (!(c->max_norm >= 0)) return fail(AR_INVALID_ARGUMENT, "max_norm must be >= 0");
+    if (!(c->eps >= 0) || std::isinf(c->eps)) return fail(AR_INVALID_ARGUMENT, "eps must be finite and >= 0");
+  }
+  if (reinterpret_cast<uintptr_t>(c->workspace) % 16) return fail(AR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  for (const void* p : {static_cast<const void*>(c->total), static_cast<const void*>(c->each),
+                        static_cast<const void*>(c->known)})
+    if (reinterpret_cast<uintptr_t>(p) % 4) return fail(AR_INVALID_ARGUMENT, "total, each and known must be 4-byte aligned");
+  out->norm = c->norm;
+  out->max_norm = c->max_norm;
+  out->eps = c->eps;
+  out->total = c->total;
+  out->each = c->each;
+  out->known = c->known;
+  out->workspace = c->workspace;
+  out->workspace_bytes = c->workspace_bytes;
+  out->start_event = c->start_event;
+  out->stop_event = c->stop_event;
+  return AR_OK;
+}
+
+// Memory that a call reads, or writes.
+struct Span {
+  uintptr_t lo, hi;
+  bool written;
+};
+
+// Whether a written span meets another. Lists mostly come in ascending order already.
+bool spans_meet(std::vector<Span>& v) {
+  auto by_lo = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  if (!std::is_sorted(v.begin(), v.end(), by_lo)) std::sort(v.begin(), v.end(), by_lo);
+  uintptr_t end = 0, written_end = 0;  // of the spans before
+  for (const Span& s : v) {
+    if (s.lo < (s.written ? end : written_end)) return true;
+    end = std::max(end, s.hi);
+    if (s.written) written_end = std::max(written_end, s.hi);
+  }
+  return false;
+}
+
+ar_status check_grads(const ar_grad* g, int32_t count, bool scale, std::vector<ar::Grad>* out) {
+  if (count < 0 || count > AR_MAX_GRADS)
+    return fail(AR_INVALID_ARGUMENT, "count must be in [0, " + std::to_string(AR_MAX_GRADS) + "]");
+  if (count && !g) return fail(AR_INVALID_ARGUMENT, "grads is NULL");
+  out->reserve(size_t(count));
+  std::vector<Span> spans;
+  if (scale) spans.reserve(2 * size_t(count));
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    const ar_grad& t = g[i];
+    auto bad = [&](const char* why) { return fail(AR_INVALID_ARGUMENT, "tensor " + std::to_string(i) + ": " + why); };
+    if (!is_float(t.dtype)) return bad("dtype must be AR_FP32 or AR_BF16");
+    if (t.n < 0 || t.n >= kMaxElements) return bad("n must be in [0, 2^48)");
+    total += t.n;
+    if (total >= kMaxElements) return bad("2^48 elements or more in one call");
+    if (t.n && !t.data) return bad("data is NULL");
+    const uintptr_t d = reinterpret_cast<uintptr_t>(t.data);
+    if (d % uintptr_t(float_bytes(t.dtype))) return bad("data is not aligned to its elements");
+    ar::Grad r{t.data, const_cast<void*>(t.data), t.n, t.dtype, t.dtype};
+    if (scale) {
+      const bool apart = t.out && t.out != t.data;
+      if (t.out) {
+        if (!is_float(t.out_dtype)) return bad("out_dtype must be AR_FP32 or AR_BF16");
+        if (!apart && t.out_dtype != t.dtype) return bad("clipping in place keeps the type");
+        const uintptr_t o = reinterpret_cast<uintptr_t>(t.out);
+        if (o % uintptr_t(float_bytes(t.out_dtype))) return bad("out is not aligned to its elements");
+        r.out = t.out;
+        r.out_dtype = t.out_dtype;
+        if (apart && t.n) spans.push_back({o, o + uintptr_t(t.n * float_bytes(t.out_dtype)), true});
+      }
+      if (t.n) spans.push_back({d, d + uintptr_t(t.n * float_bytes(t.dtype)), !apart});
+    }
+    out->push_back(r);
+  }
+  if (scale && spans_meet(spans)) return fail(AR_INVALID_ARGUMENT, "a tensor that is written overlaps another");
+  return AR_OK;
+}
+
+ar_status check_buckets(void* const* bufs, bool with_bufs, const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
+                        int32_t op, int32_t collective, ar::Buckets* out) {
+  if (P < 1 || P > AR_MAX_RANKS) return fail(AR_INVALID_ARGUMENT, "P must be in [1, " + std::to_string(AR_MAX_RANKS) + "]");
+  if (buckets < 0 || int64_t(buckets) * P > AR_MAX_GRADS)
+    return fail(AR_INVALID_ARGUMENT, "buckets must be >= 0, and buckets * P at most " + std::to_string(AR_MAX_GRADS));
+  if (!is_float(dtype)) return fail(AR_INVALID_ARGUMENT, "dtype must be AR_FP32 or AR_BF16");
+  if (op != AR_SUM && op != AR_AVG) return fail(AR_INVALID_ARGUMENT, "op must be AR_SUM or AR_AVG");
+  if (collective != AR_ALLREDUCE && collective != AR_REDUCE_SCATTER)
+    return fail(AR_INVALID_ARGUMENT, "collective must be AR_ALLREDUCE or AR_REDUCE_SCATTER");
+  if (buckets && !n) return fail(AR_INVALID_ARGUMENT, "n is NULL");
+  if (buckets && with_bufs && !bufs) return fail(AR_INVALID_ARGUMENT, "bufs is NULL");
+  std::vector<Span> spans;
+  if (with_bufs) spans.reserve(size_t(buckets) * size_t(P));
+  int64_t total = 0;
+  for (int32_t b = 0; b < buckets; ++b) {
+    auto bad = [&](const std::string& why) { return fail(AR_INVALID_ARGUMENT, "bucket " + std::to_string(b) + ": " + why); };
+    if (n[b] < 0 || n[b] >= kMaxElements || (total += n[b]) >= kMaxElements) return bad("n must be >= 0, and below 2^48 in all");
+    for (int32_t p = 0; with_bufs && n[b] && p < P; ++p) {
+      const uintptr_t v = reinterpret_cast<uintptr_t>(bufs[int64_t(b) * P + p]);
+      if (!v) return bad("rank " + std::to_string(p) + "'s buffer is NULL");
+      if (v % uintptr_t(float_bytes(dtype))) return bad("rank " + std::to_string(p) + "'s buffer is not aligned to its elements");
+      spans.push_back({v, v + uintptr_t(n[b] * float_bytes(dtype)), true});
+    }
+  }
+  if (spans_meet(spans)) return fail(AR_INVALID_ARGUMENT, "two buffers overlap");
+  *out = ar::Buckets{bufs, n, buckets, P, dtype, op, collective};
+  return AR_OK;
+}
+
+ar_status finish(const ar::RunResult& r) {
+  t_hip = r.hip_error;
+  if (r.status) return fail(ar_status(r.status), r.message);
+  t_msg.clear();
+  return AR_OK;
+}
+
+// No exception crosses the C boundary: the host tables of a call may not fit memory.
+template <typename F> ar_status guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(AR_INTERNAL, e.what());
+  }
+}
+
+ar_status grad_call(const ar_grad* grads, int32_t count, const ar_clip* clip, bool scale, void* stream, size_t* bytes) {
+  ar::Clip c;
+  std::vector<ar::Grad> g;
+  ar_status st = check_clip(clip, scale, &c);
+  if (st == AR_OK && c.known && !scale) st = fail(AR_INVALID_ARGUMENT, "known is for ar_grad_clip");
+  if (st == AR_OK && c.known && (c.total || c.each)) st = fail(AR_INVALID_ARGUMENT, "with known, total and each must be NULL");
+  if (st == AR_OK && !scale && !bytes && !c.total) st = fail(AR_INVALID_ARGUMENT, "total is NULL");
+  if (st == AR_OK) st = check_grads(grads, count, scale, &g);
+  if (st != AR_OK) return st;
+  if (bytes) {
+    *bytes = ar::grad_workspace(g.data(), int64_t(g.size()), c);
+    return AR_OK;
+  }
+  return finish(ar::run_grad(g.data(), int64_t(g.size()), c, scale, stream));
 }
 
 }  // namespace
@@ -428,6 +575,47 @@ ar_status ar_cost_steps(const ar_schedule* sh, int64_t* sent, int64_t* recv, int
   if (!sh || !sent || !recv || !reduced) return fail(AR_INVALID_ARGUMENT, "NULL argument");
   ar::cost_steps(*reinterpret_cast<const ar::Schedule*>(sh), sent, recv, reduced);
   return AR_OK;
+}
+
+ar_status ar_grad_norm(const ar_grad* grads, int32_t count, const ar_clip* clip, void* stream) {
+  return guarded([&] { return grad_call(grads, count, clip, false, stream, nullptr); });
+}
+
+ar_status ar_grad_clip(const ar_grad* grads, int32_t count, const ar_clip* clip, void* stream) {
+  return guarded([&] { return grad_call(grads, count, clip, true, stream, nullptr); });
+}
+
+ar_status ar_grad_workspace_bytes(const ar_grad* grads, int32_t count, const ar_clip* clip, size_t* bytes) {
+  if (!bytes) return fail(AR_INVALID_ARGUMENT, "bytes is NULL");
+  // out plays no part in the size, known does: read the list as the clip does only if it asks for one
+  return guarded([&] { return grad_call(grads, count, clip, clip && clip->known, nullptr, bytes); });
+}
+
+ar_status ar_allreduce_clip(void* const* bufs, const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
+                            int32_t op, int32_t collective, const ar_clip* clip, void* stream) {
+  return guarded([&] {
+    ar::Clip c;
+    ar::Buckets b;
+    ar_status st = check_clip(clip, true, &c);
+    if (st == AR_OK && c.known) st = fail(AR_INVALID_ARGUMENT, "known is for ar_grad_clip");
+    if (st == AR_OK) st = check_buckets(bufs, true, n, buckets, P, dtype, op, collective, &b);
+    if (st != AR_OK) return st;
+    return finish(ar::run_allreduce_clip(b, c, stream));
+  });
+}
+
+ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
+                                            int32_t op, int32_t collective, const ar_clip* clip, size_t* bytes) {
+  if (!bytes) return fail(AR_INVALID_ARGUMENT, "bytes is NULL");
+  return guarded([&] {
+    ar::Clip c;
+    ar::Buckets b;
+    ar_status st = check_clip(clip, true, &c);
+    if (st == AR_OK) st = check_buckets(nullptr, false, n, buckets, P, dtype, op, collective, &b);
+    if (st != AR_OK) return st;
+    *bytes = ar::allreduce_clip_workspace(b, c);
+    return AR_OK;
+  });
 }
 
 }  // extern "C"

@@ -305,7 +305,7 @@ ar_status ar_kernel_of(const ar_call* call, int32_t* kernel);
  * are kept because enqueued or captured calls may still use them. */
 typedef struct ar_cache_stats {
   int64_t live_plans, retired_plans;
-  int64_t workspaces, retired_workspaces;
+  int64_t workspaces, retired_workspaces;  /* those of the gradient calls among them */
   int64_t plan_device_bytes;       /* tables of live and retired plans */
   int64_t workspace_device_bytes;  /* live and retired workspaces */
 } ar_cache_stats;
@@ -326,6 +326,76 @@ ar_status ar_release_cached(void);
  * enqueued afterwards use the new value. max_blocks outside [1, 2^24 - 1] returns
  * AR_INVALID_ARGUMENT and changes nothing. previous (may be NULL) receives the old value. */
 ar_status ar_set_launch_blocks(int64_t max_blocks, int64_t* previous);
+
+/* ---- gradient norms and clipping ----
+ * What a training step does with the reduced gradients: their global norm N over many tensors,
+ * and a scaling that limits it to max_norm,
+ *   scale = 1                    if N + eps <= max_norm
+ *           max_norm / (N + eps) otherwise
+ *   y     = scale g, rounded once to y's type,
+ * on tensors of fp32 and bf16, which one call may mix. A gradient within the limit keeps its bits.
+ *  - Norms: squares are summed in 64 bits (in an order that the tensors' sizes fix), so no fp32 or
+ *    bf16 value overflows or vanishes, and a call's result is the same on every run. The results
+ *    are fp32. Infinities and NaN count as they are: the norm is then infinite or NaN, and
+ *    scaling by it gives 0 (0 times an infinity: NaN) or NaN. The caller tests the norm.
+ *  - Stream, errors, capture: as for the Allreduce. These calls keep no plan and copy nothing to the
+ *    device: the tensors' pointers and sizes travel as kernel arguments, so grads, bufs and n may
+ *    change once the call returned, and a captured call replays on what it was given.
+ *  - Workspace: device scratch of ar_grad_workspace_bytes() or ar_allreduce_clip_workspace_bytes()
+ *    bytes, 16-byte aligned; its contents need no preparation. NULL: the library's own, one per
+ *    (device, stream), kept like the literal workspaces; under stream capture such a call returns
+ *    AR_UNSUPPORTED, since a graph replays beside whatever else uses the stream's workspace.
+ *  - Memory: any address that is a multiple of the element size. Tensors that a call writes must
+ *    not overlap any other tensor of the call (AR_INVALID_ARGUMENT), nor total, each, known or the
+ *    workspace (not checked). */
+typedef enum { AR_NORM_L2 = 0, AR_NORM_MAX = 1 } ar_norm; /* 2-norm; largest magnitude */
+
+/* One gradient tensor of n contiguous elements. */
+typedef struct ar_grad {
+  const void* data;  /* may be NULL if n is 0 */
+  void* out;         /* ar_grad_clip: receives the n scaled elements; NULL (or data, with out_dtype
+                        equal to dtype): in place. ar_grad_norm ignores it */
+  int64_t n;         /* 0 <= n < 2^48 */
+  int32_t dtype;     /* AR_FP32 or AR_BF16 */
+  int32_t out_dtype; /* of out, if it is not NULL: AR_FP32 or AR_BF16 */
+} ar_grad;
+
+#define AR_MAX_GRADS 65536 /* tensors of one call; buckets of one call times its ranks */
+
+typedef struct ar_clip {
+  int32_t norm;       /* ar_norm */
+  float max_norm;     /* >= 0, or infinite: scale by 1 (ar_grad_norm ignores it and eps) */
+  float eps;          /* >= 0, finite; 1e-6 is customary */
+  float* total;       /* device: receives N. May be NULL unless the call only computes it */
+  float* each;        /* device, one per tensor (ar_allreduce_clip: per bucket), or NULL: receives
+                         the tensors' own norms */
+  const float* known; /* device, or NULL. ar_grad_clip: N, computed before (for a gradient whose
+                         tensors lie in several calls); the call only scales, and total and each must
+                         be NULL. The other calls take none */
+  void* workspace;
+  size_t workspace_bytes;
+  void* start_event;  /* as in ar_call */
+  void* stop_event;
+} ar_clip;
+
+/* The norm of `count` tensors (0 <= count <= AR_MAX_GRADS; 0 of none). */
+ar_status ar_grad_norm(const ar_grad* grads, int32_t count, const ar_clip* clip, void* stream);
+/* The same, and every tensor scaled to limit it. */
+ar_status ar_grad_clip(const ar_grad* grads, int32_t count, const ar_clip* clip, void* stream);
+ar_status ar_grad_workspace_bytes(const ar_grad* grads, int32_t count, const ar_clip* clip, size_t* bytes);
+
+/* The Allreduce of `buckets` gradient buckets over P ranks with the clipping of the result: the ranks
+ * are combined as an AR_DIRECT Allreduce combines them (rank order, fp32; op AR_SUM or AR_AVG), N is
+ * the norm over all buckets of the combined values before they are rounded to dtype, and every rank
+ * ends with the scaled values, rounded once. A gradient within the limit ends with the bits of
+ * ar_allreduce(..., AR_DIRECT). collective AR_REDUCE_SCATTER: rank q ends with its part of that, in
+ * place (ar_collective); its other elements are untouched.
+ * bufs: host array of buckets * P device pointers, bucket b's rank p at bufs[b * P + p], each to n[b]
+ * elements (n[b] >= 0). dtype: AR_FP32 or AR_BF16. buckets * P <= AR_MAX_GRADS. */
+ar_status ar_allreduce_clip(void* const* bufs, const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
+                            int32_t op, int32_t collective, const ar_clip* clip, void* stream);
+ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
+                                            int32_t op, int32_t collective, const ar_clip* clip, size_t* bytes);
 
 /* ---- schedules on the host (no GPU needed) ---- */
 typedef struct ar_schedule ar_schedule;
