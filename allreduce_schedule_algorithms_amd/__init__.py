@@ -64,59 +64,78 @@ def all_gather(tensors, algo="ring", exec="fused", batch=1, stream=None, workspa
 
 
 # ---- gradient norms and clipping ----
-def _float_types():
+# A call on a few small tensors takes the GPU about 5 us, so what Python does per tensor counts: the
+# tensors' properties are read by maps over the unbound methods, and the common place of a call (the
+# current device and stream) is found without building torch's objects for it.
+_TYPES = None  # torch dtype -> ar_dtype
+
+
+def _torch():
+    global _TYPES
     import torch
-    return {torch.float32: 1, torch.bfloat16: 2}  # Dtype.AR_FP32, Dtype.AR_BF16
+    if _TYPES is None:
+        _TYPES = {torch.float32: int(Dtype.AR_FP32), torch.bfloat16: int(Dtype.AR_BF16)}
+    return torch
 
 
 def _invalid(message):
     return ArError(Status.AR_INVALID_ARGUMENT, message)
 
 
+def _check_tensors(torch, tensors, what):
+    """(device index, ar_dtype of every tensor) of contiguous CUDA tensors on one device."""
+    T = torch.Tensor
+    devices = set(map(T.get_device, tensors))
+    types = [_TYPES.get(t.dtype) for t in tensors]
+    if len(devices) != 1 or -1 in devices or None in types or not all(map(T.is_contiguous, tensors)):
+        raise _invalid(f"{what} must be contiguous float32 or bfloat16 tensors on one CUDA device")
+    return devices.pop(), types
+
+
 def _grads(tensors, out=None):
-    """(GradList, device) of contiguous CUDA tensors on one device."""
-    types = _float_types()
+    """(GradList, device index) of gradients, and of where they go."""
+    torch = _torch()
     tensors = list(tensors)
-    if not tensors:
+    count = len(tensors)
+    if not count:
         return GradList((), 0), None
-    device = tensors[0].device
-    words = []
-    for i, t in enumerate(tensors):
-        d = types.get(t.dtype)
-        if d is None or not t.is_cuda or t.device != device or not t.is_contiguous():
-            raise _invalid(f"gradient {i} must be a contiguous float32 or bfloat16 tensor on {device}, a CUDA device")
-        words += (t.data_ptr(), 0, t.numel(), d)
+    T = torch.Tensor
+    index, types = _check_tensors(torch, tensors, "gradients")
+    words = [0] * (4 * count)
+    words[0::4] = map(T.data_ptr, tensors)
+    words[2::4] = sizes = list(map(T.numel, tensors))
     if out is not None:
         out = list(out)
-        if len(out) != len(tensors):
-            raise _invalid(f"{len(tensors)} gradients, and {len(out)} outputs")
-        for i, (t, o) in enumerate(zip(tensors, out)):
-            d = types.get(o.dtype)
-            if d is None or o.device != device or not o.is_contiguous() or o.numel() != t.numel():
-                raise _invalid(f"output {i} must be a contiguous float32 or bfloat16 tensor of its gradient's size on {device}")
-            words[4 * i + 1] = o.data_ptr()
-            words[4 * i + 3] |= d << 32
-    return GradList(words, len(tensors)), device
+        if len(out) != count:
+            raise _invalid(f"{count} gradients, and {len(out)} outputs")
+        there, kinds = _check_tensors(torch, out, "outputs")
+        if there != index or list(map(T.numel, out)) != sizes:
+            raise _invalid("every output must be of its gradient's size, on its device")
+        words[1::4] = map(T.data_ptr, out)
+        types = [d | k << 32 for d, k in zip(types, kinds)]
+    words[3::4] = types
+    return GradList(words, count), index
 
 
 class _Place:
-    """The device and stream of a call, with what it allocates there."""
+    """The device and stream of a call, and what it allocates there."""
 
-    def __init__(self, device, stream):
-        import torch
-        self.torch = torch
+    def __init__(self, index, stream):
+        self.torch = torch = _torch()
+        torch.cuda.init()
         current = torch.cuda.current_device()
-        index = current if device is None or device.index is None else device.index
-        self.device = torch.device("cuda", index)
-        self.guards = [] if index == current else [torch.cuda.device(index)]
-        here = torch.cuda.current_stream(self.device)
+        self.index = index = current if index is None else index
+        self.guards = () if index == current else (torch.cuda.device(index),)
+        self.stream = torch._C._cuda_getCurrentRawStream(index)
+        if stream is None:
+            return
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device) if stream else torch.cuda.default_stream(self.device)
-        self.stream = here if stream is None else stream
-        if self.stream.device != self.device:
-            raise _invalid(f"the stream is on {self.stream.device}, the gradients on {self.device}")
-        if self.stream != here:  # the caller's results and the scratch belong to the stream that writes them
-            self.guards.append(torch.cuda.stream(self.stream))
+            stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
+        if stream.device.index != index:
+            raise _invalid(f"the stream is on {stream.device}, the gradients on cuda:{index}")
+        if stream.cuda_stream != self.stream:  # results and scratch belong to the stream that writes them
+            self.guards += (torch.cuda.stream(stream),)
+            self.stream = stream.cuda_stream
 
     def __enter__(self):
         for g in self.guards:
@@ -128,13 +147,15 @@ class _Place:
             g.__exit__(*err)
 
     def floats(self, *shape):
-        return self.torch.empty(shape, dtype=self.torch.float32, device=self.device)
+        return self.torch.empty(shape, dtype=self.torch.float32, device="cuda")
 
-    def scratch(self, clip, workspace, bytes_of):
+    def scratch(self, clip, workspace, need):
         """Point clip at the caller's workspace, or at one of torch's (in a captured call: of the graph's own memory)."""
         if workspace is None:
-            workspace = self.torch.empty(bytes_of(clip), dtype=self.torch.uint8, device=self.device)
-        elif workspace.device != self.device or not workspace.is_contiguous():
+            if not need:
+                return None
+            workspace = self.torch.empty(need, dtype=self.torch.uint8, device="cuda")
+        elif workspace.get_device() != self.index or not workspace.is_contiguous():
             raise _invalid("workspace must be a contiguous tensor on the gradients' device")
         clip.workspace, clip.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         return workspace
@@ -144,15 +165,16 @@ def grad_norm(grads, norm="l2", per_tensor=False, stream=None, workspace=None):
     """Global norm of a list of contiguous float32 / bfloat16 CUDA tensors, as a 0-dim float32 tensor.
 
     norm: "l2" or "max" (largest magnitude). per_tensor: return (norm, norms), norms holding
-    every tensor's own. ``stream`` defaults to torch's current stream, ``workspace`` (a tensor of
-    ar_grad_workspace_bytes) to scratch from torch's allocator.
+    every tensor's own. ``stream`` defaults to torch's current stream (results are ready on the
+    stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to scratch from torch's
+    allocator.
     """
-    table, device = _grads(grads)
-    with _Place(device, stream) as at:
+    table, index = _grads(grads)
+    with _Place(index, stream) as at:
         total = at.floats()
         each = at.floats(table.count) if per_tensor else None
         clip = make_clip(norm, total=total, each=each)
-        workspace = at.scratch(clip, workspace, lambda c: ar_grad_workspace_bytes(table, c))
+        workspace = at.scratch(clip, workspace, 0 if workspace is not None else ar_grad_workspace_bytes(table, clip))
         ar_grad_norm(table, clip, at.stream)
     return (total, each) if per_tensor else total
 
@@ -164,16 +186,16 @@ def grad_clip(grads, max_norm, norm="l2", eps=1e-6, out=None, total_norm=None, s
     float32 or bfloat16). total_norm: a float32 CUDA tensor of one element that holds the norm
     already (of a gradient spread over several calls or ranks); the call then only scales.
     """
-    table, device = _grads(grads, out)
-    with _Place(device, stream) as at:
+    table, index = _grads(grads, out)
+    with _Place(index, stream) as at:
         if total_norm is not None:
-            if total_norm.dtype != at.torch.float32 or total_norm.numel() != 1 or total_norm.device != at.device:
+            if total_norm.dtype != at.torch.float32 or total_norm.numel() != 1 or total_norm.get_device() != at.index:
                 raise _invalid("total_norm must be a float32 tensor of one element on the gradients' device")
             ar_grad_clip(table, make_clip(norm, max_norm, eps, known=total_norm), at.stream)
             return total_norm
         total = at.floats()
         clip = make_clip(norm, max_norm, eps, total=total)
-        workspace = at.scratch(clip, workspace, lambda c: ar_grad_workspace_bytes(table, c))
+        workspace = at.scratch(clip, workspace, 0 if workspace is not None else ar_grad_workspace_bytes(table, clip))
         ar_grad_clip(table, clip, at.stream)
     return total
 
@@ -187,30 +209,26 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
     0-dim float32 tensor) is over all buckets, of the combined values before they are rounded;
     the scaled values are rounded once. collective "reduce_scatter": rank q ends with its part.
     """
-    import torch
+    torch = _torch()
+    T = torch.Tensor
     buckets = list(buckets)
-    if buckets and isinstance(buckets[0], torch.Tensor):
+    if buckets and isinstance(buckets[0], T):
         buckets = [buckets]
-    if not buckets or not len(buckets[0]):
-        raise _invalid("allreduce_clip needs a bucket with a rank's tensor")
-    P, first = len(buckets[0]), buckets[0][0]
-    dtype = {torch.float32: Dtype.AR_FP32, torch.bfloat16: Dtype.AR_BF16}.get(first.dtype)
-    if dtype is None:
-        raise _invalid(f"unsupported tensor dtype {first.dtype}")
-    ptrs, sizes = [], []
-    for b in buckets:
-        if len(b) != P:
-            raise _invalid("every bucket needs a tensor of every rank")
-        n = b[0].numel()
-        for t in b:
-            if t.dtype != first.dtype or t.numel() != n or not t.is_cuda or t.device != first.device or not t.is_contiguous():
-                raise _invalid("a bucket's tensors must be contiguous CUDA tensors of one dtype, size and device")
-            ptrs.append(t.data_ptr())
-        sizes.append(n)
-    with _Place(first.device, stream) as at:
+    P = len(buckets[0]) if buckets else 0
+    if not P or any(len(b) != P for b in buckets):
+        raise _invalid("allreduce_clip needs buckets with a tensor of every rank")
+    tensors = [t for b in buckets for t in b]
+    index, types = _check_tensors(torch, tensors, "the ranks' tensors")
+    numels = list(map(T.numel, tensors))
+    sizes = numels[::P]
+    if numels != [n for n in sizes for _ in range(P)] or len(set(types)) != 1:
+        raise _invalid("a bucket's tensors must be of one size, and all tensors of one dtype")
+    dtype = types[0]
+    with _Place(index, stream) as at:
         total = at.floats()
         clip = make_clip(norm, max_norm, eps, total=total)
-        workspace = at.scratch(clip, workspace,
-                               lambda c: ar_allreduce_clip_workspace_bytes(sizes, P, dtype, op, collective, c))
-        ar_allreduce_clip(ptrs, sizes, P, dtype, op, collective, clip, at.stream)
+        if workspace is None:
+            need = ar_allreduce_clip_workspace_bytes(sizes, P, dtype, op, collective, clip)
+        workspace = at.scratch(clip, workspace, 0 if workspace is not None else need)
+        ar_allreduce_clip(marshal_ptrs(list(map(T.data_ptr, tensors))), sizes, P, dtype, op, collective, clip, at.stream)
     return total

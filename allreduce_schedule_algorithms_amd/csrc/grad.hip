@@ -114,11 +114,15 @@ template <int KIND> struct Part {
   }
 };
 
+template <int KIND> __device__ __forceinline__ void join_wave(Part<KIND>& p) {  // valid in lane 0
+#pragma unroll
+  for (int d = 32; d; d >>= 1) p.join(__shfl_down(p.v, d));
+}
+
 // The workgroup's partial, valid in thread 0: within a wave by shuffles, then over the waves in order.
 template <int KIND, int THREADS> __device__ __forceinline__ void join_group(Part<KIND>& p) {
   __shared__ double wave[THREADS / 64];
-#pragma unroll
-  for (int d = 32; d; d >>= 1) p.join(__shfl_down(p.v, d));
+  join_wave(p);
   __syncthreads();  // the array's last readers
   if (threadIdx.x % 64 == 0) wave[threadIdx.x / 64] = p.v;
   __syncthreads();
@@ -190,25 +194,26 @@ template <typename TAB> __device__ __forceinline__ int find_first(const TAB& tab
 }
 
 constexpr int kUnroll = 4;  // vectors of a thread in flight
-template <int KIND, int DT, bool NT> __device__ __forceinline__ void norm_item(const void* src, int64_t e0, int cnt, Part<KIND>& p) {
+// L lanes (a workgroup's, or a wave's), of which this is `lane`, go over an item together.
+template <int KIND, int DT, int L, bool NT> __device__ __forceinline__ void norm_item(const void* src, int64_t e0, int cnt, int lane, Part<KIND>& p) {
   constexpr int V = DT == D_BF16 ? 8 : 4;
   const int nv = cnt / V;
-  int v = threadIdx.x;
-  for (; v + (kUnroll - 1) * kThreads < nv; v += kUnroll * kThreads) {
+  int v = lane;
+  for (; v + (kUnroll - 1) * L < nv; v += kUnroll * L) {
     typename Raw<DT, V>::T r[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) r[j] = ld_raw<DT, V, NT>(src, e0 + int64_t(v + j * kThreads) * V);
+    for (int j = 0; j < kUnroll; ++j) r[j] = ld_raw<DT, V, NT>(src, e0 + int64_t(v + j * L) * V);
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) p.add(value<DT, V>(r[j], i));
   }
-  for (; v < nv; v += kThreads) {
+  for (; v < nv; v += L) {
     const typename Raw<DT, V>::T r = ld_raw<DT, V, NT>(src, e0 + int64_t(v) * V);
 #pragma unroll
     for (int i = 0; i < V; ++i) p.add(value<DT, V>(r, i));
   }
-  const int t = nv * V + threadIdx.x;
+  const int t = nv * V + lane;
   if (t < cnt) p.add(ld_one<DT>(src, e0 + t));
 }
 
@@ -233,8 +238,8 @@ template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) v
   Part<KIND> p;
   for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
     const GradItem w = grad_item(tab, it);
-    if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, NT>(tab.src[w.i], w.e0, w.cnt, p);
-    else norm_item<KIND, D_FP32, NT>(tab.src[w.i], w.e0, w.cnt, p);
+    if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
+    else norm_item<KIND, D_FP32, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     if constexpr (EACH) {
       join_group<KIND, kThreads>(p);
       if (threadIdx.x == 0) partial[tab.at + it] = p.v;
@@ -270,32 +275,43 @@ template <int KIND> __global__ __launch_bounds__(64) void k_norm_each(EachTab ta
   if (threadIdx.x == 0) each[i] = float(p.norm());
 }
 
-template <int DS, int DD> __device__ __forceinline__ void scale_item(const void* src, void* dst, int64_t e0, int cnt, Factor f) {
+template <int DS, int DD, int L> __device__ __forceinline__ void scale_item(const void* src, void* dst, int64_t e0, int cnt, int lane, Factor f) {
   // between the types, 4 elements a thread: its stores (or loads) then join its neighbours' to whole lines
   constexpr int V = DS == D_BF16 && DD == D_BF16 ? 8 : 4;
   const int nv = cnt / V;
-  int v = threadIdx.x;
-  for (; v + (kUnroll - 1) * kThreads < nv; v += kUnroll * kThreads) {
+  int v = lane;
+  for (; v + (kUnroll - 1) * L < nv; v += kUnroll * L) {
     typename Raw<DS, V>::T r[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) r[j] = ld_raw<DS, V, true>(src, e0 + int64_t(v + j * kThreads) * V);
+    for (int j = 0; j < kUnroll; ++j) r[j] = ld_raw<DS, V, true>(src, e0 + int64_t(v + j * L) * V);
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) {
       float x[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = f(value<DS, V>(r[j], i));
-      st_raw<DD, V, true>(dst, e0 + int64_t(v + j * kThreads) * V, pack<DD, V>(x));
+      st_raw<DD, V, true>(dst, e0 + int64_t(v + j * L) * V, pack<DD, V>(x));
     }
   }
-  for (; v < nv; v += kThreads) {
+  for (; v < nv; v += L) {
     const typename Raw<DS, V>::T r = ld_raw<DS, V, true>(src, e0 + int64_t(v) * V);
     float x[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) x[i] = f(value<DS, V>(r, i));
     st_raw<DD, V, true>(dst, e0 + int64_t(v) * V, pack<DD, V>(x));
   }
-  const int t = nv * V + threadIdx.x;
+  const int t = nv * V + lane;
   if (t < cnt) st_one<DD>(dst, e0 + t, f(ld_one<DS>(src, e0 + t)));
+}
+
+template <int L> __device__ __forceinline__ void scale_any(const GradTab& tab, const GradItem& w, int lane, Factor f) {
+  const void* s = tab.src[w.i];
+  void* d = tab.dst[w.i];
+  switch (int(tab.n4[w.i] & 3)) {
+    case 0: scale_item<D_FP32, D_FP32, L>(s, d, w.e0, w.cnt, lane, f); break;
+    case 1: scale_item<D_BF16, D_FP32, L>(s, d, w.e0, w.cnt, lane, f); break;
+    case 2: scale_item<D_FP32, D_BF16, L>(s, d, w.e0, w.cnt, lane, f); break;
+    default: scale_item<D_BF16, D_BF16, L>(s, d, w.e0, w.cnt, lane, f); break;
+  }
 }
 
 // What the passes that scale start from.
@@ -322,16 +338,44 @@ __device__ __forceinline__ int last_item(int items) { return items - 1 - int((it
 
 template <int KIND> __global__ __launch_bounds__(kThreads) void k_grad_scale(GradTab tab, Limit lim) {
   const Factor f = factor_for<KIND>(lim);
-  for (int k = last_item(tab.first[tab.count]); k >= 0; k -= int(gridDim.x)) {
-    const GradItem w = grad_item(tab, k);
-    const void* s = tab.src[w.i];
-    void* d = tab.dst[w.i];
-    switch (int(tab.n4[w.i] & 3)) {
-      case 0: scale_item<D_FP32, D_FP32>(s, d, w.e0, w.cnt, f); break;
-      case 1: scale_item<D_BF16, D_FP32>(s, d, w.e0, w.cnt, f); break;
-      case 2: scale_item<D_FP32, D_BF16>(s, d, w.e0, w.cnt, f); break;
-      default: scale_item<D_BF16, D_BF16>(s, d, w.e0, w.cnt, f); break;
+  for (int k = last_item(tab.first[tab.count]); k >= 0; k -= int(gridDim.x)) scale_any<kThreads>(tab, grad_item(tab, k), threadIdx.x, f);
+}
+
+// A short list in one launch: one workgroup, whose waves take an item each. Its second look at the
+// elements finds them in the L2.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64, kSmallItems = 48;
+template <int KIND, bool SCALE>
+__global__ __launch_bounds__(kSmallThreads) void k_grad_small(GradTab tab, float* total, float* each, float max_norm, float eps) {
+  __shared__ double own[kSmallItems];
+  __shared__ double all;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64, items = tab.first[tab.count];
+  Part<KIND> p;
+  for (int it = wave; it < items; it += kSmallWaves) {
+    const GradItem w = grad_item(tab, it);
+    Part<KIND> q;
+    if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, 64, false>(tab.src[w.i], w.e0, w.cnt, lane, q);
+    else norm_item<KIND, D_FP32, 64, false>(tab.src[w.i], w.e0, w.cnt, lane, q);
+    p.join(q.v);
+    if (each) {
+      join_wave(q);
+      if (lane == 0) own[it] = q.v;
     }
+  }
+  join_group<KIND, kSmallThreads>(p);
+  if (threadIdx.x == 0) {
+    all = p.norm();
+    if (total) *total = float(all);
+  }
+  __syncthreads();
+  if (each)
+    for (int i = threadIdx.x; i < tab.count; i += kSmallThreads) {
+      Part<KIND> q;
+      for (int k = tab.first[i]; k < tab.first[i + 1]; ++k) q.join(own[k]);
+      each[i] = float(q.norm());
+    }
+  if constexpr (SCALE) {
+    const Factor f = factor_of(all, max_norm, eps);
+    for (int it = wave; it < items; it += kSmallWaves) scale_any<64>(tab, grad_item(tab, it), lane, f);
   }
 }
 
@@ -424,9 +468,20 @@ __device__ __forceinline__ void sum_ranks(void* const* ptr, int P, float div, in
   }
 }
 
+// One element's sum, with the loads of up to 32 ranks in flight: what lies behind the last whole vector has
+// as many ranks to wait for as the rest.
 template <int DT> __device__ __forceinline__ float sum_one(void* const* ptr, int P, float div, int64_t e) {
-  float acc = ld_one<DT>(ptr[0], e);
-  for (int q = 1; q < P; ++q) acc = acc + ld_one<DT>(ptr[q], e);
+  constexpr int B = 32;
+  float acc = 0;
+  for (int base = 0; base < P; base += B) {
+    float x[B];
+#pragma unroll
+    for (int r = 0; r < B; ++r)
+      if (base + r < P) x[r] = ld_one<DT>(ptr[base + r], e);
+#pragma unroll
+    for (int r = 0; r < B; ++r)
+      if (base + r < P) acc = base + r ? acc + x[r] : x[r];
+  }
   return div > 0 ? acc / div : acc;
 }
 
@@ -548,6 +603,46 @@ template <int DT, int KIND> __global__ __launch_bounds__(kThreads) void k_bucket
       for (int q = q0; q < q1; ++q) st_one<DT>(ptr[q], w.e0 + t, s);
     }
   }
+}
+
+// Few elements in one launch: one workgroup, whose waves take an item of 64 elements each and keep their sums
+// in registers between the passes (24 x 106 fp32: 5.9 us against 12.6 for two launches, 8 x 1024: 5.9 and
+// 6.7; of two items to a wave, 8 x 2048, 8.3 and 6.9).
+constexpr int kSmallSpan = 64;
+template <int DT, int KIND>
+__global__ __launch_bounds__(kSmallThreads) void k_bucket_small(BucketTab tab, float* total, float* each, float max_norm, float eps) {
+  __shared__ double own[kSmallWaves];
+  __shared__ double all;
+  const int it = __builtin_amdgcn_readfirstlane(threadIdx.x / 64), lane = threadIdx.x % 64;
+  Part<KIND> p;
+  BucketItem w{0, 0, 0, 0};
+  float sum = 0;
+  if (it < tab.first[tab.count]) w = bucket_item(tab, it);
+  void* const* ptr = tab.p + w.b * tab.P;
+  if (lane < w.cnt) {
+    sum = sum_one<DT>(ptr, tab.P, tab.div, w.e0 + lane);
+    p.add(sum);
+  }
+  if (each) {
+    Part<KIND> q = p;
+    join_wave(q);
+    if (lane == 0) own[it] = q.v;
+  }
+  join_group<KIND, kSmallThreads>(p);
+  if (threadIdx.x == 0) {
+    all = p.norm();
+    if (total) *total = float(all);
+  }
+  __syncthreads();
+  if (each && threadIdx.x < tab.count) {
+    Part<KIND> q;
+    for (int k = tab.first[threadIdx.x]; k < tab.first[threadIdx.x + 1]; ++k) q.join(own[k]);
+    each[threadIdx.x] = float(q.norm());
+  }
+  const float y = factor_of(all, max_norm, eps)(sum);
+  const int q0 = tab.owners ? w.owner : 0, q1 = tab.owners ? w.owner + 1 : tab.P;
+  if (lane < w.cnt)
+    for (int q = q0; q < q1; ++q) st_one<DT>(ptr[q], w.e0 + lane, y);
 }
 
 // ----------------------------------------------------------------------------
@@ -692,6 +787,11 @@ int64_t total_of(const Grad* g, int64_t count) {
   return t;
 }
 
+// Whether one workgroup takes the whole list: one launch and no workspace, about 2 us of the host's time,
+// against two launches, whose many waves soon make up for the second. Norm, fp32: 24 items 4.7 us on the
+// GPU (two launches 5.5), 48 items 6.4 (5.5); with the scaling 12 items 6.3 (6.5), 24 items 8.5 (6.6).
+bool small_list(int64_t count, int64_t items, bool scale) { return count <= kTabTensors && items <= (scale ? kSmallWaves : kSmallItems); }
+
 }  // namespace
 
 size_t grad_workspace(const Grad* g, int64_t count, const Clip& clip) {
@@ -699,6 +799,7 @@ size_t grad_workspace(const Grad* g, int64_t count, const Clip& clip) {
   const int64_t per = item_size(total_of(g, count), clip.each);
   int64_t items = 0;
   for (int64_t i = 0; i < count; ++i) items += pieces(g[i].n, per);
+  if (small_list(count, items, true)) return 0;  // enough for either call
   return kHead + partial_bytes(items, pieces(count, kTabTensors), clip.each);
 }
 
@@ -721,9 +822,20 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
       tab.first[k + 1] = tab.first[k] + int32_t(pieces(t.n, per));
       firsts.push_back(tab.at + tab.first[k + 1]);
     }
-    if (tab.first[tab.count]) tabs.push_back(tab);
+    if (tab.first[tab.count] || count <= kTabTensors) tabs.push_back(tab);
   }
   const int32_t items = firsts.back();
+  Sequence s{st, {reinterpret_cast<hipEvent_t>(clip.start_event), reinterpret_cast<hipEvent_t>(clip.stop_event)}, 0};
+  if (!clip.known && small_list(count, items, scale)) {
+    GradTab none;
+    none.count = 0;
+    none.first[0] = 0;
+    const GradTab& t = tabs.empty() ? none : tabs[0];
+    s.left = 1;
+    if (scale) { AR_KIND(clip.norm, s.launch(k_grad_small<KIND, true>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
+    else { AR_KIND(clip.norm, s.launch(k_grad_small<KIND, false>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
+    return s.done();
+  }
   std::vector<int64_t> blocks;
   int32_t partials = clip.each ? items : 0;
   for (GradTab& t : tabs) {
@@ -740,7 +852,6 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
   }
   double* joined = reinterpret_cast<double*>(ws);
   double* partial = reinterpret_cast<double*>(ws + kHead);
-  Sequence s{st, {reinterpret_cast<hipEvent_t>(clip.start_event), reinterpret_cast<hipEvent_t>(clip.stop_event)}, 0};
   const int64_t nt = int64_t(tabs.size());
   const bool final = !clip.known && (!scale || clip.each || !nt);  // otherwise the scaling pass joins the partials
   s.left = (clip.known ? 0 : nt) + (scale ? nt : 0) + (final ? 1 : 0) + (clip.each ? pieces(count, kEachTensors) : 0);
@@ -788,11 +899,9 @@ struct BucketPlan {
 
 bool low_in_workspace(const Buckets& b) { return b.dtype == D_BF16 && b.coll == C_REDUCE_SCATTER && b.P > 1; }
 
-BucketPlan plan_buckets(const Buckets& b, bool each) {
+BucketPlan plan_buckets(const Buckets& b, int64_t per) {
   BucketPlan pl;
-  int64_t total = 0;
-  for (int64_t i = 0; i < b.count; ++i) total += b.n[i];
-  const int64_t per = item_size(total, each), fit = std::min<int64_t>(kTabBuckets, kTabPtrs / b.P);
+  const int64_t fit = std::min<int64_t>(kTabBuckets, kTabPtrs / b.P);
   const bool scatter = b.coll == C_REDUCE_SCATTER;
   for (int64_t i0 = 0; i0 < b.count; i0 += fit) {
     BucketTab tab;
@@ -818,10 +927,22 @@ BucketPlan plan_buckets(const Buckets& b, bool each) {
       tab.first[k + 1] = tab.first[k] + (n ? tab.ipp[k] * (scatter ? b.P : 1) : 0);
       pl.firsts.push_back(tab.at + tab.first[k + 1]);
     }
-    if (tab.first[tab.count]) pl.tabs.push_back(tab);
+    if (tab.first[tab.count] || b.count <= fit) pl.tabs.push_back(tab);
   }
   pl.launches = int64_t(pl.tabs.size());
   return pl;
+}
+
+// The call's plan; small: one workgroup takes all of it.
+BucketPlan plan_call(const Buckets& b, bool each, bool* small) {
+  const bool scatter = b.coll == C_REDUCE_SCATTER;
+  int64_t total = 0, items = 0;
+  for (int64_t i = 0; i < b.count; ++i) {
+    total += b.n[i];
+    if (b.n[i]) items += scatter ? b.P * pieces(pieces(b.n[i], b.P), kSmallSpan) : pieces(b.n[i], kSmallSpan);
+  }
+  *small = b.count <= std::min<int64_t>(kTabBuckets, kTabPtrs / b.P) && items <= kSmallWaves;
+  return plan_buckets(b, *small ? kSmallSpan : item_size(total, each));
 }
 
 // Where the lower halves start, behind the partials.
@@ -830,14 +951,26 @@ size_t low_offset(const BucketPlan& pl, bool each) { return kHead + partial_byte
 }  // namespace
 
 size_t allreduce_clip_workspace(const Buckets& b, const Clip& clip) {
-  const BucketPlan pl = plan_buckets(b, clip.each);
-  return low_offset(pl, clip.each) + pl.low_bytes;
+  bool small;
+  const BucketPlan pl = plan_call(b, clip.each, &small);
+  return small ? 0 : low_offset(pl, clip.each) + pl.low_bytes;
 }
 
 RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  BucketPlan pl = plan_buckets(b, clip.each);
+  bool small;
+  BucketPlan pl = plan_call(b, clip.each, &small);
   const int32_t items = pl.firsts.back();
+  Sequence s{st, {reinterpret_cast<hipEvent_t>(clip.start_event), reinterpret_cast<hipEvent_t>(clip.stop_event)}, 0};
+  if (small) {
+    BucketTab none;
+    std::memset(&none, 0, sizeof(none));
+    const BucketTab& t = pl.tabs.empty() ? none : pl.tabs[0];
+    s.left = 1;
+    if (b.dtype == D_BF16) { AR_KIND(clip.norm, s.launch(k_bucket_small<D_BF16, KIND>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
+    else { AR_KIND(clip.norm, s.launch(k_bucket_small<D_FP32, KIND>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
+    return s.done();
+  }
   std::unique_lock<std::mutex> lk;
   char* ws = nullptr;
   const RunResult r = workspace_of(clip, low_offset(pl, clip.each) + pl.low_bytes, st, lk, &ws);
@@ -855,7 +988,6 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
     t.at = partials;
     partials += int32_t(blocks.back());
   }
-  Sequence s{st, {reinterpret_cast<hipEvent_t>(clip.start_event), reinterpret_cast<hipEvent_t>(clip.stop_event)}, 0};
   const int64_t nt = int64_t(pl.tabs.size());
   const bool final = clip.each || !nt;  // otherwise the second pass joins the partials
   s.left = 2 * nt + (final ? 1 : 0) + (clip.each ? pieces(b.count, kEachTensors) : 0);

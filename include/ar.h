@@ -342,9 +342,10 @@ ar_status ar_set_launch_blocks(int64_t max_blocks, int64_t* previous);
  *    device: the tensors' pointers and sizes travel as kernel arguments, so grads, bufs and n may
  *    change once the call returned, and a captured call replays on what it was given.
  *  - Workspace: device scratch of ar_grad_workspace_bytes() or ar_allreduce_clip_workspace_bytes()
- *    bytes, 16-byte aligned; its contents need no preparation. NULL: the library's own, one per
- *    (device, stream), kept like the literal workspaces; under stream capture such a call returns
- *    AR_UNSUPPORTED, since a graph replays beside whatever else uses the stream's workspace.
+ *    bytes (0 for small calls), 16-byte aligned; its contents need no preparation. NULL: the library's
+ *    own, one per (device, stream), kept like the literal workspaces; under stream capture a call that
+ *    needs one then returns AR_UNSUPPORTED, since a graph replays beside whatever else uses the
+ *    stream's workspace.
  *  - Memory: any address that is a multiple of the element size. Tensors that a call writes must
  *    not overlap any other tensor of the call (AR_INVALID_ARGUMENT), nor total, each, known or the
  *    workspace (not checked). */

@@ -451,16 +451,17 @@ def test_graphs():
 
 def test_capture_needs_a_workspace():
     A, torch = lib(), torch_mod()
-    t = torch.ones(100, device="cuda")
+    n = 1_000_000
+    t = torch.ones(n, device="cuda")
     total = torch.zeros((), device="cuda")
-    table = A.marshal_grads([(t.data_ptr(), 0, 100, "fp32", "fp32")])
+    table = A.marshal_grads([(t.data_ptr(), 0, n, "fp32", "fp32")])
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         total.add_(1)
         s = torch.cuda.current_stream()
         for call in (lambda: A.ar_grad_norm(table, A.make_clip(total=total), s),
                      lambda: A.ar_grad_clip(table, A.make_clip(max_norm=1.0), s),
-                     lambda: A.ar_allreduce_clip([t], [100], 1, "fp32", "sum", "allreduce", A.make_clip(max_norm=1.0), s)):
+                     lambda: A.ar_allreduce_clip([t], [n], 1, "fp32", "sum", "allreduce", A.make_clip(max_norm=1.0), s)):
             with pytest.raises(A.ArError) as e:
                 call()
             assert e.value.status == A.Status.AR_UNSUPPORTED

@@ -120,17 +120,23 @@ def test_allreduce_clip_buffers():
 
 
 def test_workspace_bytes():
-    one = A.ar_grad_workspace_bytes(grads(GOOD), clip())
+    # one workgroup takes a few small tensors and needs none
+    assert A.ar_grad_workspace_bytes(grads(GOOD), clip()) == 0
+    one = A.ar_grad_workspace_bytes(grads((BASE, 0, 200_000)), clip())
     assert 0 < one <= 4096
-    # a partial for every 2048 elements or fewer, longer items past 2^25 elements
-    many = A.ar_grad_workspace_bytes(grads(*[(BASE + i * 4096, 0, 1000) for i in range(5000)]), clip())
-    assert one < many < 1 << 20
-    assert A.ar_grad_workspace_bytes(grads((BASE, 0, 1 << 40)), clip()) < 1 << 20
-    assert A.ar_grad_workspace_bytes(grads(GOOD), clip(known=BASE - 64, total=None)) == 0
+    # a partial for every workgroup, or for every item where the tensors' own norms are asked for
+    sizes = [1000] * 5000
+    many = grads(*[(BASE + i * 4096, 0, n) for i, n in enumerate(sizes)])
+    assert one < A.ar_grad_workspace_bytes(many, clip()) < 1 << 16
+    assert A.ar_grad_workspace_bytes(many, clip(each=BASE - (1 << 20))) >= 8 * 5000
+    for each in (None, BASE - 256):
+        assert A.ar_grad_workspace_bytes(grads((BASE, 0, 1 << 40)), clip(each=each)) < 1 << 20
+    assert A.ar_grad_workspace_bytes(grads((BASE, 0, 200_000)), clip(known=BASE - 64, total=None)) == 0
+    args = (8, "bf16", "sum")
+    assert A.ar_allreduce_clip_workspace_bytes([106], *args, "allreduce", clip()) == 0
     n = 10_000
-    plain = A.ar_allreduce_clip_workspace_bytes([n, n], 8, "bf16", "sum", "allreduce", clip())
-    scatter = A.ar_allreduce_clip_workspace_bytes([n, n], 8, "bf16", "sum", "reduce_scatter", clip())
-    assert plain < 1 << 16 and scatter >= 2 * n * 2  # the lower halves of the sums
+    assert 0 < A.ar_allreduce_clip_workspace_bytes([n, n], *args, "allreduce", clip()) < 1 << 16
+    assert A.ar_allreduce_clip_workspace_bytes([n, n], *args, "reduce_scatter", clip()) >= 2 * n * 2  # lower halves of the sums
 
 
 def test_torch_side_refuses_host_tensors():
