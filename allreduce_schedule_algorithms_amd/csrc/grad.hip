@@ -130,13 +130,26 @@ template <int KIND, int THREADS> __device__ __forceinline__ void join_group(Part
     for (int w = 1; w < THREADS / 64; ++w) p.join(wave[w]);
 }
 
+// `count` partials joined in one order, the result in thread 0: a thread's loads are in flight together.
+template <int KIND, int THREADS> __device__ __forceinline__ Part<KIND> join_partials(const double* partial, int count) {
+  constexpr int U = 8;
+  Part<KIND> p;
+  for (int i = threadIdx.x; i < count; i += U * THREADS) {
+    double x[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) x[j] = i + j * THREADS < count ? partial[i + j * THREADS] : 0.0;
+#pragma unroll
+    for (int j = 0; j < U; ++j) p.join(x[j]);
+  }
+  join_group<KIND, THREADS>(p);
+  return p;
+}
+
 // The norm that a call's partials make, in every thread of a workgroup: each of them joins them by
-// itself, in one order, which costs less than a launch between two passes.
+// itself, which costs less than a launch between two passes.
 template <int KIND, int THREADS> __device__ __forceinline__ Part<KIND> join_all(const double* partial, int count) {
   __shared__ double all;
-  Part<KIND> p;
-  for (int i = threadIdx.x; i < count; i += THREADS) p.join(partial[i]);
-  join_group<KIND, THREADS>(p);
+  Part<KIND> p = join_partials<KIND, THREADS>(partial, count);
   if (threadIdx.x == 0) all = p.v;
   __syncthreads();
   p.v = all;
@@ -252,27 +265,27 @@ template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) v
   }
 }
 
-constexpr int kFinalThreads = 1024;
-// joined: the partials as one, for the pass that scales.
-template <int KIND> __global__ __launch_bounds__(kFinalThreads) void k_norm_final(const double* partial, int count, double* joined, float* total) {
-  const Part<KIND> p = join_all<KIND, kFinalThreads>(partial, count);
-  if (threadIdx.x == 0) {
-    *joined = p.v;
-    if (total) *total = float(p.norm());
-  }
-}
-
-constexpr int kEachTensors = 900;
+// The call's norm (a call without tensors' own norms: the first table is empty), and the tensors' own: a
+// workgroup joins one tensor's partials, the one behind the last tensor all of them. `joined` is for a
+// pass that scales.
+constexpr int kFinalThreads = 512, kEachTensors = 900;
 struct EachTab {
   int32_t first[kEachTensors + 1];  // first partial of every tensor
+  int32_t count;
 };
 
-template <int KIND> __global__ __launch_bounds__(64) void k_norm_each(EachTab tab, const double* partial, float* each) {
+template <int KIND> __global__ __launch_bounds__(kFinalThreads) void k_norm_final(EachTab tab, const double* partial, int all, double* joined, float* total, float* each) {
   const int i = blockIdx.x;
-  Part<KIND> p;
-  for (int k = tab.first[i] + threadIdx.x; k < tab.first[i + 1]; k += 64) p.join(partial[k]);
-  join_group<KIND, 64>(p);
-  if (threadIdx.x == 0) each[i] = float(p.norm());
+  if (i < tab.count) {
+    const Part<KIND> p = join_partials<KIND, kFinalThreads>(partial + tab.first[i], tab.first[i + 1] - tab.first[i]);
+    if (threadIdx.x == 0) each[i] = float(p.norm());
+  } else {
+    const Part<KIND> p = join_partials<KIND, kFinalThreads>(partial, all);
+    if (threadIdx.x == 0) {
+      *joined = p.v;
+      if (total) *total = float(p.norm());
+    }
+  }
 }
 
 template <int DS, int DD, int L> __device__ __forceinline__ void scale_item(const void* src, void* dst, int64_t e0, int cnt, int lane, Factor f) {
@@ -770,16 +783,18 @@ size_t partial_bytes(int64_t items, int64_t launches, bool each) {
   if ((kind) == N_L2) { constexpr int KIND = N_L2; __VA_ARGS__; } \
   else { constexpr int KIND = N_MAX; __VA_ARGS__; }
 
-// Every tensor's or bucket's own norm from the call's partials.
-void launch_each(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, const double* partial) {
-  const int64_t count = int64_t(firsts.size()) - 1;
-  for (int64_t i0 = 0; i0 < count; i0 += kEachTensors) {
+// The norm of the call, and every tensor's or bucket's own (clip.each; firsts: their first partials).
+void launch_final(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, const double* partial, int partials, double* joined) {
+  const int64_t count = clip.each ? int64_t(firsts.size()) - 1 : 0;
+  for (int64_t i0 = 0; i0 == 0 || i0 < count; i0 += kEachTensors) {
     EachTab tab;
-    const int64_t c = std::min<int64_t>(kEachTensors, count - i0);
-    std::memcpy(tab.first, firsts.data() + i0, size_t(c + 1) * sizeof(int32_t));
-    AR_KIND(clip.norm, s.launch(k_norm_each<KIND>, c, 64, tab, partial, clip.each + i0));
+    tab.count = int32_t(std::min<int64_t>(kEachTensors, count - i0));
+    std::memcpy(tab.first, firsts.data() + i0, size_t(tab.count + 1) * sizeof(int32_t));
+    const int64_t blocks = tab.count + (i0 + kEachTensors >= count ? 1 : 0);
+    AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, blocks, kFinalThreads, tab, partial, partials, joined, clip.total, clip.each + i0));
   }
 }
+int64_t final_launches(const Clip& clip, int64_t count) { return clip.each ? std::max<int64_t>(1, pieces(count, kEachTensors)) : 1; }
 
 int64_t total_of(const Grad* g, int64_t count) {
   int64_t t = 0;
@@ -854,15 +869,14 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
   double* partial = reinterpret_cast<double*>(ws + kHead);
   const int64_t nt = int64_t(tabs.size());
   const bool final = !clip.known && (!scale || clip.each || !nt);  // otherwise the scaling pass joins the partials
-  s.left = (clip.known ? 0 : nt) + (scale ? nt : 0) + (final ? 1 : 0) + (clip.each ? pieces(count, kEachTensors) : 0);
+  s.left = (clip.known ? 0 : nt) + (scale ? nt : 0) + (final ? final_launches(clip, count) : 0);
   if (!clip.known)
     for (int64_t k = 0; k < nt; ++k) {
       if (clip.each) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, true, true>, blocks[k], kThreads, tabs[k], partial)); }
       else if (!scale) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, true>, blocks[k], kThreads, tabs[k], partial)); }
       else { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, false>, blocks[k], kThreads, tabs[k], partial)); }
     }
-  if (final) AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, 1, kFinalThreads, (const double*)partial, int(partials), joined, clip.total));
-  if (clip.each) launch_each(s, clip, firsts, partial);
+  if (final) launch_final(s, clip, firsts, partial, int(partials), joined);
   if (scale) {
     Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, clip.known, final ? nullptr : clip.total};
     for (int64_t k = nt - 1; k >= 0; --k) {
@@ -990,7 +1004,7 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   }
   const int64_t nt = int64_t(pl.tabs.size());
   const bool final = clip.each || !nt;  // otherwise the second pass joins the partials
-  s.left = 2 * nt + (final ? 1 : 0) + (clip.each ? pieces(b.count, kEachTensors) : 0);
+  s.left = 2 * nt + (final ? final_launches(clip, b.count) : 0);
   const int batch = leaf_batch(b.P);
   for (int64_t k = 0; k < nt; ++k) {
 #define AR_REDUCE(DT_, EACH_) AR_KIND(clip.norm, launch_reduce<DT_, KIND, EACH_>(s, batch, blocks[k], pl.tabs[k], partial))
@@ -1001,8 +1015,7 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
     }
 #undef AR_REDUCE
   }
-  if (final) AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, 1, kFinalThreads, (const double*)partial, int(partials), joined, clip.total));
-  if (clip.each) launch_each(s, clip, pl.firsts, partial);
+  if (final) launch_final(s, clip, pl.firsts, partial, int(partials), joined);
   Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, nullptr, final ? nullptr : clip.total};
   for (int64_t k = 0; k < nt; ++k) {
     if (b.dtype == D_BF16) { AR_KIND(clip.norm, s.launch(k_bucket_spread<D_BF16, KIND>, blocks[k], kThreads, pl.tabs[k], lim)); }
