@@ -130,6 +130,13 @@ template <int KIND, int THREADS> __device__ __forceinline__ void join_group(Part
     for (int w = 1; w < THREADS / 64; ++w) p.join(wave[w]);
 }
 
+// An item's partials, one from each wave: its workgroup need not meet.
+constexpr int kWaves = kThreads / 64;
+template <int KIND> __device__ __forceinline__ void put_waves(Part<KIND> p, double* partial) {
+  join_wave(p);
+  if (threadIdx.x % 64 == 0) partial[threadIdx.x / 64] = p.v;
+}
+
 // `count` partials joined in one order, the result in thread 0: a thread's loads are in flight together.
 template <int KIND, int THREADS> __device__ __forceinline__ Part<KIND> join_partials(const double* partial, int count) {
   constexpr int U = 8;
@@ -244,7 +251,7 @@ __device__ __forceinline__ GradItem grad_item(const GradTab& tab, int it) {
   return w;
 }
 
-// EACH: a partial for every item (which the tensors' own norms are joined from), otherwise one for
+// EACH: partials for every item (which the tensors' own norms are joined from), otherwise one for
 // every workgroup over all of its items. NT (a norm alone): the loads leave the cache in front of HBM to
 // others, 990 M bf16 355 -> 326 us; a pass that a scaling follows leaves its last part there.
 template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTab tab, double* partial) {
@@ -254,8 +261,7 @@ template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) v
     if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     else norm_item<KIND, D_FP32, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     if constexpr (EACH) {
-      join_group<KIND, kThreads>(p);
-      if (threadIdx.x == 0) partial[tab.at + it] = p.v;
+      put_waves(p, partial + int64_t(tab.at + it) * kWaves);
       p = Part<KIND>();
     }
   }
@@ -403,11 +409,12 @@ __global__ __launch_bounds__(kSmallThreads) void k_grad_small(GradTab tab, float
 // The sums lie in the result's own place: fp32 sums in rank 0's buffer (the Allreduce), or in the
 // owner's part (the reduce-scatter); a bf16 sum's upper half there and its lower half at the same
 // place of rank 1's buffer, or of the workspace (the reduce-scatter leaves other elements alone).
-// With one rank the sum is its only operand and has no lower half.
+// Few ranks are read twice instead, and no sum is kept: the Allreduce then moves 3 P elements in place of
+// 2 P + 2 in fp32, and of 2 P + 4 in bf16, whose fp32 sums take two each.
 constexpr int kTabPtrs = 400, kTabBuckets = 16;
 struct BucketTab {
   void* p[kTabPtrs];               // P pointers of every bucket
-  uint16_t* low[kTabBuckets];      // lower halves of bf16 sums, by element; null: none
+  uint16_t* low[kTabBuckets];      // lower halves of bf16 sums, by element
   int64_t part[kTabBuckets];       // elements per part (the whole bucket for the Allreduce)
   int64_t n[kTabBuckets];
   int32_t first[kTabBuckets + 1];  // first work item
@@ -440,14 +447,14 @@ __device__ __forceinline__ BucketItem bucket_item(const BucketTab& tab, int it) 
 // is added; a thread's M vectors go together. One load at a time took 135 us for the sums of 7 x 2^24
 // fp32 and 134 us for those of 192 x 2^20 bf16; loading the next batch before adding this one gained
 // nothing (178 and 132 us for the whole call, against 175 and 135).
-template <int DT, int V, int M, int B>
+template <int DT, int V, int M, int B, bool NT>
 __device__ __forceinline__ void ld_ranks(void* const* ptr, int P, int base, int64_t e, const bool (&ok)[M], typename Raw<DT, V>::T (&r)[B][M]) {
 #pragma unroll
   for (int k = 0; k < B; ++k) {
     const void* p = ptr[base + k < P ? base + k : base];
 #pragma unroll
     for (int j = 0; j < M; ++j)
-      if (ok[j]) r[k][j] = ld_raw<DT, V, true>(p, e + j * kThreads * V);
+      if (ok[j]) r[k][j] = ld_raw<DT, V, NT>(p, e + j * kThreads * V);
   }
 }
 
@@ -466,11 +473,11 @@ __device__ __forceinline__ void add_ranks(int P, int base, const typename Raw<DT
   }
 }
 
-template <int DT, int V, int M, int B>
+template <int DT, int V, int M, int B, bool NT>
 __device__ __forceinline__ void sum_ranks(void* const* ptr, int P, float div, int64_t e, const bool (&ok)[M], float (&acc)[M][V]) {
   for (int base = 0; base < P; base += B) {
     typename Raw<DT, V>::T r[B][M];
-    ld_ranks<DT, V, M, B>(ptr, P, base, e, ok, r);
+    ld_ranks<DT, V, M, B, NT>(ptr, P, base, e, ok, r);
     add_ranks<DT, V, M, B>(P, base, r, acc);
   }
   if (div > 0) {
@@ -511,7 +518,7 @@ template <int DT, int V> __device__ __forceinline__ void put_sum(void* own, uint
       l[i] = (a & 0xffffu) | (b << 16);
     }
     st_raw<D_BF16, V, false>(own, e, h);
-    if (low) st_raw<D_BF16, V, false>(low, e, l);
+    st_raw<D_BF16, V, false>(low, e, l);
   }
 }
 
@@ -520,7 +527,7 @@ template <int DT> __device__ __forceinline__ void put_one(void* own, uint16_t* l
     static_cast<float*>(own)[e] = s;
   } else {
     static_cast<uint16_t*>(own)[e] = uint16_t(as_u(s) >> 16);
-    if (low) low[e] = uint16_t(as_u(s));
+    low[e] = uint16_t(as_u(s));
   }
 }
 
@@ -529,20 +536,19 @@ template <int DT, int V> __device__ __forceinline__ void get_sum(const void* own
 #pragma unroll
   for (int i = 0; i < V; ++i) s[i] = value<DT, V>(h, i);
   if constexpr (DT == D_BF16) {
-    if (low) {
-      const typename Raw<DT, V>::T l = ld_raw<DT, V, false>(low, e);
+    const typename Raw<DT, V>::T l = ld_raw<DT, V, false>(low, e);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = as_f(as_u(s[i]) | (i % 2 ? l[i / 2] >> 16 : l[i / 2] & 0xffffu));
-    }
+    for (int i = 0; i < V; ++i) s[i] = as_f(as_u(s[i]) | (i % 2 ? l[i / 2] >> 16 : l[i / 2] & 0xffffu));
   }
 }
 
 template <int DT> __device__ __forceinline__ float get_one(const void* own, const uint16_t* low, int64_t e) {
   const float s = ld_one<DT>(own, e);
-  return DT == D_BF16 && low ? as_f(as_u(s) | low[e]) : s;
+  return DT == D_BF16 ? as_f(as_u(s) | low[e]) : s;
 }
 
-template <int DT, int KIND, int B, bool EACH>
+// KEEP: the sums stay for the second pass. Otherwise the second pass reads the ranks again.
+template <int DT, int KIND, int B, bool EACH, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, double* partial) {
   constexpr int V = DT == D_BF16 ? 8 : 4, M = 8 / V;
   Part<KIND> p;
@@ -555,24 +561,23 @@ __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, doubl
 #pragma unroll
       for (int j = 0; j < M; ++j) ok[j] = v + j * kThreads < nv;
       float s[M][V];
-      sum_ranks<DT, V, M, B>(ptr, tab.P, tab.div, w.e0 + int64_t(v) * V, ok, s);
+      sum_ranks<DT, V, M, B, KEEP>(ptr, tab.P, tab.div, w.e0 + int64_t(v) * V, ok, s);
 #pragma unroll
       for (int j = 0; j < M; ++j)
         if (ok[j]) {
 #pragma unroll
           for (int i = 0; i < V; ++i) p.add(s[j][i]);
-          put_sum<DT, V>(ptr[w.owner], tab.low[w.b], w.e0 + int64_t(v + j * kThreads) * V, s[j]);
+          if constexpr (KEEP) put_sum<DT, V>(ptr[w.owner], tab.low[w.b], w.e0 + int64_t(v + j * kThreads) * V, s[j]);
         }
     }
     const int t = nv * V + threadIdx.x;
     if (t < w.cnt) {
       const float s = sum_one<DT>(ptr, tab.P, tab.div, w.e0 + t);
       p.add(s);
-      put_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t, s);
+      if constexpr (KEEP) put_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t, s);
     }
     if constexpr (EACH) {
-      join_group<KIND, kThreads>(p);
-      if (threadIdx.x == 0) partial[tab.at + it] = p.v;
+      put_waves(p, partial + int64_t(tab.at + it) * kWaves);
       p = Part<KIND>();
     }
   }
@@ -585,34 +590,46 @@ __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, doubl
 // Items go in the first pass's order, workgroup by workgroup: the sums are read on the XCD that wrote
 // them, out of its L2 or the cache in front of HBM, which the stores to the ranks do not pass through
 // (7 x 2^24 fp32: 213 us for the call with plain stores, 178 with these).
-template <int DT, int KIND> __global__ __launch_bounds__(kThreads) void k_bucket_spread(BucketTab tab, Limit lim) {
+//
+// B > 0: the first pass kept no sums, and this one makes them again from B ranks, backwards from what the
+// first read last.
+template <int DT, int KIND, int B> __global__ __launch_bounds__(kThreads) void k_bucket_spread(BucketTab tab, Limit lim) {
   constexpr int V = DT == D_BF16 ? 8 : 4, M = 8 / V;
   const Factor f = factor_for<KIND>(lim);
-  for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
+  const int items = tab.first[tab.count], step = B ? -int(gridDim.x) : int(gridDim.x);
+  for (int it = B ? last_item(items) : blockIdx.x; B ? it >= 0 : it < items; it += step) {
     const BucketItem w = bucket_item(tab, it);
     void* const* ptr = tab.p + w.b * tab.P;
     const int q0 = tab.owners ? w.owner : 0, q1 = tab.owners ? w.owner + 1 : tab.P;
     const int nv = w.cnt / V;
     for (int v = threadIdx.x; v < nv; v += kThreads * M) {
+      const int64_t e = w.e0 + int64_t(v) * V;
       bool ok[M];
+      float s[M][V];
+#pragma unroll
+      for (int j = 0; j < M; ++j) ok[j] = v + j * kThreads < nv;
+      if constexpr (B > 0) {
+        sum_ranks<DT, V, M, B, true>(ptr, tab.P, tab.div, e, ok, s);
+      } else {
+#pragma unroll
+        for (int j = 0; j < M; ++j)
+          if (ok[j]) get_sum<DT, V>(ptr[w.owner], tab.low[w.b], e + j * kThreads * V, s[j]);
+      }
       typename Raw<DT, V>::T y[M];
 #pragma unroll
       for (int j = 0; j < M; ++j) {
-        ok[j] = v + j * kThreads < nv;
-        float s[V];
-        if (ok[j]) get_sum<DT, V>(ptr[w.owner], tab.low[w.b], w.e0 + int64_t(v + j * kThreads) * V, s);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = f(s[i]);
-        y[j] = pack<DT, V>(s);
+        for (int i = 0; i < V; ++i) s[j][i] = f(s[j][i]);
+        y[j] = pack<DT, V>(s[j]);
       }
       for (int q = q0; q < q1; ++q)
 #pragma unroll
         for (int j = 0; j < M; ++j)
-          if (ok[j]) st_raw<DT, V, true>(ptr[q], w.e0 + int64_t(v + j * kThreads) * V, y[j]);
+          if (ok[j]) st_raw<DT, V, true>(ptr[q], e + j * kThreads * V, y[j]);
     }
     const int t = nv * V + threadIdx.x;
     if (t < w.cnt) {
-      const float s = f(get_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t));
+      const float s = f(B ? sum_one<DT>(ptr, tab.P, tab.div, w.e0 + t) : get_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t));
       for (int q = q0; q < q1; ++q) st_one<DT>(ptr[q], w.e0 + t, s);
     }
   }
@@ -768,28 +785,29 @@ struct Sequence {
   }
 };
 
-// Workgroups of a launch with `items` of the call's `all` items: fewer than most_blocks() where that
-// gives every workgroup the same count of items.
+// Workgroups of a launch with `items` of the call's `all` items. Their counts of items may differ by one:
+// as many workgroups on every compute unit matter more (7 x 2^24 fp32: 175 us with 1536 workgroups of 5
+// or 6 items, 184 with 1366 of 6).
 int64_t blocks_for(int64_t items, int64_t all) {
-  const int64_t rounds = std::max<int64_t>(1, pieces(all, most_blocks()));
-  return std::max<int64_t>(1, std::min<int64_t>(pieces(items, rounds), launch_blocks()));
+  const int64_t most = most_blocks();
+  return std::max<int64_t>(1, std::min<int64_t>(all <= most ? items : pieces(items * most, all), launch_blocks()));
 }
-// Bytes of a call's partials: one per item, or per workgroup (blocks_for rounds up once a launch).
+// Bytes of a call's partials: one per wave and item, or per workgroup (blocks_for rounds up once a launch).
 size_t partial_bytes(int64_t items, int64_t launches, bool each) {
-  return round_up(size_t(each ? items : std::min(items, most_blocks() + launches)) * sizeof(double));
+  return round_up(size_t(each ? items * kWaves : std::min(items, most_blocks() + launches)) * sizeof(double));
 }
 
 #define AR_KIND(kind, ...)                                   \
   if ((kind) == N_L2) { constexpr int KIND = N_L2; __VA_ARGS__; } \
   else { constexpr int KIND = N_MAX; __VA_ARGS__; }
 
-// The norm of the call, and every tensor's or bucket's own (clip.each; firsts: their first partials).
+// The norm of the call, and every tensor's or bucket's own (clip.each; firsts: their first items).
 void launch_final(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, const double* partial, int partials, double* joined) {
   const int64_t count = clip.each ? int64_t(firsts.size()) - 1 : 0;
   for (int64_t i0 = 0; i0 == 0 || i0 < count; i0 += kEachTensors) {
     EachTab tab;
     tab.count = int32_t(std::min<int64_t>(kEachTensors, count - i0));
-    std::memcpy(tab.first, firsts.data() + i0, size_t(tab.count + 1) * sizeof(int32_t));
+    for (int k = 0; k <= tab.count; ++k) tab.first[k] = firsts[size_t(i0 + k)] * kWaves;
     const int64_t blocks = tab.count + (i0 + kEachTensors >= count ? 1 : 0);
     AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, blocks, kFinalThreads, tab, partial, partials, joined, clip.total, clip.each + i0));
   }
@@ -852,7 +870,7 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
     return s.done();
   }
   std::vector<int64_t> blocks;
-  int32_t partials = clip.each ? items : 0;
+  int32_t partials = clip.each ? items * kWaves : 0;
   for (GradTab& t : tabs) {
     blocks.push_back(blocks_for(t.first[t.count], items));
     if (clip.each) continue;
@@ -889,10 +907,23 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
 
 namespace {
 
-template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int batch, int64_t blocks, const BucketTab& t, double* partial) {
-#define AR_REDUCE_B(B_) s.launch(k_bucket_reduce<DT, KIND, B_, EACH>, blocks, kThreads, t, partial)
+// Ranks that the second pass reads again rather than finding their sums (30 M elements a rank, kept
+// and read again, us): fp32 2 ranks 132 and 116, 3 ranks 166 and 174; bf16 2 ranks 80 and 60, 3 ranks
+// 105 and 89, 4 ranks 121 and 119, and for the reduce-scatter 92 and 94.
+constexpr int32_t most_reread(int dtype) { return dtype == D_BF16 ? 3 : 2; }
+
+template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int64_t blocks, const BucketTab& t, double* partial) {
+#define AR_REDUCE_B(B_) s.launch(k_bucket_reduce<DT, KIND, B_, EACH, true>, blocks, kThreads, t, partial)
+  if (t.P <= most_reread(DT)) {
+    switch (t.P) {
+      case 1: s.launch(k_bucket_reduce<DT, KIND, 1, EACH, false>, blocks, kThreads, t, partial); break;
+      case 2: s.launch(k_bucket_reduce<DT, KIND, 2, EACH, false>, blocks, kThreads, t, partial); break;
+      default: if constexpr (DT == D_BF16) s.launch(k_bucket_reduce<DT, KIND, 3, EACH, false>, blocks, kThreads, t, partial);
+    }
+    return;
+  }
+  const int batch = leaf_batch(t.P);
   switch (batch) {
-    case 1: AR_REDUCE_B(1); break;
     case 2: AR_REDUCE_B(2); break;
     case 3: AR_REDUCE_B(3); break;
     case 4: AR_REDUCE_B(4); break;
@@ -904,6 +935,18 @@ template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int batch
 #undef AR_REDUCE_B
 }
 
+template <int DT, int KIND> void launch_spread(Sequence& s, int64_t blocks, const BucketTab& t, const Limit& lim) {
+  if (t.P > most_reread(DT)) {
+    s.launch(k_bucket_spread<DT, KIND, 0>, blocks, kThreads, t, lim);
+    return;
+  }
+  switch (t.P) {
+    case 1: s.launch(k_bucket_spread<DT, KIND, 1>, blocks, kThreads, t, lim); break;
+    case 2: s.launch(k_bucket_spread<DT, KIND, 2>, blocks, kThreads, t, lim); break;
+    default: if constexpr (DT == D_BF16) s.launch(k_bucket_spread<DT, KIND, 3>, blocks, kThreads, t, lim);
+  }
+}
+
 struct BucketPlan {
   std::vector<BucketTab> tabs;
   std::vector<int32_t> firsts{0};
@@ -911,7 +954,7 @@ struct BucketPlan {
   size_t low_bytes = 0;  // lower halves kept in the workspace
 };
 
-bool low_in_workspace(const Buckets& b) { return b.dtype == D_BF16 && b.coll == C_REDUCE_SCATTER && b.P > 1; }
+bool low_in_workspace(const Buckets& b) { return b.dtype == D_BF16 && b.coll == C_REDUCE_SCATTER && b.P > most_reread(b.dtype); }
 
 BucketPlan plan_buckets(const Buckets& b, int64_t per) {
   BucketPlan pl;
@@ -935,7 +978,7 @@ BucketPlan plan_buckets(const Buckets& b, int64_t per) {
       if (low_in_workspace(b)) {
         tab.low[k] = reinterpret_cast<uint16_t*>(pl.low_bytes);  // an offset until the workspace is known
         pl.low_bytes += round_up(size_t(n) * 2);
-      } else if (b.dtype == D_BF16 && b.P > 1) {
+      } else if (b.dtype == D_BF16 && b.P > most_reread(b.dtype)) {
         tab.low[k] = static_cast<uint16_t*>(tab.p[k * b.P + 1]);
       }
       tab.first[k + 1] = tab.first[k] + (n ? tab.ipp[k] * (scatter ? b.P : 1) : 0);
@@ -992,7 +1035,7 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   double* joined = reinterpret_cast<double*>(ws);
   double* partial = reinterpret_cast<double*>(ws + kHead);
   std::vector<int64_t> blocks;
-  int32_t partials = clip.each ? items : 0;
+  int32_t partials = clip.each ? items * kWaves : 0;
   char* low = ws + low_offset(pl, clip.each);
   for (BucketTab& t : pl.tabs) {
     if (low_in_workspace(b))
@@ -1005,9 +1048,8 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   const int64_t nt = int64_t(pl.tabs.size());
   const bool final = clip.each || !nt;  // otherwise the second pass joins the partials
   s.left = 2 * nt + (final ? final_launches(clip, b.count) : 0);
-  const int batch = leaf_batch(b.P);
   for (int64_t k = 0; k < nt; ++k) {
-#define AR_REDUCE(DT_, EACH_) AR_KIND(clip.norm, launch_reduce<DT_, KIND, EACH_>(s, batch, blocks[k], pl.tabs[k], partial))
+#define AR_REDUCE(DT_, EACH_) AR_KIND(clip.norm, launch_reduce<DT_, KIND, EACH_>(s, blocks[k], pl.tabs[k], partial))
     if (b.dtype == D_BF16) {
       if (clip.each) { AR_REDUCE(D_BF16, true); } else { AR_REDUCE(D_BF16, false); }
     } else {
@@ -1018,8 +1060,8 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   if (final) launch_final(s, clip, pl.firsts, partial, int(partials), joined);
   Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, nullptr, final ? nullptr : clip.total};
   for (int64_t k = 0; k < nt; ++k) {
-    if (b.dtype == D_BF16) { AR_KIND(clip.norm, s.launch(k_bucket_spread<D_BF16, KIND>, blocks[k], kThreads, pl.tabs[k], lim)); }
-    else { AR_KIND(clip.norm, s.launch(k_bucket_spread<D_FP32, KIND>, blocks[k], kThreads, pl.tabs[k], lim)); }
+    if (b.dtype == D_BF16) { AR_KIND(clip.norm, launch_spread<D_BF16, KIND>(s, blocks[k], pl.tabs[k], lim)); }
+    else { AR_KIND(clip.norm, launch_spread<D_FP32, KIND>(s, blocks[k], pl.tabs[k], lim)); }
     lim.total = nullptr;
   }
   return s.done();
