@@ -411,15 +411,18 @@ __global__ __launch_bounds__(kSmallThreads) void k_grad_small(GradTab tab, float
 // place of rank 1's buffer, or of the workspace (the reduce-scatter leaves other elements alone).
 // Few ranks are read twice instead, and no sum is kept: the Allreduce then moves 3 P elements in place of
 // 2 P + 2 in fp32, and of 2 P + 4 in bf16, whose fp32 sums take two each.
-constexpr int kTabPtrs = 400, kTabBuckets = 16;
+// A bucket's pointers fill whole batches of kRankBatch, the last one again behind the last rank: a
+// batch's pointers are then one scalar load, and its ranks' loads go out together with no test between
+// them (the extra ones find their lines in the cache).
+constexpr int kTabPtrs = 400, kTabBuckets = 16, kRankBatch = 16;
 struct BucketTab {
-  void* p[kTabPtrs];               // P pointers of every bucket
+  void* p[kTabPtrs];               // `stride` pointers of every bucket
   uint16_t* low[kTabBuckets];      // lower halves of bf16 sums, by element
   int64_t part[kTabBuckets];       // elements per part (the whole bucket for the Allreduce)
   int64_t n[kTabBuckets];
   int32_t first[kTabBuckets + 1];  // first work item
   int32_t ipp[kTabBuckets];        // work items per part
-  int32_t count, P, at;
+  int32_t count, P, stride, at;
   int32_t owners;                  // 1: part q belongs to rank q alone
   int64_t per;
   float div;                       // > 0: the sum is divided by it
@@ -448,10 +451,10 @@ __device__ __forceinline__ BucketItem bucket_item(const BucketTab& tab, int it) 
 // fp32 and 134 us for those of 192 x 2^20 bf16; loading the next batch before adding this one gained
 // nothing (178 and 132 us for the whole call, against 175 and 135).
 template <int DT, int V, int M, int B, bool NT>
-__device__ __forceinline__ void ld_ranks(void* const* ptr, int P, int base, int64_t e, const bool (&ok)[M], typename Raw<DT, V>::T (&r)[B][M]) {
+__device__ __forceinline__ void ld_ranks(void* const* ptr, int base, int64_t e, const bool (&ok)[M], typename Raw<DT, V>::T (&r)[B][M]) {
 #pragma unroll
   for (int k = 0; k < B; ++k) {
-    const void* p = ptr[base + k < P ? base + k : base];
+    const void* p = ptr[base + k];
 #pragma unroll
     for (int j = 0; j < M; ++j)
       if (ok[j]) r[k][j] = ld_raw<DT, V, NT>(p, e + j * kThreads * V);
@@ -477,7 +480,7 @@ template <int DT, int V, int M, int B, bool NT>
 __device__ __forceinline__ void sum_ranks(void* const* ptr, int P, float div, int64_t e, const bool (&ok)[M], float (&acc)[M][V]) {
   for (int base = 0; base < P; base += B) {
     typename Raw<DT, V>::T r[B][M];
-    ld_ranks<DT, V, M, B, NT>(ptr, P, base, e, ok, r);
+    ld_ranks<DT, V, M, B, NT>(ptr, base, e, ok, r);
     add_ranks<DT, V, M, B>(P, base, r, acc);
   }
   if (div > 0) {
@@ -488,21 +491,31 @@ __device__ __forceinline__ void sum_ranks(void* const* ptr, int P, float div, in
   }
 }
 
-// One element's sum, with the loads of up to 32 ranks in flight: what lies behind the last whole vector has
-// as many ranks to wait for as the rest.
+// One element's sum: what lies behind the last whole vector has as many ranks to wait for as the rest.
 template <int DT> __device__ __forceinline__ float sum_one(void* const* ptr, int P, float div, int64_t e) {
-  constexpr int B = 32;
   float acc = 0;
-  for (int base = 0; base < P; base += B) {
-    float x[B];
+  for (int base = 0; base < P; base += kRankBatch) {
+    float x[kRankBatch];
 #pragma unroll
-    for (int r = 0; r < B; ++r)
-      if (base + r < P) x[r] = ld_one<DT>(ptr[base + r], e);
+    for (int r = 0; r < kRankBatch; ++r) x[r] = ld_one<DT>(ptr[base + r], e);
 #pragma unroll
-    for (int r = 0; r < B; ++r)
+    for (int r = 0; r < kRankBatch; ++r)
       if (base + r < P) acc = base + r ? acc + x[r] : x[r];
   }
   return div > 0 ? acc / div : acc;
+}
+
+// f(rank's buffer) for ranks [q0, q1), with their pointers looked up together.
+template <typename F> __device__ __forceinline__ void to_ranks(void* const* ptr, int q0, int q1, F&& f) {
+  int q = q0;
+  for (; q + 8 <= q1; q += 8) {
+    void* p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = ptr[q + k];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f(p[k]);
+  }
+  for (; q < q1; ++q) f(ptr[q]);
 }
 
 // Whole sums to and from their place.
@@ -547,14 +560,17 @@ template <int DT> __device__ __forceinline__ float get_one(const void* own, cons
   return DT == D_BF16 ? as_f(as_u(s) | low[e]) : s;
 }
 
+// Vectors of a thread that go together: an item of 2048 elements is one for bf16 and two for fp32.
+template <int DT> constexpr int kPair = DT == D_BF16 ? 1 : 2;
+
 // KEEP: the sums stay for the second pass. Otherwise the second pass reads the ranks again.
-template <int DT, int KIND, int B, bool EACH, bool KEEP>
+template <int DT, int KIND, int B, int M, bool EACH, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, double* partial) {
-  constexpr int V = DT == D_BF16 ? 8 : 4, M = 8 / V;
+  constexpr int V = DT == D_BF16 ? 8 : 4;
   Part<KIND> p;
   for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
     const BucketItem w = bucket_item(tab, it);
-    void* const* ptr = tab.p + w.b * tab.P;
+    void* const* ptr = tab.p + w.b * tab.stride;
     const int nv = w.cnt / V;
     for (int v = threadIdx.x; v < nv; v += kThreads * M) {
       bool ok[M];
@@ -594,12 +610,12 @@ __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, doubl
 // B > 0: the first pass kept no sums, and this one makes them again from B ranks, backwards from what the
 // first read last.
 template <int DT, int KIND, int B> __global__ __launch_bounds__(kThreads) void k_bucket_spread(BucketTab tab, Limit lim) {
-  constexpr int V = DT == D_BF16 ? 8 : 4, M = 8 / V;
+  constexpr int V = DT == D_BF16 ? 8 : 4, M = kPair<DT>;
   const Factor f = factor_for<KIND>(lim);
   const int items = tab.first[tab.count], step = B ? -int(gridDim.x) : int(gridDim.x);
   for (int it = B ? last_item(items) : blockIdx.x; B ? it >= 0 : it < items; it += step) {
     const BucketItem w = bucket_item(tab, it);
-    void* const* ptr = tab.p + w.b * tab.P;
+    void* const* ptr = tab.p + w.b * tab.stride;
     const int q0 = tab.owners ? w.owner : 0, q1 = tab.owners ? w.owner + 1 : tab.P;
     const int nv = w.cnt / V;
     for (int v = threadIdx.x; v < nv; v += kThreads * M) {
@@ -622,22 +638,23 @@ template <int DT, int KIND, int B> __global__ __launch_bounds__(kThreads) void k
         for (int i = 0; i < V; ++i) s[j][i] = f(s[j][i]);
         y[j] = pack<DT, V>(s[j]);
       }
-      for (int q = q0; q < q1; ++q)
+      to_ranks(ptr, q0, q1, [&](void* p) {
 #pragma unroll
         for (int j = 0; j < M; ++j)
-          if (ok[j]) st_raw<DT, V, true>(ptr[q], e + j * kThreads * V, y[j]);
+          if (ok[j]) st_raw<DT, V, true>(p, e + j * kThreads * V, y[j]);
+      });
     }
     const int t = nv * V + threadIdx.x;
     if (t < w.cnt) {
       const float s = f(B ? sum_one<DT>(ptr, tab.P, tab.div, w.e0 + t) : get_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t));
-      for (int q = q0; q < q1; ++q) st_one<DT>(ptr[q], w.e0 + t, s);
+      to_ranks(ptr, q0, q1, [&](void* p) { st_one<DT>(p, w.e0 + t, s); });
     }
   }
 }
 
 // Few elements in one launch: one workgroup, whose waves take an item of 64 elements each and keep their sums
-// in registers between the passes (24 x 106 fp32: 5.9 us against 12.6 for two launches, 8 x 1024: 5.9 and
-// 6.7; of two items to a wave, 8 x 2048, 8.3 and 6.9).
+// in registers between the passes (8 x 1024 fp32: 5.4 us against 6.7 for two launches, 24 x 106: 5.6 and
+// 12.6; with two items to a wave, 8 x 2048, 8.3 and 6.9).
 constexpr int kSmallSpan = 64;
 template <int DT, int KIND>
 __global__ __launch_bounds__(kSmallThreads) void k_bucket_small(BucketTab tab, float* total, float* each, float max_norm, float eps) {
@@ -648,7 +665,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_bucket_small(BucketTab tab, f
   BucketItem w{0, 0, 0, 0};
   float sum = 0;
   if (it < tab.first[tab.count]) w = bucket_item(tab, it);
-  void* const* ptr = tab.p + w.b * tab.P;
+  void* const* ptr = tab.p + w.b * tab.stride;
   if (lane < w.cnt) {
     sum = sum_one<DT>(ptr, tab.P, tab.div, w.e0 + lane);
     p.add(sum);
@@ -671,8 +688,7 @@ __global__ __launch_bounds__(kSmallThreads) void k_bucket_small(BucketTab tab, f
   }
   const float y = factor_of(all, max_norm, eps)(sum);
   const int q0 = tab.owners ? w.owner : 0, q1 = tab.owners ? w.owner + 1 : tab.P;
-  if (lane < w.cnt)
-    for (int q = q0; q < q1; ++q) st_one<DT>(ptr[q], w.e0 + lane, y);
+  if (lane < w.cnt) to_ranks(ptr, q0, q1, [&](void* p) { st_one<DT>(p, w.e0 + lane, y); });
 }
 
 // ----------------------------------------------------------------------------
@@ -907,29 +923,34 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
 
 namespace {
 
+// Few elements are cut finer and, of many ranks, 16 loaded together: what such a call waits for is one
+// batch of loads after the other. us for a call: 127 ranks x 2250 fp32 35 -> 21, 24 x 60000 13.8 -> 11.0,
+// 192 x 65536 bf16 52 -> 32, 64 x 2^18 25 -> 21, 8 x 65536 fp32 9.4 -> 8.5; 8 x 2^19 fp32 would take
+// 12.5 for 12.1, and 192 x 2^20 bf16 150 for 143.
+constexpr int64_t kFineUnit = 512, kFineTotal = int64_t(1) << 18;
+
 // Ranks that the second pass reads again rather than finding their sums (30 M elements a rank, kept
 // and read again, us): fp32 2 ranks 132 and 116, 3 ranks 166 and 174; bf16 2 ranks 80 and 60, 3 ranks
 // 105 and 89, 4 ranks 121 and 119, and for the reduce-scatter 92 and 94.
 constexpr int32_t most_reread(int dtype) { return dtype == D_BF16 ? 3 : 2; }
 
 template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int64_t blocks, const BucketTab& t, double* partial) {
-#define AR_REDUCE_B(B_) s.launch(k_bucket_reduce<DT, KIND, B_, EACH, true>, blocks, kThreads, t, partial)
+#define AR_REDUCE_B(B_) s.launch(k_bucket_reduce<DT, KIND, B_, kPair<DT>, EACH, true>, blocks, kThreads, t, partial)
   if (t.P <= most_reread(DT)) {
     switch (t.P) {
-      case 1: s.launch(k_bucket_reduce<DT, KIND, 1, EACH, false>, blocks, kThreads, t, partial); break;
-      case 2: s.launch(k_bucket_reduce<DT, KIND, 2, EACH, false>, blocks, kThreads, t, partial); break;
-      default: if constexpr (DT == D_BF16) s.launch(k_bucket_reduce<DT, KIND, 3, EACH, false>, blocks, kThreads, t, partial);
+      case 1: s.launch(k_bucket_reduce<DT, KIND, 1, kPair<DT>, EACH, false>, blocks, kThreads, t, partial); break;
+      case 2: s.launch(k_bucket_reduce<DT, KIND, 2, kPair<DT>, EACH, false>, blocks, kThreads, t, partial); break;
+      default: if constexpr (DT == D_BF16) s.launch(k_bucket_reduce<DT, KIND, 3, kPair<DT>, EACH, false>, blocks, kThreads, t, partial);
     }
     return;
   }
-  const int batch = leaf_batch(t.P);
-  switch (batch) {
-    case 2: AR_REDUCE_B(2); break;
+  switch (t.P <= 8 ? t.P : t.per == kFineUnit ? 16 : 8) {
     case 3: AR_REDUCE_B(3); break;
     case 4: AR_REDUCE_B(4); break;
     case 5: AR_REDUCE_B(5); break;
     case 6: AR_REDUCE_B(6); break;
     case 7: AR_REDUCE_B(7); break;
+    case 16: s.launch(k_bucket_reduce<DT, KIND, 16, 1, EACH, true>, blocks, kThreads, t, partial); break;
     default: AR_REDUCE_B(8); break;
   }
 #undef AR_REDUCE_B
@@ -956,22 +977,26 @@ struct BucketPlan {
 
 bool low_in_workspace(const Buckets& b) { return b.dtype == D_BF16 && b.coll == C_REDUCE_SCATTER && b.P > most_reread(b.dtype); }
 
+int rank_stride(int P) { return (P + kRankBatch - 1) / kRankBatch * kRankBatch; }
+
 BucketPlan plan_buckets(const Buckets& b, int64_t per) {
   BucketPlan pl;
-  const int64_t fit = std::min<int64_t>(kTabBuckets, kTabPtrs / b.P);
+  const int stride = rank_stride(b.P);
+  const int64_t fit = std::min<int64_t>(kTabBuckets, kTabPtrs / stride);
   const bool scatter = b.coll == C_REDUCE_SCATTER;
   for (int64_t i0 = 0; i0 < b.count; i0 += fit) {
     BucketTab tab;
     std::memset(&tab, 0, sizeof(tab));
     tab.count = int32_t(std::min(fit, b.count - i0));
     tab.P = b.P;
+    tab.stride = stride;
     tab.at = pl.firsts.back();
     tab.owners = scatter;
     tab.per = per;
     tab.div = b.op == O_AVG ? float(b.P) : 0.0f;
     for (int k = 0; k < tab.count; ++k) {
       const int64_t n = b.n[i0 + k], part = scatter ? pieces(n, b.P) : n;
-      for (int q = 0; q < b.P; ++q) tab.p[k * b.P + q] = b.bufs ? b.bufs[(i0 + k) * b.P + q] : nullptr;  // none: only the size is asked
+      for (int q = 0; b.bufs && q < stride; ++q) tab.p[k * stride + q] = b.bufs[(i0 + k) * b.P + std::min(q, b.P - 1)];  // none: only the size is asked
       tab.n[k] = n;
       tab.part[k] = part;
       tab.ipp[k] = int32_t(std::max<int64_t>(1, pieces(part, per)));
@@ -979,7 +1004,7 @@ BucketPlan plan_buckets(const Buckets& b, int64_t per) {
         tab.low[k] = reinterpret_cast<uint16_t*>(pl.low_bytes);  // an offset until the workspace is known
         pl.low_bytes += round_up(size_t(n) * 2);
       } else if (b.dtype == D_BF16 && b.P > most_reread(b.dtype)) {
-        tab.low[k] = static_cast<uint16_t*>(tab.p[k * b.P + 1]);
+        tab.low[k] = static_cast<uint16_t*>(tab.p[k * stride + 1]);
       }
       tab.first[k + 1] = tab.first[k] + (n ? tab.ipp[k] * (scatter ? b.P : 1) : 0);
       pl.firsts.push_back(tab.at + tab.first[k + 1]);
@@ -998,8 +1023,8 @@ BucketPlan plan_call(const Buckets& b, bool each, bool* small) {
     total += b.n[i];
     if (b.n[i]) items += scatter ? b.P * pieces(pieces(b.n[i], b.P), kSmallSpan) : pieces(b.n[i], kSmallSpan);
   }
-  *small = b.count <= std::min<int64_t>(kTabBuckets, kTabPtrs / b.P) && items <= kSmallWaves;
-  return plan_buckets(b, *small ? kSmallSpan : item_size(total, each));
+  *small = b.count <= std::min<int64_t>(kTabBuckets, kTabPtrs / rank_stride(b.P)) && items <= kSmallWaves;
+  return plan_buckets(b, *small ? kSmallSpan : total <= kFineTotal ? kFineUnit : item_size(total, each));
 }
 
 // Where the lower halves start, behind the partials.
