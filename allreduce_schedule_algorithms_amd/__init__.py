@@ -6,6 +6,8 @@ has no CPU fallback and fails loudly when the library is missing.
 """
 from __future__ import annotations
 
+from array import array
+
 from . import _ar
 from ._ar import (  # noqa: F401
     ALGO_NAMES, ALGOS, AR_KNOB_AUTO, COLLECTIVES, COST_FORMS, DTYPES, EXECS, OPS, Algo, ArError, Collective,
@@ -97,6 +99,10 @@ def _grads(tensors, out=None):
     torch = _torch()
     tensors = list(tensors)
     count = len(tensors)
+    if out is not None:
+        out = list(out)
+        if len(out) != count:
+            raise _invalid(f"{count} gradients, and {len(out)} outputs")
     if not count:
         return GradList((), 0), None
     T = torch.Tensor
@@ -105,9 +111,6 @@ def _grads(tensors, out=None):
     words[0::4] = map(T.data_ptr, tensors)
     words[2::4] = sizes = list(map(T.numel, tensors))
     if out is not None:
-        out = list(out)
-        if len(out) != count:
-            raise _invalid(f"{count} gradients, and {len(out)} outputs")
         there, kinds = _check_tensors(torch, out, "outputs")
         if there != index or list(map(T.numel, out)) != sizes:
             raise _invalid("every output must be of its gradient's size, on its device")
@@ -223,12 +226,10 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
     sizes = numels[::P]
     if numels != [n for n in sizes for _ in range(P)] or len(set(types)) != 1:
         raise _invalid("a bucket's tensors must be of one size, and all tensors of one dtype")
-    dtype = types[0]
+    args = sizes, P, types[0], _ar._enum(OPS, op), _ar._enum(COLLECTIVES, collective)
     with _Place(index, stream) as at:
         total = at.floats()
         clip = make_clip(norm, max_norm, eps, total=total)
-        if workspace is None:
-            need = ar_allreduce_clip_workspace_bytes(sizes, P, dtype, op, collective, clip)
-        workspace = at.scratch(clip, workspace, 0 if workspace is not None else need)
-        ar_allreduce_clip(marshal_ptrs(list(map(T.data_ptr, tensors))), sizes, P, dtype, op, collective, clip, at.stream)
+        workspace = at.scratch(clip, workspace, 0 if workspace is not None else ar_allreduce_clip_workspace_bytes(*args, clip))
+        ar_allreduce_clip(array("Q", map(T.data_ptr, tensors)), *args, clip, at.stream)
     return total

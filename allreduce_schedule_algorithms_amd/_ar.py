@@ -405,9 +405,11 @@ def ar_grad_workspace_bytes(grads: GradList, clip: ar_clip) -> int:
 
 
 def ar_allreduce_clip(bufs, n, P, dtype, op, collective, clip: ar_clip, stream=None):
-    """bufs: buckets * P pointers or tensors, bucket by bucket; n: the buckets' elements."""
+    """bufs: buckets * P pointers or tensors, bucket by bucket (or an array of them, as marshal_ptrs or array("Q")
+    makes it); n: the buckets' elements."""
     sizes = array.array("q", n)
-    _check(lib.ar_allreduce_clip(_ptrs(bufs), sizes.buffer_info()[0], len(sizes), int(P), _enum(DTYPES, dtype),
+    ptrs = bufs.buffer_info()[0] if isinstance(bufs, array.array) else _ptrs(bufs)
+    _check(lib.ar_allreduce_clip(ptrs, sizes.buffer_info()[0], len(sizes), int(P), _enum(DTYPES, dtype),
                                  _enum(OPS, op), _enum(COLLECTIVES, collective), C.byref(clip), _stream(stream)))
 
 

@@ -435,19 +435,22 @@ ar_status ar_cache_stats_get(ar_cache_stats* out) {
   const ar::CacheStats c = ar::cache_stats();
   out->live_plans = c.live_plans;
   out->retired_plans = c.retired_plans;
-  out->workspaces = c.workspaces;
-  out->retired_workspaces = c.retired_workspaces;
+  const ar::GradCache g = ar::grad_cache();
+  out->workspaces = c.workspaces + g.live;
+  out->retired_workspaces = c.retired_workspaces + g.retired;
   out->plan_device_bytes = c.plan_device_bytes;
-  out->workspace_device_bytes = c.workspace_device_bytes;
+  out->workspace_device_bytes = c.workspace_device_bytes + g.bytes;
   return AR_OK;
 }
 
 ar_status ar_release_cached(void) {
-  ar::RunResult r = ar::release_cached();
+  ar::RunResult r = ar::grad_cache_wait();
+  if (!r.status) r = ar::release_cached();
   if (r.status) {
     t_hip = r.hip_error;
     return fail(ar_status(r.status), r.message);
   }
+  ar::grad_cache_free();
   return AR_OK;
 }
 

@@ -34,7 +34,6 @@
 #include <vector>
 
 #include "exec.h"
-#include "grad.h"
 #include "jit.h"
 #include "launch.h"
 
@@ -1193,10 +1192,6 @@ CacheStats cache_stats() {
     ++c.retired_workspaces;
     c.workspace_device_bytes += int64_t(w.bytes);
   }
-  const GradCache g = grad_cache();
-  c.workspaces += g.live;
-  c.retired_workspaces += g.retired;
-  c.workspace_device_bytes += g.bytes;
   return c;
 }
 
@@ -1211,7 +1206,6 @@ RunResult release_cached() {
   for (const auto& kv : plan_cache()) note(kv.second->device);
   for (const auto& p : retired_plans()) note(p->device);
   for (const auto& kv : ws_cache()) note(kv.first.first);
-  grad_cache_devices([](int d, void* to) { (*static_cast<decltype(note)*>(to))(d); }, &note);
   RunResult res;
   // every launch that may read a table or workspace ends before it is freed
   for (int d : devs) {
@@ -1231,7 +1225,6 @@ RunResult release_cached() {
     if (w.p) (void)hipFree(w.p);
   ws_cache().clear();
   retired_ws().clear();
-  grad_cache_free();
   sched_cache().clear();
   ++g_plan_generation;
   if (have_cur) (void)hipSetDevice(cur);

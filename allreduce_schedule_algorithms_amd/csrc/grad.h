@@ -47,7 +47,7 @@ struct GradCache {
   int64_t live = 0, retired = 0, bytes = 0;
 };
 GradCache grad_cache();
-void grad_cache_devices(void (*note)(int, void*), void* to);
-void grad_cache_free();  // after every device above was synchronized
+RunResult grad_cache_wait();  // synchronize every device they belong to
+void grad_cache_free();       // after that
 
 }  // namespace ar

@@ -23,6 +23,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <set>
 #include <vector>
 
 #include "kernels.h"
@@ -1106,10 +1107,22 @@ GradCache grad_cache() {
   return c;
 }
 
-void grad_cache_devices(void (*note)(int, void*), void* to) {
+RunResult grad_cache_wait() {
   std::lock_guard<std::mutex> lk(g_mu);
-  for (const auto& kv : kept()) note(kv.first.first, to);
-  for (const Kept& w : retired()) note(w.device, to);
+  std::set<int> devices;
+  for (const auto& kv : kept()) devices.insert(kv.first.first);
+  for (const Kept& w : retired()) devices.insert(w.device);
+  if (devices.empty()) return RunResult{};
+  int current = 0;
+  hipError_t e = hipGetDevice(&current);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  for (int d : devices) {
+    e = hipSetDevice(d);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    if (e != hipSuccess) break;
+  }
+  (void)hipSetDevice(current);
+  return e == hipSuccess ? RunResult{} : hip_fail(e, "synchronizing before the release");
 }
 
 void grad_cache_free() {
