@@ -702,6 +702,7 @@ RunResult hip_fail(hipError_t e, const char* what) {
   r.status = 4;  // AR_HIP_ERROR
   r.hip_error = int(e);
   r.message = std::string(what) + ": " + hipGetErrorString(e);
+  (void)hipGetLastError();  // reported here: not left for a later call that asks for the last error
   return r;
 }
 
@@ -778,20 +779,22 @@ RunResult workspace_of(const Clip& clip, size_t need, hipStream_t st, std::uniqu
   return r;
 }
 
-// The call's launches in order: the first records the start event, the last the stop event.
+// The call's launches in order: the first records the start event, the last the stop event. Errors are
+// taken from the launch itself, not from the thread's last one, which may be another call's.
+template <typename T> struct Same { using type = T; };
 struct Sequence {
   hipStream_t st;
   Evs ev;
   int64_t left;
   bool begun = false;
   hipError_t err = hipSuccess;
-  template <typename K, typename... A> void launch(K k, int64_t blocks, int threads, A... a) {
+  template <typename... A> void launch(void (*k)(A...), int64_t blocks, int threads, typename Same<A>::type... a) {
     if (err != hipSuccess) return;
     --left;
-    hipExtLaunchKernelGGL(k, dim3(unsigned(blocks)), dim3(unsigned(threads)), 0, st, begun ? nullptr : ev.start,
-                          left ? nullptr : ev.stop, 0, a...);
+    void* args[] = {static_cast<void*>(&a)...};
+    err = hipExtLaunchKernel(reinterpret_cast<const void*>(k), dim3(unsigned(blocks)), dim3(unsigned(threads)), args, 0, st,
+                             begun ? nullptr : ev.start, left ? nullptr : ev.stop, 0);
     begun = true;
-    err = hipGetLastError();
   }
   RunResult done() {
     if (err == hipSuccess && !begun) {  // no launch: both events mark this point of the stream
@@ -818,18 +821,19 @@ size_t partial_bytes(int64_t items, int64_t launches, bool each) {
   if ((kind) == N_L2) { constexpr int KIND = N_L2; __VA_ARGS__; } \
   else { constexpr int KIND = N_MAX; __VA_ARGS__; }
 
-// The norm of the call, and every tensor's or bucket's own (clip.each; firsts: their first items).
-void launch_final(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, const double* partial, int partials, double* joined) {
+// The norm of the call, and every tensor's or bucket's own before it (clip.each; firsts: their first items).
+int64_t final_cap() { return std::min<int64_t>(kEachTensors, launch_blocks()); }
+int64_t final_launches(const Clip& clip, int64_t count, int64_t cap) { return pieces((clip.each ? count : 0) + 1, cap); }
+void launch_final(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, int64_t cap, const double* partial, int partials, double* joined) {
   const int64_t count = clip.each ? int64_t(firsts.size()) - 1 : 0;
-  for (int64_t i0 = 0; i0 == 0 || i0 < count; i0 += kEachTensors) {
+  for (int64_t i0 = 0; i0 <= count; i0 += cap) {
     EachTab tab;
-    tab.count = int32_t(std::min<int64_t>(kEachTensors, count - i0));
+    const int64_t blocks = std::min(cap, count + 1 - i0);
+    tab.count = int32_t(std::min(cap, count - i0));
     for (int k = 0; k <= tab.count; ++k) tab.first[k] = firsts[size_t(i0 + k)] * kWaves;
-    const int64_t blocks = tab.count + (i0 + kEachTensors >= count ? 1 : 0);
     AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, blocks, kFinalThreads, tab, partial, partials, joined, clip.total, clip.each + i0));
   }
 }
-int64_t final_launches(const Clip& clip, int64_t count) { return clip.each ? std::max<int64_t>(1, pieces(count, kEachTensors)) : 1; }
 
 int64_t total_of(const Grad* g, int64_t count) {
   int64_t t = 0;
@@ -904,14 +908,15 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
   double* partial = reinterpret_cast<double*>(ws + kHead);
   const int64_t nt = int64_t(tabs.size());
   const bool final = !clip.known && (!scale || clip.each || !nt);  // otherwise the scaling pass joins the partials
-  s.left = (clip.known ? 0 : nt) + (scale ? nt : 0) + (final ? final_launches(clip, count) : 0);
+  const int64_t cap = final_cap();
+  s.left = (clip.known ? 0 : nt) + (scale ? nt : 0) + (final ? final_launches(clip, count, cap) : 0);
   if (!clip.known)
     for (int64_t k = 0; k < nt; ++k) {
       if (clip.each) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, true, true>, blocks[k], kThreads, tabs[k], partial)); }
       else if (!scale) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, true>, blocks[k], kThreads, tabs[k], partial)); }
       else { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, false>, blocks[k], kThreads, tabs[k], partial)); }
     }
-  if (final) launch_final(s, clip, firsts, partial, int(partials), joined);
+  if (final) launch_final(s, clip, firsts, cap, partial, int(partials), joined);
   if (scale) {
     Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, clip.known, final ? nullptr : clip.total};
     for (int64_t k = nt - 1; k >= 0; --k) {
@@ -1073,7 +1078,8 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   }
   const int64_t nt = int64_t(pl.tabs.size());
   const bool final = clip.each || !nt;  // otherwise the second pass joins the partials
-  s.left = 2 * nt + (final ? final_launches(clip, b.count) : 0);
+  const int64_t cap = final_cap();
+  s.left = 2 * nt + (final ? final_launches(clip, b.count, cap) : 0);
   for (int64_t k = 0; k < nt; ++k) {
 #define AR_REDUCE(DT_, EACH_) AR_KIND(clip.norm, launch_reduce<DT_, KIND, EACH_>(s, blocks[k], pl.tabs[k], partial))
     if (b.dtype == D_BF16) {
@@ -1083,7 +1089,7 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
     }
 #undef AR_REDUCE
   }
-  if (final) launch_final(s, clip, pl.firsts, partial, int(partials), joined);
+  if (final) launch_final(s, clip, pl.firsts, cap, partial, int(partials), joined);
   Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, nullptr, final ? nullptr : clip.total};
   for (int64_t k = 0; k < nt; ++k) {
     if (b.dtype == D_BF16) { AR_KIND(clip.norm, launch_spread<D_BF16, KIND>(s, blocks[k], pl.tabs[k], lim)); }

@@ -565,3 +565,65 @@ def test_offsets_past_32_bits():
     for b in (t, other):
         assert [float(v) for v in (b[0], b[1 << 31], b[1 << 32], b[-1])] == [0.5, 1.0, 2.0, 10.0]
         assert int((b != 0).sum()) == 4
+
+
+@pytest.mark.parametrize("collective", ["allreduce", "reduce_scatter"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("P", [1, 2, 3, 4, 5, 6, 7, 8, 9, 24, 40])
+def test_allreduce_clip_long(P, dtype, collective):
+    # past the sizes that are cut finer: items of 2048 elements and more, every batch of ranks
+    n = 300_011 if P <= 9 else 262_147
+    x = inputs.make(dtype, P, n, seed=P)
+    check_allreduce_clip([x], "avg" if P % 2 else "sum", "l2" if P % 3 else "max", collective, lambda N: N / 3, P % 2 * 3)
+
+
+@pytest.mark.parametrize("limit", [1, 3, 16_777_215])
+def test_own_norms_under_a_launch_limit(limit):
+    A, torch = lib(), torch_mod()
+    sizes = [(i * 977) % 5000 for i in range(300)]
+    host = [values(n, "fp32" if i % 3 else "bf16", i) for i, n in enumerate(sizes)]
+    want, each = og.norms(host, "l2")
+    dev = [on_gpu(b, i % 3)[0] for i, b in enumerate(host)]
+    hosts = [inputs.make("bf16", 5, n, seed=n) for n in (0, 40_000, 9000, 300_000, 7)]
+    ranks = [v for x in hosts for v, _ in ranks_on_gpu(x)]
+    sums = [og.combine(x, "avg").astype(np.float64) for x in hosts]
+    total, own = torch.empty((), device="cuda"), torch.empty(len(hosts), device="cuda")
+    old = A.ar_set_launch_blocks(limit)
+    try:
+        got, norms = A.grad_norm(dev, per_tensor=True)
+        A.ar_allreduce_clip(ranks, [x.shape[1] for x in hosts], 5, "bf16", "avg", "allreduce",
+                            A.make_clip("l2", 1.0, total=total, each=own), torch.cuda.current_stream())
+        torch.cuda.synchronize()
+    finally:
+        A.ar_set_launch_blocks(old)
+    assert close(float(got), want, U) and close(norms.cpu().numpy(), each, U)
+    assert close(own.cpu().numpy(), [og.norm_of(s, "l2") for s in sums], U)
+    norm = og.norm_of(np.array([og.norm_of(s, "l2") for s in sums]), "l2")
+    assert close(float(total), norm, U)
+    for k, (x, s) in enumerate(zip(hosts, sums)):
+        for p in range(5):
+            assert fits(host_bits(ranks[5 * k + p]), s * og.factor(norm, 1.0, 1e-6), True)
+
+
+def test_known_norm_over_several_tables():
+    A, torch = lib(), torch_mod()
+    host = [values((i * 311) % 4000, TYPES[i % 2], i) for i in range(400)]
+    dev = [on_gpu(b, i % 5)[0] for i, b in enumerate(host)]
+    out = [torch.empty(b.size, dtype=torch.bfloat16 if i % 3 else torch.float32, device="cuda") for i, b in enumerate(host)]
+    A.grad_clip(dev, 2.0, out=out, total_norm=torch.tensor([8.0], device="cuda"))
+    for b, o in zip(host, out):
+        assert fits(host_bits(o), og.widen(b) * og.factor(8.0, 2.0, 1e-6), o.dtype == torch.bfloat16)
+
+
+def test_an_earlier_calls_error_is_not_taken_for_this_ones():
+    import ctypes
+    A, torch = lib(), torch_mod()
+    hip = ctypes.CDLL("libamdhip64.so.7")
+    t = torch.full((100,), 2.0, device="cuda")
+    torch.cuda.synchronize()
+    assert hip.hipSetDevice(1000) != 0  # leaves an error for whoever asks for the thread's last one
+    table = A.marshal_grads([(t.data_ptr(), 0, 100, "fp32", "fp32")])
+    total = t.new_empty(())
+    A.ar_grad_norm(table, A.make_clip(total=total), torch.cuda.current_stream())
+    hip.hipGetLastError()
+    assert float(total) == 20.0

@@ -143,7 +143,9 @@ def test_torch_side_refuses_host_tensors():
     import torch
     t = torch.zeros(4)
     for call in (lambda: A.grad_norm([t]), lambda: A.grad_clip([t], 1.0), lambda: A.allreduce_clip([t, t.clone()], 1.0),
-                 lambda: A.allreduce_clip([], 1.0), lambda: A.allreduce_clip([[]], 1.0)):
+                 lambda: A.allreduce_clip([], 1.0), lambda: A.allreduce_clip([[]], 1.0),
+                 lambda: A.allreduce_clip([[t], [t, t]], 1.0), lambda: A.grad_clip([], 1.0, out=[t]),
+                 lambda: A.grad_clip([t], 1.0, out=[])):
         refused(call)
 
 
