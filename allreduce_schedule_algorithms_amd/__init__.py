@@ -152,12 +152,17 @@ class _Place:
     def floats(self, *shape):
         return self.torch.empty(shape, dtype=self.torch.float32, device="cuda")
 
-    def scratch(self, clip, workspace, need):
-        """Point clip at the caller's workspace, or at one of torch's (in a captured call: of the graph's own memory)."""
+    def scratch(self, clip, workspace, need, large=False):
+        """Point clip at the caller's workspace. Without one, the library's own serves a call that is not captured
+        (a few kB per stream, and no allocation here); otherwise need() bytes come from torch: in a captured call
+        from the graph's own memory, and where they grow with the gradient (large) from memory that torch reuses."""
         if workspace is None:
-            if not need:
+            if not large and not self.torch.cuda.is_current_stream_capturing():
                 return None
-            workspace = self.torch.empty(need, dtype=self.torch.uint8, device="cuda")
+            size = need()
+            if not size:
+                return None
+            workspace = self.torch.empty(size, dtype=self.torch.uint8, device="cuda")
         elif workspace.get_device() != self.index or not workspace.is_contiguous():
             raise _invalid("workspace must be a contiguous tensor on the gradients' device")
         clip.workspace, clip.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -169,15 +174,15 @@ def grad_norm(grads, norm="l2", per_tensor=False, stream=None, workspace=None):
 
     norm: "l2" or "max" (largest magnitude). per_tensor: return (norm, norms), norms holding
     every tensor's own. ``stream`` defaults to torch's current stream (results are ready on the
-    stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to scratch from torch's
-    allocator.
+    stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to the library's own or,
+    in a captured call, to memory of the graph.
     """
     table, index = _grads(grads)
     with _Place(index, stream) as at:
         total = at.floats()
         each = at.floats(table.count) if per_tensor else None
         clip = make_clip(norm, total=total, each=each)
-        workspace = at.scratch(clip, workspace, 0 if workspace is not None else ar_grad_workspace_bytes(table, clip))
+        workspace = at.scratch(clip, workspace, lambda: ar_grad_workspace_bytes(table, clip))
         ar_grad_norm(table, clip, at.stream)
     return (total, each) if per_tensor else total
 
@@ -198,7 +203,7 @@ def grad_clip(grads, max_norm, norm="l2", eps=1e-6, out=None, total_norm=None, s
             return total_norm
         total = at.floats()
         clip = make_clip(norm, max_norm, eps, total=total)
-        workspace = at.scratch(clip, workspace, 0 if workspace is not None else ar_grad_workspace_bytes(table, clip))
+        workspace = at.scratch(clip, workspace, lambda: ar_grad_workspace_bytes(table, clip))
         ar_grad_clip(table, clip, at.stream)
     return total
 
@@ -230,6 +235,7 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
     with _Place(index, stream) as at:
         total = at.floats()
         clip = make_clip(norm, max_norm, eps, total=total)
-        workspace = at.scratch(clip, workspace, 0 if workspace is not None else ar_allreduce_clip_workspace_bytes(*args, clip))
+        workspace = at.scratch(clip, workspace, lambda: ar_allreduce_clip_workspace_bytes(*args, clip),
+                               large=args[4] == Collective.AR_REDUCE_SCATTER)
         ar_allreduce_clip(array("Q", map(T.data_ptr, tensors)), *args, clip, at.stream)
     return total
