@@ -197,8 +197,9 @@ struct GradTab {
   int64_t n4[kTabTensors];         // elements << 2 | out is bf16 << 1 | data is bf16
   int32_t first[kTabTensors + 1];  // first work item of every tensor, from 0
   int32_t count;
-  int32_t at;   // place of this launch's first partial among the call's
-  int64_t per;  // elements per work item
+  int32_t at;     // place of this launch's first partial among the call's
+  int32_t item0;  // its first item among the call's
+  int64_t per;    // elements per work item
 };
 static_assert(sizeof(GradTab) <= 4000, "kernel arguments");
 
@@ -252,28 +253,27 @@ __device__ __forceinline__ GradItem grad_item(const GradTab& tab, int it) {
   return w;
 }
 
-// EACH: partials for every item (which the tensors' own norms are joined from), otherwise one for
-// every workgroup over all of its items. NT (a norm alone): the loads leave the cache in front of HBM to
+// A partial for every workgroup over all of its items, and (EACH) `own` ones for every item, which the
+// tensors' norms are joined from. NT (a norm alone): the loads leave the cache in front of HBM to
 // others, 990 M bf16 355 -> 326 us; a pass that a scaling follows leaves its last part there.
-template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTab tab, double* partial) {
-  Part<KIND> p;
+template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTab tab, double* partial, double* own) {
+  Part<KIND> p, all;
   for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
     const GradItem w = grad_item(tab, it);
     if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     else norm_item<KIND, D_FP32, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     if constexpr (EACH) {
-      put_waves(p, partial + int64_t(tab.at + it) * kWaves);
+      all.join(p.v);
+      put_waves(p, own + int64_t(tab.item0 + it) * kWaves);
       p = Part<KIND>();
     }
   }
-  if constexpr (!EACH) {
-    join_group<KIND, kThreads>(p);
-    if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = p.v;
-  }
+  if constexpr (EACH) p = all;
+  join_group<KIND, kThreads>(p);
+  if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = p.v;
 }
 
-// The call's norm (a call without tensors' own norms: the first table is empty), and the tensors' own: a
-// workgroup joins one tensor's partials, the one behind the last tensor all of them. `joined` is for a
+// The tensors' own norms, a workgroup to a tensor, and behind the last tensor the call's. `joined` is for a
 // pass that scales.
 constexpr int kFinalThreads = 512, kEachTensors = 900;
 struct EachTab {
@@ -281,13 +281,13 @@ struct EachTab {
   int32_t count;
 };
 
-template <int KIND> __global__ __launch_bounds__(kFinalThreads) void k_norm_final(EachTab tab, const double* partial, int all, double* joined, float* total, float* each) {
+template <int KIND> __global__ __launch_bounds__(kFinalThreads) void k_norm_final(EachTab tab, const double* partial, int count, const double* own, double* joined, float* total, float* each) {
   const int i = blockIdx.x;
   if (i < tab.count) {
-    const Part<KIND> p = join_partials<KIND, kFinalThreads>(partial + tab.first[i], tab.first[i + 1] - tab.first[i]);
+    const Part<KIND> p = join_partials<KIND, kFinalThreads>(own + tab.first[i], tab.first[i + 1] - tab.first[i]);
     if (threadIdx.x == 0) each[i] = float(p.norm());
   } else {
-    const Part<KIND> p = join_partials<KIND, kFinalThreads>(partial, all);
+    const Part<KIND> p = join_partials<KIND, kFinalThreads>(partial, count);
     if (threadIdx.x == 0) {
       *joined = p.v;
       if (total) *total = float(p.norm());
@@ -423,7 +423,8 @@ struct BucketTab {
   int64_t n[kTabBuckets];
   int32_t first[kTabBuckets + 1];  // first work item
   int32_t ipp[kTabBuckets];        // work items per part
-  int32_t count, P, stride, at;
+  int32_t count, P, stride;
+  int32_t at, item0;               // as in GradTab
   int32_t owners;                  // 1: part q belongs to rank q alone
   int64_t per;
   float div;                       // > 0: the sum is divided by it
@@ -566,9 +567,9 @@ template <int DT> constexpr int kPair = DT == D_BF16 ? 1 : 2;
 
 // KEEP: the sums stay for the second pass. Otherwise the second pass reads the ranks again.
 template <int DT, int KIND, int B, int M, bool EACH, bool KEEP>
-__global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, double* partial) {
+__global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, double* partial, double* own) {
   constexpr int V = DT == D_BF16 ? 8 : 4;
-  Part<KIND> p;
+  Part<KIND> p, all;
   for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
     const BucketItem w = bucket_item(tab, it);
     void* const* ptr = tab.p + w.b * tab.stride;
@@ -594,14 +595,14 @@ __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, doubl
       if constexpr (KEEP) put_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t, s);
     }
     if constexpr (EACH) {
-      put_waves(p, partial + int64_t(tab.at + it) * kWaves);
+      all.join(p.v);
+      put_waves(p, own + int64_t(tab.item0 + it) * kWaves);
       p = Part<KIND>();
     }
   }
-  if constexpr (!EACH) {
-    join_group<KIND, kThreads>(p);
-    if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = p.v;
-  }
+  if constexpr (EACH) p = all;
+  join_group<KIND, kThreads>(p);
+  if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = p.v;
 }
 
 // Items go in the first pass's order, workgroup by workgroup: the sums are read on the XCD that wrote
@@ -805,17 +806,30 @@ struct Sequence {
   }
 };
 
-// Workgroups of a launch with `items` of the call's `all` items. Their counts of items may differ by one:
-// as many workgroups on every compute unit matter more (7 x 2^24 fp32: 175 us with 1536 workgroups of 5
-// or 6 items, 184 with 1366 of 6).
-int64_t blocks_for(int64_t items, int64_t all) {
-  const int64_t most = most_blocks();
-  return std::max<int64_t>(1, std::min<int64_t>(all <= most ? items : pieces(items * most, all), launch_blocks()));
-}
-// Bytes of a call's partials: one per wave and item, or per workgroup (blocks_for rounds up once a launch).
+// Workgroups of a launch. Their counts of items may differ by one: as many workgroups on every compute
+// unit matter more (7 x 2^24 fp32: 175 us with 1536 workgroups of 5 or 6 items, 184 with 1366 of 6).
+int64_t blocks_for(int64_t items) { return std::max<int64_t>(1, std::min({items, most_blocks(), launch_blocks()})); }
+
+// Where a call's partials lie behind kHead: one per workgroup of its launches, then (each) one per wave and
+// item. The size is that of launches with all of their workgroups.
+struct Partials {
+  std::vector<int64_t> blocks;  // workgroups of every launch
+  int32_t count = 0;            // partials of workgroups
+};
 size_t partial_bytes(int64_t items, int64_t launches, bool each) {
-  return round_up(size_t(each ? items * kWaves : std::min(items, most_blocks() + launches)) * sizeof(double));
+  return round_up(size_t(std::min(items, launches * most_blocks()) + (each ? items * kWaves : 0)) * sizeof(double));
 }
+template <typename TAB> Partials place_partials(std::vector<TAB>& tabs) {
+  Partials r;
+  for (TAB& t : tabs) {
+    r.blocks.push_back(blocks_for(t.first[t.count]));
+    t.at = r.count;
+    r.count += int32_t(r.blocks.back());
+  }
+  return r;
+}
+// Whether a pass that scales is to join this many partials in every workgroup: two launches' worth of them.
+bool few_partials(int64_t count) { return count <= 2 * most_blocks(); }
 
 #define AR_KIND(kind, ...)                                   \
   if ((kind) == N_L2) { constexpr int KIND = N_L2; __VA_ARGS__; } \
@@ -824,14 +838,14 @@ size_t partial_bytes(int64_t items, int64_t launches, bool each) {
 // The norm of the call, and every tensor's or bucket's own before it (clip.each; firsts: their first items).
 int64_t final_cap() { return std::min<int64_t>(kEachTensors, launch_blocks()); }
 int64_t final_launches(const Clip& clip, int64_t count, int64_t cap) { return pieces((clip.each ? count : 0) + 1, cap); }
-void launch_final(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, int64_t cap, const double* partial, int partials, double* joined) {
+void launch_final(Sequence& s, const Clip& clip, const std::vector<int32_t>& firsts, int64_t cap, const double* partial, int partials, const double* own, double* joined) {
   const int64_t count = clip.each ? int64_t(firsts.size()) - 1 : 0;
   for (int64_t i0 = 0; i0 <= count; i0 += cap) {
     EachTab tab;
     const int64_t blocks = std::min(cap, count + 1 - i0);
     tab.count = int32_t(std::min(cap, count - i0));
     for (int k = 0; k <= tab.count; ++k) tab.first[k] = firsts[size_t(i0 + k)] * kWaves;
-    AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, blocks, kFinalThreads, tab, partial, partials, joined, clip.total, clip.each + i0));
+    AR_KIND(clip.norm, s.launch(k_norm_final<KIND>, blocks, kFinalThreads, tab, partial, partials, own, joined, clip.total, clip.each + i0));
   }
 }
 
@@ -866,7 +880,7 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
     GradTab tab;
     std::memset(&tab, 0, sizeof(tab));
     tab.count = int32_t(std::min<int64_t>(kTabTensors, count - i0));
-    tab.at = firsts.back();
+    tab.item0 = firsts.back();
     tab.per = per;
     for (int k = 0; k < tab.count; ++k) {
       const Grad& t = g[i0 + k];
@@ -874,7 +888,7 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
       tab.dst[k] = t.out;
       tab.n4[k] = (t.n << 2) | (t.out_dtype == D_BF16 ? 2 : 0) | (t.dtype == D_BF16 ? 1 : 0);
       tab.first[k + 1] = tab.first[k] + int32_t(pieces(t.n, per));
-      firsts.push_back(tab.at + tab.first[k + 1]);
+      firsts.push_back(tab.item0 + tab.first[k + 1]);
     }
     if (tab.first[tab.count] || count <= kTabTensors) tabs.push_back(tab);
   }
@@ -890,14 +904,7 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
     else { AR_KIND(clip.norm, s.launch(k_grad_small<KIND, false>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
     return s.done();
   }
-  std::vector<int64_t> blocks;
-  int32_t partials = clip.each ? items * kWaves : 0;
-  for (GradTab& t : tabs) {
-    blocks.push_back(blocks_for(t.first[t.count], items));
-    if (clip.each) continue;
-    t.at = partials;
-    partials += int32_t(blocks.back());
-  }
+  const Partials parts = place_partials(tabs);
   std::unique_lock<std::mutex> lk;
   char* ws = nullptr;
   if (!clip.known) {
@@ -906,21 +913,22 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
   }
   double* joined = reinterpret_cast<double*>(ws);
   double* partial = reinterpret_cast<double*>(ws + kHead);
+  double* own = partial + parts.count;
   const int64_t nt = int64_t(tabs.size());
-  const bool final = !clip.known && (!scale || clip.each || !nt);  // otherwise the scaling pass joins the partials
+  const bool final = !clip.known && (!scale || clip.each || !nt || !few_partials(parts.count));  // otherwise the scaling pass joins them
   const int64_t cap = final_cap();
   s.left = (clip.known ? 0 : nt) + (scale ? nt : 0) + (final ? final_launches(clip, count, cap) : 0);
   if (!clip.known)
     for (int64_t k = 0; k < nt; ++k) {
-      if (clip.each) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, true, true>, blocks[k], kThreads, tabs[k], partial)); }
-      else if (!scale) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, true>, blocks[k], kThreads, tabs[k], partial)); }
-      else { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, false>, blocks[k], kThreads, tabs[k], partial)); }
+      if (clip.each) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, true, true>, parts.blocks[k], kThreads, tabs[k], partial, own)); }
+      else if (!scale) { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, true>, parts.blocks[k], kThreads, tabs[k], partial, own)); }
+      else { AR_KIND(clip.norm, s.launch(k_grad_norm<KIND, false, false>, parts.blocks[k], kThreads, tabs[k], partial, own)); }
     }
-  if (final) launch_final(s, clip, firsts, cap, partial, int(partials), joined);
+  if (final) launch_final(s, clip, firsts, cap, partial, parts.count, own, joined);
   if (scale) {
-    Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, clip.known, final ? nullptr : clip.total};
+    Limit lim{final ? joined : partial, final ? 1 : parts.count, clip.max_norm, clip.eps, clip.known, final ? nullptr : clip.total};
     for (int64_t k = nt - 1; k >= 0; --k) {
-      AR_KIND(clip.norm, s.launch(k_grad_scale<KIND>, blocks[k], kThreads, tabs[k], lim));
+      AR_KIND(clip.norm, s.launch(k_grad_scale<KIND>, parts.blocks[k], kThreads, tabs[k], lim));
       lim.total = nullptr;
     }
   }
@@ -940,13 +948,13 @@ constexpr int64_t kFineUnit = 512, kFineTotal = int64_t(1) << 18;
 // 105 and 89, 4 ranks 121 and 119, and for the reduce-scatter 92 and 94.
 constexpr int32_t most_reread(int dtype) { return dtype == D_BF16 ? 3 : 2; }
 
-template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int64_t blocks, const BucketTab& t, double* partial) {
-#define AR_REDUCE_B(B_) s.launch(k_bucket_reduce<DT, KIND, B_, kPair<DT>, EACH, true>, blocks, kThreads, t, partial)
+template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int64_t blocks, const BucketTab& t, double* partial, double* own) {
+#define AR_REDUCE_B(B_) s.launch(k_bucket_reduce<DT, KIND, B_, kPair<DT>, EACH, true>, blocks, kThreads, t, partial, own)
   if (t.P <= most_reread(DT)) {
     switch (t.P) {
-      case 1: s.launch(k_bucket_reduce<DT, KIND, 1, kPair<DT>, EACH, false>, blocks, kThreads, t, partial); break;
-      case 2: s.launch(k_bucket_reduce<DT, KIND, 2, kPair<DT>, EACH, false>, blocks, kThreads, t, partial); break;
-      default: if constexpr (DT == D_BF16) s.launch(k_bucket_reduce<DT, KIND, 3, kPair<DT>, EACH, false>, blocks, kThreads, t, partial);
+      case 1: s.launch(k_bucket_reduce<DT, KIND, 1, kPair<DT>, EACH, false>, blocks, kThreads, t, partial, own); break;
+      case 2: s.launch(k_bucket_reduce<DT, KIND, 2, kPair<DT>, EACH, false>, blocks, kThreads, t, partial, own); break;
+      default: if constexpr (DT == D_BF16) s.launch(k_bucket_reduce<DT, KIND, 3, kPair<DT>, EACH, false>, blocks, kThreads, t, partial, own);
     }
     return;
   }
@@ -956,7 +964,7 @@ template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int64_t b
     case 5: AR_REDUCE_B(5); break;
     case 6: AR_REDUCE_B(6); break;
     case 7: AR_REDUCE_B(7); break;
-    case 16: s.launch(k_bucket_reduce<DT, KIND, 16, 1, EACH, true>, blocks, kThreads, t, partial); break;
+    case 16: s.launch(k_bucket_reduce<DT, KIND, 16, 1, EACH, true>, blocks, kThreads, t, partial, own); break;
     default: AR_REDUCE_B(8); break;
   }
 #undef AR_REDUCE_B
@@ -996,7 +1004,7 @@ BucketPlan plan_buckets(const Buckets& b, int64_t per) {
     tab.count = int32_t(std::min(fit, b.count - i0));
     tab.P = b.P;
     tab.stride = stride;
-    tab.at = pl.firsts.back();
+    tab.item0 = pl.firsts.back();
     tab.owners = scatter;
     tab.per = per;
     tab.div = b.op == O_AVG ? float(b.P) : 0.0f;
@@ -1013,7 +1021,7 @@ BucketPlan plan_buckets(const Buckets& b, int64_t per) {
         tab.low[k] = static_cast<uint16_t*>(tab.p[k * stride + 1]);
       }
       tab.first[k + 1] = tab.first[k] + (n ? tab.ipp[k] * (scatter ? b.P : 1) : 0);
-      pl.firsts.push_back(tab.at + tab.first[k + 1]);
+      pl.firsts.push_back(tab.item0 + tab.first[k + 1]);
     }
     if (tab.first[tab.count] || b.count <= fit) pl.tabs.push_back(tab);
   }
@@ -1048,7 +1056,6 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   bool small;
   BucketPlan pl = plan_call(b, clip.each, &small);
-  const int32_t items = pl.firsts.back();
   Sequence s{st, {reinterpret_cast<hipEvent_t>(clip.start_event), reinterpret_cast<hipEvent_t>(clip.stop_event)}, 0};
   if (small) {
     BucketTab none;
@@ -1065,23 +1072,18 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
   if (r.status) return r;
   double* joined = reinterpret_cast<double*>(ws);
   double* partial = reinterpret_cast<double*>(ws + kHead);
-  std::vector<int64_t> blocks;
-  int32_t partials = clip.each ? items * kWaves : 0;
+  const Partials parts = place_partials(pl.tabs);
+  double* own = partial + parts.count;
   char* low = ws + low_offset(pl, clip.each);
-  for (BucketTab& t : pl.tabs) {
-    if (low_in_workspace(b))
-      for (int k = 0; k < t.count; ++k) t.low[k] = reinterpret_cast<uint16_t*>(low + reinterpret_cast<size_t>(t.low[k]));
-    blocks.push_back(blocks_for(t.first[t.count], items));
-    if (clip.each) continue;
-    t.at = partials;
-    partials += int32_t(blocks.back());
-  }
+  for (BucketTab& t : pl.tabs)
+    for (int k = 0; low_in_workspace(b) && k < t.count; ++k)
+      t.low[k] = reinterpret_cast<uint16_t*>(low + reinterpret_cast<size_t>(t.low[k]));
   const int64_t nt = int64_t(pl.tabs.size());
-  const bool final = clip.each || !nt;  // otherwise the second pass joins the partials
+  const bool final = clip.each || !nt || !few_partials(parts.count);  // otherwise the second pass joins them
   const int64_t cap = final_cap();
   s.left = 2 * nt + (final ? final_launches(clip, b.count, cap) : 0);
   for (int64_t k = 0; k < nt; ++k) {
-#define AR_REDUCE(DT_, EACH_) AR_KIND(clip.norm, launch_reduce<DT_, KIND, EACH_>(s, blocks[k], pl.tabs[k], partial))
+#define AR_REDUCE(DT_, EACH_) AR_KIND(clip.norm, launch_reduce<DT_, KIND, EACH_>(s, parts.blocks[k], pl.tabs[k], partial, own))
     if (b.dtype == D_BF16) {
       if (clip.each) { AR_REDUCE(D_BF16, true); } else { AR_REDUCE(D_BF16, false); }
     } else {
@@ -1089,11 +1091,11 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
     }
 #undef AR_REDUCE
   }
-  if (final) launch_final(s, clip, pl.firsts, cap, partial, int(partials), joined);
-  Limit lim{final ? joined : partial, final ? 1 : partials, clip.max_norm, clip.eps, nullptr, final ? nullptr : clip.total};
+  if (final) launch_final(s, clip, pl.firsts, cap, partial, parts.count, own, joined);
+  Limit lim{final ? joined : partial, final ? 1 : parts.count, clip.max_norm, clip.eps, nullptr, final ? nullptr : clip.total};
   for (int64_t k = 0; k < nt; ++k) {
-    if (b.dtype == D_BF16) { AR_KIND(clip.norm, launch_spread<D_BF16, KIND>(s, blocks[k], pl.tabs[k], lim)); }
-    else { AR_KIND(clip.norm, launch_spread<D_FP32, KIND>(s, blocks[k], pl.tabs[k], lim)); }
+    if (b.dtype == D_BF16) { AR_KIND(clip.norm, launch_spread<D_BF16, KIND>(s, parts.blocks[k], pl.tabs[k], lim)); }
+    else { AR_KIND(clip.norm, launch_spread<D_FP32, KIND>(s, parts.blocks[k], pl.tabs[k], lim)); }
     lim.total = nullptr;
   }
   return s.done();
