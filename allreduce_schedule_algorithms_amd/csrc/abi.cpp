@@ -444,14 +444,16 @@ ar_status ar_cache_stats_get(ar_cache_stats* out) {
 }
 
 ar_status ar_release_cached(void) {
-  ar::RunResult r = ar::grad_cache_wait();
-  if (!r.status) r = ar::release_cached();
-  if (r.status) {
-    t_hip = r.hip_error;
-    return fail(ar_status(r.status), r.message);
-  }
-  ar::grad_cache_free();
-  return AR_OK;
+  return guarded([]() -> ar_status {
+    ar::RunResult r = ar::grad_cache_wait();
+    if (!r.status) r = ar::release_cached();
+    if (r.status) {
+      t_hip = r.hip_error;
+      return fail(ar_status(r.status), r.message);
+    }
+    ar::grad_cache_free();
+    return AR_OK;
+  });
 }
 
 ar_status ar_schedule_build(const ar_call* call, ar_schedule** out) {

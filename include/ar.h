@@ -334,9 +334,9 @@ ar_status ar_set_launch_blocks(int64_t max_blocks, int64_t* previous);
  *           max_norm / (N + eps) otherwise
  *   y     = scale g, rounded once to y's type,
  * on tensors of fp32 and bf16, which one call may mix. A gradient within the limit keeps its bits.
- *  - Norms: squares are summed in 64 bits (in an order that the tensors' sizes fix), so no fp32 or
- *    bf16 value overflows or vanishes, and a call's result is the same on every run. The results
- *    are fp32. Infinities and NaN count as they are: the norm is then infinite or NaN, and
+ *  - Norms: squares are summed in 64 bits, so no fp32 or bf16 value overflows or vanishes, in an
+ *    order that the sizes, the device and ar_set_launch_blocks() fix, so a call gives the same bits
+ *    on every run. The results are fp32. Infinities and NaN count as they are: the norm is then infinite or NaN, and
  *    scaling by it gives 0 (0 times an infinity: NaN) or NaN. The caller tests the norm.
  *  - Stream, errors, capture: as for the Allreduce. These calls keep no plan and copy nothing to the
  *    device: the tensors' pointers and sizes travel as kernel arguments, so grads, bufs and n may

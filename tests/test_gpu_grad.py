@@ -627,3 +627,45 @@ def test_an_earlier_calls_error_is_not_taken_for_this_ones():
     A.ar_grad_norm(table, A.make_clip(total=total), torch.cuda.current_stream())
     hip.hipGetLastError()
     assert float(total) == 20.0
+
+
+@pytest.mark.parametrize("sizes", [[100, 0, 3, 2000], [100_003, 0, 40_000, 7], [1 + i % 900 for i in range(200)]], ids=["small", "large", "tables"])
+def test_clip_with_own_norms(sizes):
+    A, torch = lib(), torch_mod()
+    host = [values(n, TYPES[i % 2], i) for i, n in enumerate(sizes)]
+    norm, each = og.norms(host, "l2")
+    dev = [on_gpu(b)[0] for b in host]
+    total, own = torch.empty((), device="cuda"), torch.full((len(sizes) + 1,), -1.0, device="cuda")
+    table = A.marshal_grads([(t.data_ptr(), 0, t.numel(), d, d) for t, d in zip(dev, (TYPES[i % 2] for i in range(len(sizes))))])
+    A.ar_grad_clip(table, A.make_clip("l2", norm / 4, total=total, each=own), torch.cuda.current_stream())
+    assert close(float(total), norm, U) and close(own[:-1].cpu().numpy(), each, U) and float(own[-1]) == -1
+    for b, v in zip(host, dev):
+        assert fits(host_bits(v), og.widen(b) * og.factor(norm, norm / 4, 1e-6), b.dtype == np.uint16)
+
+
+@pytest.mark.parametrize("collective", ["allreduce", "reduce_scatter"])
+def test_own_norms_of_small_buckets(collective):
+    A, torch = lib(), torch_mod()
+    hosts = [inputs.make("fp32", 3, n, seed=n) for n in (5, 0, 130, 64)]
+    dev = [v for x in hosts for v, _ in ranks_on_gpu(x)]
+    total, own = torch.empty((), device="cuda"), torch.full((5,), -1.0, device="cuda")
+    args = ([5, 0, 130, 64], 3, "fp32", "sum", collective)
+    assert A.ar_allreduce_clip_workspace_bytes(*args, A.make_clip(max_norm=1.0, each=own)) == 0
+    A.ar_allreduce_clip(dev, *args, A.make_clip("l2", 1.0, total=total, each=own), torch.cuda.current_stream())
+    want = [og.norm_of(og.combine(x, "sum").astype(np.float64), "l2") for x in hosts]
+    assert close(own[:-1].cpu().numpy(), want, U) and float(own[-1]) == -1
+    assert close(float(total), og.norm_of(np.array(want), "l2"), U)
+
+
+def test_clip_of_many_launches():
+    """More partials than the scaling pass joins by itself: three tables and more, each with a full grid."""
+    A, torch = lib(), torch_mod()
+    sizes = [40_000 + i % 13 for i in range(600)]
+    flat = torch.randn(sum(sizes), device="cuda")
+    grads = list(flat.split(sizes))
+    exact = flat.double()
+    norm = float(exact.pow(2).sum().sqrt())
+    got = A.grad_clip(grads, norm / 3)
+    assert close(float(got), norm, U)
+    want = exact * og.factor(norm, norm / 3, 1e-6)
+    assert bool(((flat.double() - want).abs() <= 2 * U * SLACK * want.abs() + 2.0 ** -150).all())
