@@ -94,8 +94,14 @@ def _check_tensors(torch, tensors, what):
     return devices.pop(), types
 
 
-def _grads(tensors, out=None):
-    """(GradList, device index) of gradients, and of where they go."""
+def grad_list(tensors, out=None):
+    """GradList of gradients, and of where a clip puts them: built once, a caller that repeats calls on tensors
+    whose memory stays where it is passes it to grad_norm and grad_clip in place of the lists, which saves the
+    host about 0.25 us a tensor and call. It keeps the tensors alive."""
+    if isinstance(tensors, GradList):
+        if out is not None:
+            raise _invalid("a GradList holds its outputs already")
+        return tensors
     torch = _torch()
     tensors = list(tensors)
     count = len(tensors)
@@ -104,7 +110,7 @@ def _grads(tensors, out=None):
         if len(out) != count:
             raise _invalid(f"{count} gradients, and {len(out)} outputs")
     if not count:
-        return GradList((), 0), None
+        return GradList((), 0)
     T = torch.Tensor
     index, types = _check_tensors(torch, tensors, "gradients")
     words = [0] * (4 * count)
@@ -117,7 +123,7 @@ def _grads(tensors, out=None):
         words[1::4] = map(T.data_ptr, out)
         types = [d | k << 32 for d, k in zip(types, kinds)]
     words[3::4] = types
-    return GradList(words, count), index
+    return GradList(words, count, index, (tensors, out))
 
 
 class _Place:
@@ -170,15 +176,16 @@ class _Place:
 
 
 def grad_norm(grads, norm="l2", per_tensor=False, stream=None, workspace=None):
-    """Global norm of a list of contiguous float32 / bfloat16 CUDA tensors, as a 0-dim float32 tensor.
+    """Global norm of a list of contiguous float32 / bfloat16 CUDA tensors (or a grad_list of them), as a 0-dim
+    float32 tensor.
 
     norm: "l2" or "max" (largest magnitude). per_tensor: return (norm, norms), norms holding
     every tensor's own. ``stream`` defaults to torch's current stream (results are ready on the
     stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to the library's own or,
     in a captured call, to memory of the graph.
     """
-    table, index = _grads(grads)
-    with _Place(index, stream) as at:
+    table = grad_list(grads)
+    with _Place(table.index, stream) as at:
         total = at.floats()
         each = at.floats(table.count) if per_tensor else None
         clip = make_clip(norm, total=total, each=each)
@@ -194,8 +201,8 @@ def grad_clip(grads, max_norm, norm="l2", eps=1e-6, out=None, total_norm=None, s
     float32 or bfloat16). total_norm: a float32 CUDA tensor of one element that holds the norm
     already (of a gradient spread over several calls or ranks); the call then only scales.
     """
-    table, index = _grads(grads, out)
-    with _Place(index, stream) as at:
+    table = grad_list(grads, out)
+    with _Place(table.index, stream) as at:
         if total_norm is not None:
             if total_norm.dtype != at.torch.float32 or total_norm.numel() != 1 or total_norm.get_device() != at.index:
                 raise _invalid("total_norm must be a float32 tensor of one element on the gradients' device")

@@ -361,12 +361,14 @@ def ar_set_launch_blocks(max_blocks: int) -> int:
 
 # ---- gradient norms and clipping ----
 class GradList:
-    """Host table of ar_grad records. It holds addresses, so what owns the tensors' memory has to outlive its use."""
+    """Host table of ar_grad records. It holds addresses, so what owns the tensors' memory has to outlive its use;
+    `index` is the device they are on (None: the current one) and `tensors` what keeps them, where known."""
 
-    def __init__(self, words, count):
+    def __init__(self, words, count, index=None, tensors=None):
         self.words = array.array("Q", words)  # a record is four words: data, out, n, dtype | out_dtype << 32
         self.count = count
         self.address = self.words.buffer_info()[0]
+        self.index, self.tensors = index, tensors
 
 
 def marshal_grads(records) -> GradList:

@@ -669,3 +669,24 @@ def test_clip_of_many_launches():
     assert close(float(got), norm, U)
     want = exact * og.factor(norm, norm / 3, 1e-6)
     assert bool(((flat.double() - want).abs() <= 2 * U * SLACK * want.abs() + 2.0 ** -150).all())
+
+
+def test_a_list_built_once():
+    A, torch = lib(), torch_mod()
+    host = [values(n, TYPES[i % 2], i) for i, n in enumerate((5000, 0, 77, 200_001))]
+    norm, each = og.norms(host, "l2")
+    dev = [on_gpu(b, i)[0] for i, b in enumerate(host)]
+    out = [torch.empty(b.size, device="cuda") for b in host]
+    table = A.grad_list(dev, out)
+    with pytest.raises(A.ArError):
+        A.grad_clip(table, 1.0, out=out)
+    for _ in range(2):
+        total, own = A.grad_norm(table, per_tensor=True)
+        assert close(float(total), norm, U) and close(own.cpu().numpy(), each, U)
+        assert close(float(A.grad_clip(table, norm / 2)), norm, U)
+        for b, o in zip(host, out):
+            assert fits(host_bits(o), og.widen(b) * og.factor(norm, norm / 2, 1e-6), False)
+            o.zero_()
+    dev[0].mul_(2)  # the list reads what its tensors hold
+    host[0] = host_bits(dev[0])
+    assert close(float(A.grad_norm(table)), og.norms(host, "l2")[0], U)
