@@ -771,6 +771,11 @@ RunResult workspace_of(const Clip& clip, size_t need, hipStream_t st, std::uniqu
     *out = static_cast<char*>(clip.workspace);
     return r;
   }
+  if (st == hipStreamPerThread) {  // one handle for every thread's stream
+    r.status = 2;
+    r.message = "a call on hipStreamPerThread needs a workspace of its own (" + std::to_string(need) + " bytes)";
+    return r;
+  }
   // a captured call is replayed whenever its graph is, beside whatever else then uses this stream's
   // workspace: it has to bring one of its own
   hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;

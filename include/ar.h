@@ -345,7 +345,7 @@ ar_status ar_set_launch_blocks(int64_t max_blocks, int64_t* previous);
  *    bytes (0 for small calls), 16-byte aligned; its contents need no preparation. NULL: the library's
  *    own, one per (device, stream), kept like the literal workspaces; under stream capture a call that
  *    needs one then returns AR_UNSUPPORTED, since a graph replays beside whatever else uses the
- *    stream's workspace.
+ *    stream's workspace, and so does one on hipStreamPerThread, a handle that threads share.
  *  - Memory: any address that is a multiple of the element size. Tensors that a call writes must
  *    not overlap any other tensor of the call (AR_INVALID_ARGUMENT), nor total, each, known or the
  *    workspace (not checked). */

@@ -690,3 +690,19 @@ def test_a_list_built_once():
     dev[0].mul_(2)  # the list reads what its tensors hold
     host[0] = host_bits(dev[0])
     assert close(float(A.grad_norm(table)), og.norms(host, "l2")[0], U)
+
+
+def test_the_per_thread_stream_needs_a_workspace():
+    A, torch = lib(), torch_mod()
+    per_thread = 2  # hipStreamPerThread
+    t = torch.ones(1_000_000, device="cuda")
+    total = torch.zeros((), device="cuda")
+    table = A.grad_list([t])
+    torch.cuda.synchronize()
+    with pytest.raises(A.ArError) as e:
+        A.ar_grad_norm(table, A.make_clip(total=total), per_thread)
+    assert e.value.status == A.Status.AR_UNSUPPORTED
+    ws = torch.empty(A.ar_grad_workspace_bytes(table, A.make_clip()), dtype=torch.uint8, device="cuda")
+    A.ar_grad_norm(table, A.make_clip(total=total, workspace=ws, workspace_bytes=ws.numel()), per_thread)
+    torch.cuda.synchronize()
+    assert float(total) == 1000
