@@ -94,14 +94,6 @@ template <int DT> __device__ __forceinline__ void st_one(void* base, int64_t e, 
 // A partial norm: the sum of squares, or the largest magnitude, as a double.
 template <int KIND> struct Part {
   double v = 0;
-  __device__ __forceinline__ void add(float x) {
-    if constexpr (KIND == N_L2) {
-      const double d = double(x);
-      v = __builtin_fma(d, d, v);
-    } else {
-      join(double(as_f(as_u(x) & 0x7fffffffu)));
-    }
-  }
   __device__ __forceinline__ void join(double o) {
     if constexpr (KIND == N_L2) {
       v += o;
@@ -114,6 +106,23 @@ template <int KIND> struct Part {
     if constexpr (KIND == N_L2) return sqrt(v);
     else return v;
   }
+};
+
+// What a thread gathers over an item's elements: squares in 64 bits, or magnitudes as fp32 patterns, one
+// operation an element.
+template <int KIND> struct Gather;
+template <> struct Gather<N_L2> {
+  double v = 0;
+  __device__ __forceinline__ void add(float x) {
+    const double d = double(x);
+    v = __builtin_fma(d, d, v);
+  }
+  __device__ __forceinline__ double value() const { return v; }
+};
+template <> struct Gather<N_MAX> {
+  uint32_t m = 0;
+  __device__ __forceinline__ void add(float x) { m = max(m, as_u(x) & 0x7fffffffu); }
+  __device__ __forceinline__ double value() const { return double(as_f(m)); }
 };
 
 template <int KIND> __device__ __forceinline__ void join_wave(Part<KIND>& p) {  // valid in lane 0
@@ -219,7 +228,7 @@ template <typename TAB> __device__ __forceinline__ int find_first(const TAB& tab
 
 constexpr int kUnroll = 4;  // vectors of a thread in flight
 // L lanes (a workgroup's, or a wave's), of which this is `lane`, go over an item together.
-template <int KIND, int DT, int L, bool NT> __device__ __forceinline__ void norm_item(const void* src, int64_t e0, int cnt, int lane, Part<KIND>& p) {
+template <int KIND, int DT, int L, bool NT> __device__ __forceinline__ void norm_item(const void* src, int64_t e0, int cnt, int lane, Gather<KIND>& p) {
   constexpr int V = DT == D_BF16 ? 8 : 4;
   const int nv = cnt / V;
   int v = lane;
@@ -262,20 +271,21 @@ __device__ __forceinline__ GradItem grad_item(const GradTab& tab, int it) {
 // Bound by HBM reads: 238 us for 1.58 GB of bf16, 6.6 TB/s; 26 us for 143 MB of ragged fp32, 5.4 TB/s. A
 // thread's 4 vectors in flight and 24 waves to a compute unit cover the latency.
 template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTab tab, double* partial, double* own) {
-  Part<KIND> p, all;
+  Part<KIND> all;
+  Gather<KIND> p;
   for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
     const GradItem w = grad_item(tab, it);
     if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     else norm_item<KIND, D_FP32, kThreads, NT>(tab.src[w.i], w.e0, w.cnt, threadIdx.x, p);
     if constexpr (EACH) {
-      all.join(p.v);
-      put_waves(p, own + int64_t(tab.item0 + it) * kWaves);
-      p = Part<KIND>();
+      all.join(p.value());
+      put_waves(Part<KIND>{p.value()}, own + int64_t(tab.item0 + it) * kWaves);
+      p = Gather<KIND>();
     }
   }
-  if constexpr (EACH) p = all;
-  join_group<KIND, kThreads>(p);
-  if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = p.v;
+  if constexpr (!EACH) all.v = p.value();
+  join_group<KIND, kThreads>(all);
+  if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = all.v;
 }
 
 // The tensors' own norms, a workgroup to a tensor, and behind the last tensor the call's. `joined` is for a
@@ -384,9 +394,10 @@ __global__ __launch_bounds__(kSmallThreads) void k_grad_small(GradTab tab, float
   Part<KIND> p;
   for (int it = wave; it < items; it += kSmallWaves) {
     const GradItem w = grad_item(tab, it);
-    Part<KIND> q;
-    if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, 64, false>(tab.src[w.i], w.e0, w.cnt, lane, q);
-    else norm_item<KIND, D_FP32, 64, false>(tab.src[w.i], w.e0, w.cnt, lane, q);
+    Gather<KIND> g;
+    if (tab.n4[w.i] & 1) norm_item<KIND, D_BF16, 64, false>(tab.src[w.i], w.e0, w.cnt, lane, g);
+    else norm_item<KIND, D_FP32, 64, false>(tab.src[w.i], w.e0, w.cnt, lane, g);
+    Part<KIND> q{g.value()};
     p.join(q.v);
     if (each) {
       join_wave(q);
@@ -584,7 +595,8 @@ template <int DT> constexpr int kPair = DT == D_BF16 ? 1 : 2;
 template <int DT, int KIND, int B, int M, bool EACH, bool KEEP>
 __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, double* partial, double* own) {
   constexpr int V = DT == D_BF16 ? 8 : 4;
-  Part<KIND> p, all;
+  Part<KIND> all;
+  Gather<KIND> p;
   for (int it = blockIdx.x; it < tab.first[tab.count]; it += gridDim.x) {
     const BucketItem w = bucket_item(tab, it);
     void* const* ptr = tab.p + w.b * tab.stride;
@@ -610,14 +622,14 @@ __global__ __launch_bounds__(kThreads) void k_bucket_reduce(BucketTab tab, doubl
       if constexpr (KEEP) put_one<DT>(ptr[w.owner], tab.low[w.b], w.e0 + t, s);
     }
     if constexpr (EACH) {
-      all.join(p.v);
-      put_waves(p, own + int64_t(tab.item0 + it) * kWaves);
-      p = Part<KIND>();
+      all.join(p.value());
+      put_waves(Part<KIND>{p.value()}, own + int64_t(tab.item0 + it) * kWaves);
+      p = Gather<KIND>();
     }
   }
-  if constexpr (EACH) p = all;
-  join_group<KIND, kThreads>(p);
-  if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = p.v;
+  if constexpr (!EACH) all.v = p.value();
+  join_group<KIND, kThreads>(all);
+  if (threadIdx.x == 0) partial[tab.at + blockIdx.x] = all.v;
 }
 
 // Items go in the first pass's order, workgroup by workgroup: the sums are read on the XCD that wrote
@@ -687,7 +699,9 @@ __global__ __launch_bounds__(kSmallThreads) void k_bucket_small(BucketTab tab, f
   void* const* ptr = tab.p + w.b * tab.stride;
   if (lane < w.cnt) {
     sum = sum_one<DT>(ptr, tab.P, tab.div, w.e0 + lane);
-    p.add(sum);
+    Gather<KIND> g;
+    g.add(sum);
+    p.v = g.value();
   }
   if (each) {
     Part<KIND> q = p;
