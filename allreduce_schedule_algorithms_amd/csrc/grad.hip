@@ -226,18 +226,18 @@ template <typename TAB> __device__ __forceinline__ int find_first(const TAB& tab
   return lo;
 }
 
-constexpr int kUnroll = 4;  // vectors of a thread in flight
 // L lanes (a workgroup's, or a wave's), of which this is `lane`, go over an item together.
 template <int KIND, int DT, int L, bool NT> __device__ __forceinline__ void norm_item(const void* src, int64_t e0, int cnt, int lane, Gather<KIND>& p) {
   constexpr int V = DT == D_BF16 ? 8 : 4;
+  constexpr int U = L == 64 ? 4 : 2;  // vectors of a thread in flight; with 24 waves on a compute unit two do (990 M bf16: 303 us of 4, 298 of 2)
   const int nv = cnt / V;
   int v = lane;
-  for (; v + (kUnroll - 1) * L < nv; v += kUnroll * L) {
-    typename Raw<DT, V>::T r[kUnroll];
+  for (; v + (U - 1) * L < nv; v += U * L) {
+    typename Raw<DT, V>::T r[U];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) r[j] = ld_raw<DT, V, NT>(src, e0 + int64_t(v + j * L) * V);
+    for (int j = 0; j < U; ++j) r[j] = ld_raw<DT, V, NT>(src, e0 + int64_t(v + j * L) * V);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
+    for (int j = 0; j < U; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) p.add(value<DT, V>(r[j], i));
   }
@@ -268,8 +268,8 @@ __device__ __forceinline__ GradItem grad_item(const GradTab& tab, int it) {
 // tensors' norms are joined from. NT (a norm alone): the loads leave the cache in front of HBM to
 // others, 990 M bf16 355 -> 326 us; a pass that a scaling follows leaves its last part there.
 //
-// Bound by HBM reads: 238 us for 1.58 GB of bf16, 6.6 TB/s; 26 us for 143 MB of ragged fp32, 5.4 TB/s. A
-// thread's 4 vectors in flight and 24 waves to a compute unit cover the latency.
+// Bound by HBM reads: 234 us for 1.58 GB of bf16, 6.7 TB/s; 25 us for 143 MB of ragged fp32, 5.8 TB/s. 24
+// waves to a compute unit cover the latency.
 template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTab tab, double* partial, double* own) {
   Part<KIND> all;
   Gather<KIND> p;
@@ -313,14 +313,15 @@ template <int KIND> __global__ __launch_bounds__(kFinalThreads) void k_norm_fina
 template <int DS, int DD, int L> __device__ __forceinline__ void scale_item(const void* src, void* dst, int64_t e0, int cnt, int lane, Factor f) {
   // between the types, 4 elements a thread: its stores (or loads) then join its neighbours' to whole lines
   constexpr int V = DS == D_BF16 && DD == D_BF16 ? 8 : 4;
+  constexpr int U = 64 / sizeof(typename Raw<DS, V>::T);  // 64 bytes of a thread in flight (bf16 into fp32, 477 M: 671 us of 32 bytes, 658 of 64)
   const int nv = cnt / V;
   int v = lane;
-  for (; v + (kUnroll - 1) * L < nv; v += kUnroll * L) {
-    typename Raw<DS, V>::T r[kUnroll];
+  for (; v + (U - 1) * L < nv; v += U * L) {
+    typename Raw<DS, V>::T r[U];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) r[j] = ld_raw<DS, V, true>(src, e0 + int64_t(v + j * L) * V);
+    for (int j = 0; j < U; ++j) r[j] = ld_raw<DS, V, true>(src, e0 + int64_t(v + j * L) * V);
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
+    for (int j = 0; j < U; ++j) {
       float x[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) x[i] = f(value<DS, V>(r[j], i));
@@ -373,7 +374,7 @@ template <int KIND> __device__ __forceinline__ Factor factor_for(const Limit& li
 // with non-temporal ones, 193 backwards too; 187 M fp32: 452, 376, 375.
 __device__ __forceinline__ int last_item(int items) { return items - 1 - int((items - 1 - blockIdx.x) % gridDim.x); }
 
-// Bound by HBM, reads and writes together: 504 us for 477 M bf16 into fp32 (2.86 GB, 5.7 TB/s), 277 us for
+// Bound by HBM, reads and writes together: 502 us for 477 M bf16 into fp32 (2.86 GB, 5.7 TB/s), 279 us for
 // 187 M fp32 in place (1.50 GB, 5.4 TB/s); in place within the limit there is nothing to write, and the
 // clip of 187 M fp32 takes 137 us, as good as its norm.
 template <int KIND> __global__ __launch_bounds__(kThreads) void k_grad_scale(GradTab tab, Limit lim) {
