@@ -103,10 +103,10 @@ def grad_list(tensors, out=None):
             raise _invalid("a GradList holds its outputs already")
         return tensors
     torch = _torch()
-    tensors = list(tensors)
+    tensors = [tensors] if isinstance(tensors, torch.Tensor) else list(tensors)
     count = len(tensors)
     if out is not None:
-        out = list(out)
+        out = [out] if isinstance(out, torch.Tensor) else list(out)
         if len(out) != count:
             raise _invalid(f"{count} gradients, and {len(out)} outputs")
     if not count:
@@ -176,8 +176,8 @@ class _Place:
 
 
 def grad_norm(grads, norm="l2", per_tensor=False, stream=None, workspace=None):
-    """Global norm of a list of contiguous float32 / bfloat16 CUDA tensors (or a grad_list of them), as a 0-dim
-    float32 tensor.
+    """Global norm of a list of contiguous float32 / bfloat16 CUDA tensors (or a grad_list of them, or one tensor),
+    as a 0-dim float32 tensor.
 
     norm: "l2" or "max" (largest magnitude). per_tensor: return (norm, norms), norms holding
     every tensor's own. ``stream`` defaults to torch's current stream (results are ready on the

@@ -117,6 +117,15 @@ def test_norms(name, types, kind):
         assert bits == first and alone.cpu().numpy().tobytes() == bits[0]
 
 
+def test_one_tensor_is_a_list_of_one():
+    A, torch = lib(), torch_mod()
+    t = torch.full((30, 30), 2.0, device="cuda")
+    o = torch.empty_like(t, dtype=torch.bfloat16)
+    total, own = A.grad_norm(t, per_tensor=True)
+    assert float(total) == 60 and own.shape == (1,)
+    assert float(A.grad_clip(t, 30.0, eps=0.0, out=o)) == 60 and bool((o == 1).all()) and bool((t == 2).all())
+
+
 def test_no_tensors():
     A = lib()
     total, own = A.grad_norm([], per_tensor=True)
