@@ -745,12 +745,14 @@ int64_t most_blocks() { return 6 * int64_t(device_cus()); }
 
 // Work items hold a multiple of kItemUnit elements: enough of them that a workgroup's share is many (the
 // shares then end together, however the tensors' last items fall), at most kMaxItem elements apiece
-// where that many items are not too many to count.
+// where that many items are not too many to count. The kernels count an item's elements in an int: 2^30 is the
+// most (2^48 elements with their own norms, the longest call, are then 2^18 items and their tensors' ends).
 constexpr int64_t kItemUnit = 2048, kMaxItem = 16384, kShare = 8, kEachItems = 16384, kMostItems = int64_t(1) << 24;
+constexpr int64_t kLongestItem = int64_t(1) << 30;
 constexpr int64_t kPlainBlocks = 1536;  // the items' size follows the call alone, not the device
 int64_t item_size(int64_t total, bool each) {
   int64_t per = std::min(kMaxItem, total / (kPlainBlocks * kShare));
-  per = std::max(per, total / (each ? kEachItems : kMostItems));
+  per = std::min(kLongestItem, std::max(per, total / (each ? kEachItems : kMostItems)));
   return std::max<int64_t>(1, (per + kItemUnit - 1) / kItemUnit) * kItemUnit;
 }
 int64_t pieces(int64_t n, int64_t per) { return (n + per - 1) / per; }

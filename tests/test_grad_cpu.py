@@ -139,6 +139,18 @@ def test_workspace_bytes():
     assert A.ar_allreduce_clip_workspace_bytes([n, n], *args, "reduce_scatter", clip()) >= 2 * n * 2  # lower halves of the sums
 
 
+@pytest.mark.parametrize("total", [1 << 40, 1 << 46, 1 << 47, (1 << 48) - 1])
+def test_items_with_own_norms_stay_countable(total):
+    """A kernel counts an item's elements in 32 bits: a call has total / (2^31 - 1) items or more, and with own norms
+    each of them has four 8-byte partials."""
+    least = 4 * 8 * -(-total // (2 ** 31 - 1))
+    c = clip(each=BASE - 256)
+    assert A.ar_grad_workspace_bytes(grads((BASE, 0, total)), c) >= least
+    # the same memory several times over: a norm only reads it
+    assert A.ar_grad_workspace_bytes(grads(*[(BASE, 0, total // 1024)] * 1024), c) >= least * 1023 // 1024
+    assert A.ar_allreduce_clip_workspace_bytes([total], 2, "fp32", "sum", "allreduce", c) >= least
+
+
 def test_torch_side_refuses_host_tensors():
     import torch
     t = torch.zeros(4)
