@@ -176,7 +176,10 @@ template <int KIND, int THREADS> __device__ __forceinline__ Part<KIND> join_all(
 
 // The scale as a product a b of two fp32 values: one where it has fp32's full precision, and below
 // 2^-64 (a limit far under an exploding norm) two halves of its exponent, so that x a b is right for
-// every x and rounds once more only where the result has no 24 bits.
+// every x and rounds once more only where the result has no 24 bits. b stays at fp32's smallest value where
+// its half of the exponent lies below (scales under 2^-274: a denormal limit and a norm near fp32's end), a takes
+// the rest and keeps the few bits that a result there has; neither ever becomes zero, which would turn an
+// infinity into NaN.
 struct Factor {
   float a, b;
   __device__ __forceinline__ bool one() const { return a == 1.0f && b == 1.0f; }
@@ -189,8 +192,8 @@ __device__ __forceinline__ Factor factor_of(double norm, float max_norm, float e
   if (s > 0 && s < 0x1p-64) {
     int e;
     const double m = frexp(s, &e);
-    const int ea = max(e / 2, -125);
-    return {float(ldexp(m, ea)), float(ldexp(1.0, e - ea))};
+    const int eb = max(e - max(e / 2, -125), -149);
+    return {float(fmax(ldexp(m, e - eb), 0x1p-149)), float(ldexp(1.0, eb))};
   }
   return {float(s), 1.0f};
 }

@@ -227,6 +227,37 @@ def test_clip_by_a_known_norm(known):
             assert fits(host_bits(v), og.widen(b) * f, b.dtype == np.uint16)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value,max_norm", [(3e38, 1e-45), (1.7e38, 1e-45), (3.38e38, 3e-45), (3e38, 1e-38), (-2e38, 7e-45)])
+def test_the_smallest_scales(value, max_norm, dtype):
+    """One element past the limit becomes the limit, down to scales of 2^-277; the limit itself where that is a
+    few steps of 2^-149, of which the factors' roundings are a small part."""
+    A, torch = lib(), torch_mod()
+    t = torch.tensor([0.0, value, -0.0], dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for host in (host_bits(t), np.concatenate([host_bits(t)] + [np.zeros_like(host_bits(t))] * 20_000)):
+        norm, _ = og.norms([host], "l2")
+        f = og.factor(norm, max_norm, 0.0)
+        out = torch.zeros(host.size, device="cuda")
+        view, _ = on_gpu(host)
+        A.grad_clip([view], max_norm, eps=0.0, out=[out])
+        assert fits(host_bits(out), og.widen(host) * f, False)
+        assert max_norm > 1e-40 or float(out[1]) == math.copysign(float(np.float32(max_norm)), value)
+        A.grad_clip([view], max_norm, eps=0.0)
+        assert fits(host_bits(view), og.widen(host) * f, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_an_infinity_by_a_known_norm_and_the_smallest_scale(dtype):
+    A, torch = lib(), torch_mod()
+    t = torch.tensor([math.inf, 1.0, -math.inf, math.nan, 3e38], dtype=torch.bfloat16 if dtype == "bf16" else torch.float32, device="cuda")
+    known = torch.tensor([3e38], device="cuda")
+    for max_norm in (1e-45, 1e-30, 1.0):
+        f = og.factor(float(known), max_norm, 1e-6)
+        got, want = t.clone(), og.widen(host_bits(t)) * f
+        A.grad_clip([got], max_norm, total_norm=known)
+        assert fits(host_bits(got), want, dtype == "bf16")
+
+
 # ---- the Allreduce that clips ----
 def ranks_on_gpu(x, offset=0):
     """One view per rank, rank p `offset + p` elements (mod 8) into its allocation where offset is not 0."""
