@@ -199,7 +199,8 @@ def grad_clip(grads, max_norm, norm="l2", eps=1e-6, out=None, total_norm=None, s
 
     scale = min(1, max_norm / (norm + eps)); in place, or into the tensors of ``out`` (same sizes,
     float32 or bfloat16). total_norm: a float32 CUDA tensor of one element that holds the norm
-    already (of a gradient spread over several calls or ranks); the call then only scales.
+    already (of a gradient spread over several calls or ranks), apart from what the call writes; the call then
+    only scales.
     """
     table = grad_list(grads, out)
     with _Place(table.index, stream) as at:

@@ -192,6 +192,17 @@ ar_status check_grads(const ar_grad* g, int32_t count, bool scale, std::vector<a
   return AR_OK;
 }
 
+// A known norm is read by every workgroup of a call that writes: it may not lie in what the call writes.
+ar_status check_known(const float* known, const std::vector<ar::Grad>& g) {
+  const uintptr_t k = reinterpret_cast<uintptr_t>(known);
+  for (size_t i = 0; i < g.size(); ++i) {
+    const uintptr_t o = reinterpret_cast<uintptr_t>(g[i].out);
+    if (g[i].n && k < o + uintptr_t(g[i].n * float_bytes(g[i].out_dtype)) && o < k + sizeof(float))
+      return fail(AR_INVALID_ARGUMENT, "known lies in tensor " + std::to_string(i) + "'s result");
+  }
+  return AR_OK;
+}
+
 ar_status check_buckets(void* const* bufs, bool with_bufs, const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
                         int32_t op, int32_t collective, ar::Buckets* out) {
   if (P < 1 || P > AR_MAX_RANKS) return fail(AR_INVALID_ARGUMENT, "P must be in [1, " + std::to_string(AR_MAX_RANKS) + "]");
@@ -245,6 +256,7 @@ ar_status grad_call(const ar_grad* grads, int32_t count, const ar_clip* clip, bo
   if (st == AR_OK && c.known && (c.total || c.each)) st = fail(AR_INVALID_ARGUMENT, "with known, total and each must be NULL");
   if (st == AR_OK && !scale && !bytes && !c.total) st = fail(AR_INVALID_ARGUMENT, "total is NULL");
   if (st == AR_OK) st = check_grads(grads, count, scale, &g);
+  if (st == AR_OK && c.known) st = check_known(c.known, g);
   if (st != AR_OK) return st;
   if (bytes) {
     *bytes = ar::grad_workspace(g.data(), int64_t(g.size()), c);

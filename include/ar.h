@@ -347,7 +347,7 @@ ar_status ar_set_launch_blocks(int64_t max_blocks, int64_t* previous);
  *    needs one then returns AR_UNSUPPORTED, since a graph replays beside whatever else uses the
  *    stream's workspace, and so does one on hipStreamPerThread, a handle that threads share.
  *  - Memory: any address that is a multiple of the element size. Tensors that a call writes must
- *    not overlap any other tensor of the call (AR_INVALID_ARGUMENT), nor total, each, known or the
+ *    not overlap any other tensor of the call, nor known (AR_INVALID_ARGUMENT), nor total, each or the
  *    workspace (not checked). */
 typedef enum { AR_NORM_L2 = 0, AR_NORM_MAX = 1 } ar_norm; /* 2-norm; largest magnitude */
 

@@ -83,6 +83,22 @@ def test_overlapping_tensors():
     assert "overlap" in refused(lambda: A.ar_grad_clip(grads((BASE, BASE + 8192, 100), (BASE + 4096, BASE + 8192, 100)), clip()))
 
 
+@pytest.mark.parametrize("known", [BASE, BASE + 4, BASE + 396])
+def test_a_known_norm_may_not_lie_in_what_is_written(known):
+    c = clip(known=known, total=None)
+    for rec in (GOOD, (BASE, BASE, 100), (BASE + 8192, BASE, 100), (BASE + 8192, BASE, 200, "fp32", "bf16")):
+        for records in ([rec], [(BASE + 4096, 0, 0), (BASE + 16384, 0, 7), rec]):
+            assert "known" in refused(lambda: A.ar_grad_clip(grads(*records), c))
+            assert "known" in refused(lambda: A.ar_grad_workspace_bytes(grads(*records), c))
+
+
+@pytest.mark.parametrize("known", [BASE - 4, BASE + 400, BASE + 8192])
+def test_a_known_norm_beside_what_is_written(known):
+    # one in front, one behind, and one in a gradient that the call only reads
+    empty = (BASE, known + 2, 0, "fp32", "bf16")
+    assert A.ar_grad_workspace_bytes(grads((BASE + 8192, BASE, 100), empty), clip(known=known, total=None)) == 0
+
+
 def test_counts():
     assert "count" in refused(lambda: A._ar._check(A._ar.lib.ar_grad_norm(None, -1, clip(), None)))
     assert "count" in refused(lambda: A._ar._check(A._ar.lib.ar_grad_norm(BASE, A.AR_MAX_GRADS + 1, clip(), None)))
