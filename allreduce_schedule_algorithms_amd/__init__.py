@@ -7,6 +7,7 @@ has no CPU fallback and fails loudly when the library is missing.
 from __future__ import annotations
 
 from array import array
+from operator import or_
 
 from . import _ar
 from ._ar import (  # noqa: F401
@@ -94,6 +95,12 @@ def _check_tensors(torch, tensors, what):
     return devices.pop(), types
 
 
+def _written(torch, tensors):
+    """The kernels write through addresses: autograd, which refuses a backward pass over a saved tensor that has
+    changed, learns of it here (about 50 ns a tensor)."""
+    torch._C._increment_version(tensors)
+
+
 def grad_list(tensors, out=None):
     """GradList of gradients, and of where a clip puts them: built once, a caller that repeats calls on tensors
     whose memory stays where it is passes it to grad_norm and grad_clip in place of the lists, which saves the
@@ -121,7 +128,7 @@ def grad_list(tensors, out=None):
         if there != index or list(map(T.numel, out)) != sizes:
             raise _invalid("every output must be of its gradient's size, on its device")
         words[1::4] = map(T.data_ptr, out)
-        types = [d | k << 32 for d, k in zip(types, kinds)]
+        types = map(or_, types, map((1 << 32).__mul__, kinds))
     words[3::4] = types
     return GradList(words, count, index, (tensors, out))
 
@@ -131,8 +138,7 @@ class _Place:
 
     def __init__(self, index, stream):
         self.torch = torch = _torch()
-        torch.cuda.init()
-        current = torch.cuda.current_device()
+        current = torch.cuda.current_device()  # initializes CUDA where nothing has yet
         self.index = index = current if index is None else index
         self.guards = () if index == current else (torch.cuda.device(index),)
         self.stream = torch._C._cuda_getCurrentRawStream(index)
@@ -180,7 +186,7 @@ def grad_norm(grads, norm="l2", per_tensor=False, stream=None, workspace=None):
     as a 0-dim float32 tensor.
 
     norm: "l2" or "max" (largest magnitude). per_tensor: return (norm, norms), norms holding
-    every tensor's own. ``stream`` defaults to torch's current stream (results are ready on the
+    every tensor's own. Norms carry no gradient. ``stream`` defaults to torch's current stream (results are ready on the
     stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to the library's own or,
     in a captured call, to memory of the graph.
     """
@@ -207,12 +213,16 @@ def grad_clip(grads, max_norm, norm="l2", eps=1e-6, out=None, total_norm=None, s
         if total_norm is not None:
             if total_norm.dtype != at.torch.float32 or total_norm.numel() != 1 or total_norm.get_device() != at.index:
                 raise _invalid("total_norm must be a float32 tensor of one element on the gradients' device")
-            ar_grad_clip(table, make_clip(norm, max_norm, eps, known=total_norm), at.stream)
-            return total_norm
-        total = at.floats()
-        clip = make_clip(norm, max_norm, eps, total=total)
-        workspace = at.scratch(clip, workspace, lambda: ar_grad_workspace_bytes(table, clip))
-        ar_grad_clip(table, clip, at.stream)
+            total = total_norm
+            ar_grad_clip(table, make_clip(norm, max_norm, eps, known=total), at.stream)
+        else:
+            total = at.floats()
+            clip = make_clip(norm, max_norm, eps, total=total)
+            workspace = at.scratch(clip, workspace, lambda: ar_grad_workspace_bytes(table, clip))
+            ar_grad_clip(table, clip, at.stream)
+        if table.tensors:
+            grads, out = table.tensors
+            _written(at.torch, grads if out is None else out)
     return total
 
 
@@ -233,11 +243,11 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
     P = len(buckets[0]) if buckets else 0
     if not P or any(len(b) != P for b in buckets):
         raise _invalid("allreduce_clip needs buckets with a tensor of every rank")
-    tensors = [t for b in buckets for t in b]
+    tensors = buckets[0] if len(buckets) == 1 else [t for b in buckets for t in b]
     index, types = _check_tensors(torch, tensors, "the ranks' tensors")
     numels = list(map(T.numel, tensors))
     sizes = numels[::P]
-    if numels != [n for n in sizes for _ in range(P)] or len(set(types)) != 1:
+    if numels != (sizes * P if len(sizes) == 1 else [n for n in sizes for _ in range(P)]) or len(set(types)) != 1:
         raise _invalid("a bucket's tensors must be of one size, and all tensors of one dtype")
     args = sizes, P, types[0], _ar._enum(OPS, op), _ar._enum(COLLECTIVES, collective)
     with _Place(index, stream) as at:
@@ -246,4 +256,5 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
         workspace = at.scratch(clip, workspace, lambda: ar_allreduce_clip_workspace_bytes(*args, clip),
                                large=args[4] == Collective.AR_REDUCE_SCATTER)
         ar_allreduce_clip(array("Q", map(T.data_ptr, tensors)), *args, clip, at.stream)
+        _written(torch, tensors)
     return total

@@ -746,3 +746,35 @@ def test_the_per_thread_stream_needs_a_workspace():
     A.ar_grad_norm(table, A.make_clip(total=total, workspace=ws, workspace_bytes=ws.numel()), per_thread)
     torch.cuda.synchronize()
     assert float(total) == 1000
+
+
+@pytest.mark.parametrize("call", ["in_place", "out", "known", "list", "allreduce", "reduce_scatter", "buckets"])
+def test_autograd_sees_what_is_written(call):
+    """A tensor that autograd saved may not change before its backward pass: writing to it has to be seen."""
+    A, torch = lib(), torch_mod()
+    g, o = torch.ones(5000, device="cuda"), torch.ones(5000, device="cuda")
+    other = torch.ones(5000, device="cuda")
+    w = torch.ones(5000, device="cuda", requires_grad=True)
+    known = torch.tensor(50.0, device="cuda")
+    read, written = (g, o) if call == "out" else (other, g)
+    kept, lost = (w * read).sum(), (w * written).sum()
+    version = read._version
+    {"in_place": lambda: A.grad_clip([g], 1.0), "out": lambda: A.grad_clip([g], 1.0, out=[o]),
+     "known": lambda: A.grad_clip([g], 1.0, total_norm=known), "list": lambda: A.grad_clip(A.grad_list([g]), 1.0),
+     "allreduce": lambda: A.allreduce_clip([g, o], 1.0), "buckets": lambda: A.allreduce_clip([[o], [g]], 1.0),
+     "reduce_scatter": lambda: A.allreduce_clip((g, o), 1.0, collective="reduce_scatter")}[call]()
+    A.grad_norm([g, o, other])  # reads
+    assert read._version == version and known._version == 0
+    kept.backward()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        lost.backward()
+
+
+def test_clipping_without_a_version_count():
+    """Tensors made in inference mode have none."""
+    A, torch = lib(), torch_mod()
+    with torch.inference_mode():
+        t = torch.full((3000,), 2.0, device="cuda")
+        A.grad_clip([t], 1e9)
+    A.grad_clip([t], math.sqrt(3000.0), eps=0.0)
+    assert close(t.cpu().numpy(), np.full(3000, 1.0), 2 * U + U * U)
