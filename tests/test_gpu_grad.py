@@ -778,3 +778,107 @@ def test_clipping_without_a_version_count():
         A.grad_clip([t], 1e9)
     A.grad_clip([t], math.sqrt(3000.0), eps=0.0)
     assert close(t.cpu().numpy(), np.full(3000, 1.0), 2 * U + U * U)
+
+
+@pytest.mark.parametrize("collective", ["allreduce", "reduce_scatter"])
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("P", [1, 2, 3, 4, 7, 8, 9, 17, 33])
+def test_own_norms_of_long_buckets(P, dtype, kind, collective):
+    """Past the sizes that are cut finer, with rank counts that fill their last batch of loads and others."""
+    A, torch = lib(), torch_mod()
+    sizes = [0, 200_003, 9, 70_001, 0]
+    hosts = [inputs.make(dtype, P, n, seed=P + n) for n in sizes]
+    op = "avg" if P % 2 else "sum"
+    sums = [og.combine(x, op).astype(np.float64) for x in hosts]
+    own = [og.norm_of(s, kind) for s in sums]
+    norm = og.norm_of(np.array(own), kind)
+    dev = [ranks_on_gpu(x, P % 3) for x in hosts]
+    total, each = torch.full((), -1.0, device="cuda"), torch.full((len(sizes) + 1,), -1.0, device="cuda")
+    args = (sizes, P, dtype, op, collective)
+    clip = A.make_clip(kind, norm / 4, total=total, each=each)
+    ws = torch.empty(A.ar_allreduce_clip_workspace_bytes(*args, clip), dtype=torch.uint8, device="cuda")
+    clip.workspace, clip.workspace_bytes = ws.data_ptr(), ws.numel()
+    A.ar_allreduce_clip([v for d in dev for v, _ in d], *args, clip, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    assert close(float(total), norm, U) and close(each[:-1].cpu().numpy(), own, U) and float(each[-1]) == -1
+    f = og.factor(norm, norm / 4, 1e-6)
+    for x, d, s in zip(hosts, dev, sums):
+        n = x.shape[1]
+        part = -(-n // P)
+        for p, (view, big) in enumerate(d):
+            bits = host_bits(view)
+            lo, hi = (0, n) if collective == "allreduce" else (min(p * part, n), min((p + 1) * part, n))
+            assert fits(bits[lo:hi], s[lo:hi] * f, dtype == "bf16"), (p, n)
+            for a, b in ((0, lo), (hi, n)):
+                assert np.array_equal(bits[a:b].view(np.uint8), x[p, a:b].view(np.uint8))
+            assert margins_kept(big, (view.data_ptr() - big.data_ptr()) // view.element_size(), n)
+
+
+@pytest.mark.parametrize("collective", ["allreduce", "reduce_scatter"])
+@pytest.mark.parametrize("P,dtype", [(3, "fp32"), (2, "bf16"), (4, "bf16")])
+def test_allreduce_clip_of_many_launches(P, dtype, collective):
+    """More partials than the second pass joins by itself: a launch takes 16 buckets, and each has a full grid."""
+    A, torch = lib(), torch_mod()
+    sizes = [200_000 + i % 13 for i in range(50)]
+    ranks = torch.randn(P, sum(sizes), device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    start = ranks.clone()
+    buckets = [list(b) for b in zip(*(r.split(sizes) for r in ranks))]
+    total = start[0].float()
+    for p in range(1, P):
+        total = total + start[p].float()  # rank order, fp32
+    exact = total.double()
+    norm = float(exact.pow(2).sum().sqrt())
+    got = A.allreduce_clip(buckets, norm / 3, collective=collective)
+    assert close(float(got), norm, U)
+    want = exact * og.factor(norm, norm / 3, 1e-6)
+    bf16 = dtype == "bf16"
+    rel = (1 + 2 * U + U * U) * (1 + 2.0 ** -8) - 1 if bf16 else 2 * U + U * U
+    bound = SLACK * (rel * want.abs() + (2.0 ** -134 if bf16 else 2.0 ** -150))
+    rank = torch.cat([torch.arange(n, device="cuda") // -(-n // P) for n in sizes])
+    for p in range(P):
+        mine = (rank == p) | (collective == "allreduce")
+        assert bool((((ranks[p].double() - want).abs() <= bound) | ~mine).all())
+        assert bool(((ranks[p] == start[p]) | mine).all())
+
+
+@pytest.mark.parametrize("collective", ["allreduce", "reduce_scatter"])
+def test_kept_sums_past_32_bits(collective):
+    """Sums of more than 2^32 elements that lie between the passes, with bits in both halves."""
+    A, torch = lib(), torch_mod()
+    n, P = (1 << 32) + 12_345, 4
+    at = [0, (1 << 31) + 1, (1 << 32) + 3, n - 1]
+    ranks = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(P)]
+    for k, i in enumerate(at):  # 2^k (1 + 2^-8 + 2^-9): the upper half alone would round to 2^k
+        for r, v in zip(ranks, (1.0, 2.0 ** -8, 2.0 ** -9, 0.0)):
+            r[i] = v * 2.0 ** k
+    before = [[float(r[i]) for i in at] for r in ranks]
+    c = 1 + 2.0 ** -8 + 2.0 ** -9
+    norm = c * math.sqrt(1 + 4 + 16 + 64)
+    got = A.allreduce_clip(ranks, norm / 2, eps=0.0, collective=collective)
+    assert close(float(got), norm, U)
+    part = -(-n // P)
+    for p, r in enumerate(ranks):
+        for k, i in enumerate(at):
+            mine = collective == "allreduce" or i // part == p
+            # half of it, rounded up to the next bf16
+            assert float(r[i]) == ((1 + 2.0 ** -7) * 2.0 ** (k - 1) if mine else before[p][k]), (p, k)
+        assert int((r != 0).sum()) == sum(1 for k, i in enumerate(at) if float(r[i]) != 0)
+
+
+def test_many_empty_tensors_and_buckets():
+    A, torch = lib(), torch_mod()
+    none = [torch.empty(0, dtype=torch.bfloat16 if i % 2 else torch.float32, device="cuda") for i in range(129)]
+    for kind in ("l2", "max"):
+        total, each = A.grad_norm(none, norm=kind, per_tensor=True)
+        assert float(total) == 0 and each.tolist() == [0.0] * 129
+        assert float(A.grad_norm(none, norm=kind)) == 0 and float(A.grad_clip(none, 1.0, norm=kind)) == 0
+    assert float(A.grad_clip(none, 1.0, total_norm=torch.tensor(3.0, device="cuda"))) == 3
+    for P, buckets in ((256, 2), (256, 3), (5, 20)):
+        empty = [[torch.empty(0, device="cuda") for _ in range(P)] for _ in range(buckets)]
+        for collective in ("allreduce", "reduce_scatter"):
+            assert float(A.allreduce_clip(empty, 1.0, collective=collective)) == 0
+        total, each = torch.ones((), device="cuda"), torch.ones(buckets + 1, device="cuda")
+        A.ar_allreduce_clip([0] * (P * buckets), [0] * buckets, P, "fp32", "sum", "allreduce",
+                            A.make_clip("l2", 1.0, total=total, each=each), torch.cuda.current_stream())
+        assert float(total) == 0 and each.tolist() == [0.0] * buckets + [1.0]
