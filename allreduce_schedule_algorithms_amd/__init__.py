@@ -186,9 +186,9 @@ def grad_norm(grads, norm="l2", per_tensor=False, stream=None, workspace=None):
     as a 0-dim float32 tensor.
 
     norm: "l2" or "max" (largest magnitude). per_tensor: return (norm, norms), norms holding
-    every tensor's own. Norms carry no gradient. ``stream`` defaults to torch's current stream (results are ready on the
-    stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to the library's own or,
-    in a captured call, to memory of the graph.
+    every tensor's own. Norms carry no gradient. ``stream`` defaults to torch's current stream (results
+    are ready on the stream that is given), ``workspace`` (a tensor of ar_grad_workspace_bytes) to the
+    library's own or, in a captured call, to memory of the graph.
     """
     table = grad_list(grads)
     with _Place(table.index, stream) as at:
@@ -233,7 +233,8 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
     rank), all of one dtype (float32 or bfloat16); or one bucket's list of tensors. Ranks are combined
     in rank order, as ``allreduce(..., algo="direct")``; op "sum" or "avg". The norm (returned as a
     0-dim float32 tensor) is over all buckets, of the combined values before they are rounded;
-    the scaled values are rounded once. collective "reduce_scatter": rank q ends with its part.
+    scale and product are fp32 values, and a bf16 result is rounded from the product. collective
+    "reduce_scatter": rank q ends with its part.
     """
     torch = _torch()
     T = torch.Tensor

@@ -3,7 +3,7 @@
 //
 //   N     = sqrt(sum over every element of g^2), or the largest |g|
 //   scale = 1 where N + eps <= max_norm, else max_norm / (N + eps)
-//   y     = scale g, rounded once to y's type
+//   y     = scale g
 //
 // Every pass streams memory; the arithmetic per element is a widening, a
 // multiply-add in 64 bits and one multiplication. Tensors are cut into work items
@@ -11,6 +11,10 @@
 // partial norm at its own place, and whoever needs the norm joins the partials in
 // their order. Nothing is added atomically: the same sizes, device and launch limit
 // give the same bits, whatever runs beside the call and wherever the tensors lie.
+//
+// The scale is rounded from 64 bits to fp32, its product with g to fp32, and a bf16 y from that: each
+// element costs one fp32 multiplication (2^-23 in all, and 2^-8 more in bf16). A product in 64 bits would
+// save the middle rounding, a 2^-16th of bf16's own.
 //
 // Squares are summed in 64 bits: fp32 squares overflow from 1.8e19 on, and a sum
 // over 10^9 elements has no bits left in 24. Largest magnitudes compare the
@@ -268,10 +272,12 @@ __device__ __forceinline__ GradItem grad_item(const GradTab& tab, int it) {
 }
 
 // A partial for every workgroup over all of its items, and (EACH) `own` ones for every item, which the
-// tensors' norms are joined from. NT (a norm alone): the loads leave the cache in front of HBM to
-// others, 990 M bf16 355 -> 326 us; a pass that a scaling follows leaves its last part there.
+// tensors' norms are joined from. NT (a norm alone, and every EACH): the loads leave the cache in front of HBM
+// to others, 990 M bf16 355 -> 326 us; a pass that a scaling follows leaves its last part there. A clip that
+// asks for the tensors' own norms too has no such form: its passes over 187 M bf16 into bf16 take 58, 5 and
+// 137 us, without own norms 63 and 112.
 //
-// Bound by HBM reads: 234 us for 1.58 GB of bf16, 6.7 TB/s; 25 us for 143 MB of ragged fp32, 5.8 TB/s. 24
+// Bound by HBM reads: 234 us for 1.58 GB of bf16, 6.7 TB/s; 25 us for 143 MB of ragged fp32, 5.6 TB/s. 24
 // waves to a compute unit cover the latency.
 template <int KIND, bool EACH, bool NT> __global__ __launch_bounds__(kThreads) void k_grad_norm(GradTab tab, double* partial, double* own) {
   Part<KIND> all;
@@ -374,12 +380,12 @@ template <int KIND> __device__ __forceinline__ Factor factor_for(const Limit& li
 // The last item of a workgroup's share of `items`. The scaling pass begins there and goes backwards: what
 // the norm read last is still in the cache in front of HBM (256 MB), and neither the loads here nor the
 // stores displace it. Norm and scaling of 187 M bf16 into bf16: 242 us forwards with plain accesses, 205
-// with non-temporal ones, 193 backwards too; 187 M fp32: 452, 376, 375.
+// with non-temporal ones, 193 backwards too (175 with 64 bytes in flight); 187 M fp32: 452, 376, 375.
 __device__ __forceinline__ int last_item(int items) { return items - 1 - int((items - 1 - blockIdx.x) % gridDim.x); }
 
-// Bound by HBM, reads and writes together: 502 us for 477 M bf16 into fp32 (2.86 GB, 5.7 TB/s), 279 us for
+// Bound by HBM, reads and writes together: 501 us for 477 M bf16 into fp32 (2.86 GB, 5.7 TB/s), 280 us for
 // 187 M fp32 in place (1.50 GB, 5.4 TB/s); in place within the limit there is nothing to write, and the
-// clip of 187 M fp32 takes 137 us, as good as its norm.
+// clip of 187 M fp32 takes 129 us, 124 of them the norm's.
 template <int KIND> __global__ __launch_bounds__(kThreads) void k_grad_scale(GradTab tab, Limit lim) {
   const Factor f = factor_for<KIND>(lim);
   if (lim.in_place && f.one()) return;
@@ -441,7 +447,8 @@ __global__ __launch_bounds__(kSmallThreads) void k_grad_small(GradTab tab, float
 // 2 P + 2 in fp32, and of 2 P + 4 in bf16, whose fp32 sums take two each.
 // A bucket's pointers fill whole batches of kRankBatch, the last one again behind the last rank: a
 // batch's pointers are then one scalar load, and its ranks' loads go out together with no test between
-// them (the extra ones find their lines in the cache).
+// them. Most of the repeated loads find their lines in the cache, not all: of 400 MB of fp32, 9 ranks read
+// 444 (93 us, where 8 ranks take 79), 17 ranks 421 (83, 16 take 76) and 33 ranks 409 (75, 32 take 71).
 constexpr int kTabPtrs = 400, kTabBuckets = 16, kRankBatch = 16;
 struct BucketTab {
   void* p[kTabPtrs];               // `stride` pointers of every bucket
@@ -742,8 +749,10 @@ RunResult hip_fail(hipError_t e, const char* what) {
   return r;
 }
 
-// Workgroups of a pass over the whole call: 6 of 4 waves per compute unit. The passes' registers allow
-// 7, and a static share wants all of them resident: 2048 of them ran 4-6% longer than 1536.
+// Workgroups of a pass over the whole call: 6 of 4 waves per compute unit. A static share wants all of them
+// resident (2048 of them ran 4-6% longer than 1536), and most passes' registers allow 6 or more. The sums of fp32
+// are the exception: 7, 8 and more ranks allow 5 workgroups on a compute unit, with the buckets' own norms 4, 6
+// and 7 ranks allow 5, 8 and more 4. In such a pass over a full grid the others start when those have ended.
 int64_t most_blocks() { return 6 * int64_t(device_cus()); }
 
 // Work items hold a multiple of kItemUnit elements: enough of them that a workgroup's share is many (the
@@ -981,14 +990,15 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
 namespace {
 
 // Few elements are cut finer and, of many ranks, 16 loaded together: what such a call waits for is one
-// batch of loads after the other. us for a call: 127 ranks x 2250 fp32 35 -> 21, 24 x 60000 13.8 -> 11.0,
-// 192 x 65536 bf16 52 -> 32, 64 x 2^18 25 -> 21, 8 x 65536 fp32 9.4 -> 8.5; 8 x 2^19 fp32 would take
-// 12.5 for 12.1, and 192 x 2^20 bf16 150 for 143.
+// batch of loads after the other. us for a call in a graph, without and with that: 127 ranks x 2250 fp32
+// 29.3 and 22.8, 24 x 60000 11.5 and 10.3, 192 x 65536 bf16 40.9 and 28.0, 64 x 2^18 22.2 and 19.3, 8 x 65536
+// fp32 8.3 and 7.8; past the limit 8 x 2^19 fp32 12.5 and 13.1, 192 x 2^20 bf16 154 and 156.
 constexpr int64_t kFineUnit = 512, kFineTotal = int64_t(1) << 18;
 
 // Ranks that the second pass reads again rather than finding their sums (30 M elements a rank, kept
-// and read again, us): fp32 2 ranks 132 and 116, 3 ranks 166 and 174; bf16 2 ranks 80 and 60, 3 ranks
-// 105 and 89, 4 ranks 121 and 119, and for the reduce-scatter 92 and 94.
+// and read again, us a call in a graph): fp32 2 ranks 128 and 125, 3 ranks 168 and 187; bf16 2 ranks 87 and 68,
+// 3 ranks 111 and 97, 4 ranks 131 and 127. The reduce-scatter: fp32 2 ranks 111 and 108, 3 ranks 135 and 150;
+// bf16 3 ranks 86 and 77, 4 ranks 101 and 99.
 constexpr int32_t most_reread(int dtype) { return dtype == D_BF16 ? 3 : 2; }
 
 template <int DT, int KIND, bool EACH> void launch_reduce(Sequence& s, int64_t blocks, const BucketTab& t, double* partial, double* own) {

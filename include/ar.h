@@ -332,7 +332,9 @@ ar_status ar_set_launch_blocks(int64_t max_blocks, int64_t* previous);
  * and a scaling that limits it to max_norm,
  *   scale = 1                    if N + eps <= max_norm
  *           max_norm / (N + eps) otherwise
- *   y     = scale g, rounded once to y's type,
+ *   y     = scale g, where the scale and the product are each rounded to fp32 and a bf16 y once more: off
+ *           from the exact product by two half steps of fp32 (2^-23 of it), in bf16 by another 2^-8 of it (by
+ *           half the last bit where y lies below the smallest normal value),
  * on tensors of fp32 and bf16, which one call may mix. A gradient within the limit keeps its bits.
  *  - Norms: squares are summed in 64 bits, so no fp32 or bf16 value overflows or vanishes, in an
  *    order that the sizes, the device and ar_set_launch_blocks() fix, so a call gives the same bits
@@ -388,7 +390,7 @@ ar_status ar_grad_workspace_bytes(const ar_grad* grads, int32_t count, const ar_
 /* The Allreduce of `buckets` gradient buckets over P ranks with the clipping of the result: the ranks
  * are combined as an AR_DIRECT Allreduce combines them (rank order, fp32; op AR_SUM or AR_AVG), N is
  * the norm over all buckets of the combined values before they are rounded to dtype, and every rank
- * ends with the scaled values, rounded once. A gradient within the limit ends with the bits of
+ * ends with the scaled values, rounded as y above. A gradient within the limit ends with the bits of
  * ar_allreduce(..., AR_DIRECT). collective AR_REDUCE_SCATTER: rank q ends with its part of that, in
  * place (ar_collective); its other elements are untouched.
  * bufs: host array of buckets * P device pointers, bucket b's rank p at bufs[b * P + p], each to n[b]
