@@ -19,6 +19,7 @@ from ._ar import (  # noqa: F401
     make_call, marshal_ptrs, ar_cache_stats_get, ar_release_cached, ar_allreduce_noalloc, AR_NOALLOC_SCRATCH_BYTES,
     AR_MAX_GRADS, GradList, NORMS, Norm, ar_allreduce_clip, ar_allreduce_clip_workspace_bytes, ar_grad_clip,
     ar_grad_norm, ar_grad_workspace_bytes, make_clip, marshal_grads,
+    REDUCTIONS, Reduction, ar_vocab_loss, ar_vocab_loss_grad, ar_vocab_workspace_bytes, make_vocab,
 )
 
 _TORCH_DTYPE = {"int32": "int32", "fp32": "float32", "bf16": "bfloat16"}
@@ -147,7 +148,7 @@ class _Place:
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
         if stream.device.index != index:
-            raise _invalid(f"the stream is on {stream.device}, the gradients on cuda:{index}")
+            raise _invalid(f"the stream is on {stream.device}, the tensors on cuda:{index}")
         if stream.cuda_stream != self.stream:  # results and scratch belong to the stream that writes them
             self.guards += (torch.cuda.stream(stream),)
             self.stream = stream.cuda_stream
@@ -176,7 +177,7 @@ class _Place:
                 return None
             workspace = self.torch.empty(size, dtype=self.torch.uint8, device="cuda")
         elif workspace.get_device() != self.index or not workspace.is_contiguous():
-            raise _invalid("workspace must be a contiguous tensor on the gradients' device")
+            raise _invalid("workspace must be a contiguous tensor on the call's device")
         clip.workspace, clip.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         return workspace
 
@@ -259,3 +260,130 @@ def allreduce_clip(buckets, max_norm, op="sum", norm="l2", eps=1e-6, collective=
         ar_allreduce_clip(array("Q", map(T.data_ptr, tensors)), *args, clip, at.stream)
         _written(torch, tensors)
     return total
+
+
+# ---- losses over a vocabulary in pieces ----
+def _rows(torch, t, what, dtype, index):
+    """(address, distance of rows) of a matrix whose rows are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype != dtype or t.get_device() != index:
+        raise _invalid(f"{what} must be a matrix of {dtype} on cuda:{index}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise _invalid(f"{what}'s rows must be contiguous")
+    return t.data_ptr(), t.stride(0)
+
+
+def _outputs(torch, given, like, what, index):
+    if given is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if not isinstance(given, torch.Tensor) or given.shape != like.shape:
+        raise _invalid(f"{what} must be of its gradient's shape")
+    return given
+
+
+def _vocab(hidden, weight, ids, logits, reduction, ignore_index, temperature, token_weights, grad, out_hidden,
+           out_weight, stream, workspace):
+    torch = _torch()
+    single = isinstance(weight, torch.Tensor)
+    pieces = [weight] if single else list(weight)
+    if not isinstance(hidden, torch.Tensor) or hidden.dtype not in _TYPES or not hidden.is_cuda or hidden.dim() != 2:
+        raise _invalid("hidden must be a float32 or bfloat16 matrix on a CUDA device")
+    T, H = hidden.shape
+    index, dtype = hidden.get_device(), hidden.dtype
+    place, ld = _rows(torch, hidden, "hidden", dtype, index)
+    table = []
+    for w in pieces:
+        at, wld = _rows(torch, w, "every piece of the output matrix", dtype, index)
+        if w.shape[1] != H:
+            raise _invalid("hidden and the output matrix differ in width")
+        table.append([at, None, w.shape[0], wld, 0])
+    shape = (T,) if logits is None else (T, logits.shape[1] if isinstance(logits, torch.Tensor) and logits.dim() == 2 else 0)
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64) or ids.get_device() != index \
+            or tuple(ids.shape) != shape or (T and shape[-1] > 1 and ids.stride(-1) != 1):
+        raise _invalid("targets must be int32 or int64, one a token (a teacher's ids: as many as its logits, in "
+                       "contiguous rows), on hidden's device")
+    kw = {}
+    if logits is not None:
+        if not shape[1] or logits.dtype not in _TYPES:
+            raise _invalid("teacher logits must be a float32 or bfloat16 matrix of at least one column")
+        at, lld = _rows(torch, logits, "teacher logits", logits.dtype, index)
+        kw = dict(top=shape[1], logits=at, logits_ld=lld, logits_dtype=_TYPES[logits.dtype], ids_ld=ids.stride(0))
+    if token_weights is not None and (token_weights.dtype != torch.float32 or token_weights.get_device() != index
+                                      or tuple(token_weights.shape) != (T,) or not token_weights.is_contiguous()):
+        raise _invalid("token_weights must be contiguous float32, one a token, on hidden's device")
+    if reduction not in REDUCTIONS:
+        raise _invalid(f"reduction must be one of {', '.join(REDUCTIONS)}")
+    with _Place(index, stream) as at:
+        each = reduction == "none"
+        loss = at.floats(T) if each else at.floats()
+        d_hidden = d_weights = None
+        if grad:
+            d_hidden = _outputs(torch, out_hidden, hidden, "out_hidden", index)
+            kw["dh"], kw["dh_ld"] = _rows(torch, d_hidden, "out_hidden", dtype, index)
+            outs = [None] * len(pieces) if out_weight is None else [out_weight] if single else list(out_weight)
+            if len(outs) != len(pieces):
+                raise _invalid(f"{len(pieces)} pieces, and {len(outs)} outputs")
+            d_weights = [_outputs(torch, o, w, "out_weight", index) for o, w in zip(outs, pieces)]
+            for row, d in zip(table, d_weights):
+                row[1], row[4] = _rows(torch, d, "out_weight", dtype, index)
+        call = make_vocab(T, H, _TYPES[dtype], place, ld, [tuple(row) for row in table], ids.data_ptr(),
+                          loss.data_ptr(), temperature=temperature, reduction=reduction, ids_bytes=ids.element_size(),
+                          ignore=ignore_index,
+                          token_weights=None if token_weights is None else token_weights.data_ptr(), **kw)
+        workspace = at.scratch(call, workspace, lambda: ar_vocab_workspace_bytes(call, grad), large=True)
+        (ar_vocab_loss_grad if grad else ar_vocab_loss)(call, at.stream)
+        if grad:
+            _written(torch, [d_hidden] + d_weights)
+    return (loss, d_hidden, d_weights[0] if single else d_weights) if grad else loss
+
+
+def vocab_loss(hidden, weight, targets, reduction="mean", ignore_index=-100, temperature=1.0, token_weights=None,
+               stream=None, workspace=None):
+    """Softmax cross entropy of hidden states against a vocabulary in pieces, without keeping the logits.
+
+    hidden: [T, H], float32 or bfloat16; weight: the output matrix [V, H] of the same type, or the list of its
+    pieces [V_p, H] in rank order (rows contiguous, any distance apart); targets: [T], int32 or int64. Logits are
+    hidden weight^T / temperature. Rows whose target is ignore_index are left out (loss 0); an id outside the
+    vocabulary makes the loss NaN. token_weights: float32 [T], each row's factor. reduction: "mean" (over the rows
+    that are not left out, whatever their weight; 0 if there are none) and "sum" give a 0-dim float32 tensor,
+    "none" every row's loss. Losses carry no autograd history: vocab_loss_grad gives the gradients.
+    ``stream`` defaults to torch's current stream, ``workspace`` (ar_vocab_workspace_bytes) to memory from torch.
+    """
+    return _vocab(hidden, weight, targets, None, reduction, ignore_index, temperature, token_weights, False, None, None,
+                  stream, workspace)
+
+
+def vocab_loss_grad(hidden, weight, targets, reduction="mean", ignore_index=-100, temperature=1.0, token_weights=None,
+                    out_hidden=None, out_weight=None, stream=None, workspace=None):
+    """vocab_loss and its gradients: (loss, d_hidden, d_weight), d_weight as weight (a tensor, or a list of pieces).
+
+    The gradients are of the loss ("none": of the rows' sum), in the inputs' type; d_hidden is the sum over all
+    pieces, as an Allreduce of the ranks' parts leaves it. out_hidden, out_weight: tensors that receive them.
+    """
+    return _vocab(hidden, weight, targets, None, reduction, ignore_index, temperature, token_weights, True, out_hidden,
+                  out_weight, stream, workspace)
+
+
+def distill_loss(hidden, weight, teacher_logits, teacher_ids, reduction="mean", temperature=1.0, token_weights=None,
+                 stream=None, workspace=None):
+    """Distance of a student to a teacher's top logits, over a vocabulary in pieces, without the student's logits.
+
+    teacher_logits: [T, K], float32 or bfloat16, and teacher_ids: [T, K], int32 or int64; a negative id ends or
+    thins out a row's list, and a row without entries is left out. With q the softmax of a row's teacher logits /
+    temperature and p that of hidden weight^T / temperature over the whole vocabulary, the row's loss is
+    sum_k q_k (log q_k - log p_id(k)) (no factor of temperature squared). The other arguments as for vocab_loss.
+    """
+    return _vocab(hidden, weight, teacher_ids, _given(teacher_logits), reduction, 0, temperature, token_weights, False,
+                  None, None, stream, workspace)
+
+
+def distill_loss_grad(hidden, weight, teacher_logits, teacher_ids, reduction="mean", temperature=1.0,
+                      token_weights=None, out_hidden=None, out_weight=None, stream=None, workspace=None):
+    """distill_loss and its gradients, as vocab_loss_grad gives them. The teacher's logits get none."""
+    return _vocab(hidden, weight, teacher_ids, _given(teacher_logits), reduction, 0, temperature, token_weights, True,
+                  out_hidden, out_weight, stream, workspace)
+
+
+def _given(logits):
+    if logits is None:
+        raise _invalid("teacher logits are missing")
+    return logits

@@ -97,6 +97,13 @@ class Norm(enum.IntEnum):
     AR_NORM_MAX = 1
 
 
+class Reduction(enum.IntEnum):
+    AR_MEAN = 0
+    AR_TOTAL = 1
+    AR_NONE = 2
+
+
+REDUCTIONS = {"mean": Reduction.AR_MEAN, "sum": Reduction.AR_TOTAL, "none": Reduction.AR_NONE}
 NORMS = {"l2": Norm.AR_NORM_L2, "max": Norm.AR_NORM_MAX}
 DTYPES = {"int32": Dtype.AR_INT32, "fp32": Dtype.AR_FP32, "bf16": Dtype.AR_BF16}
 OPS = {"sum": Op.AR_SUM, "max": Op.AR_MAX, "avg": Op.AR_AVG}
@@ -165,6 +172,20 @@ class ar_clip(C.Structure):
                 ("workspace_bytes", C.c_size_t), ("start_event", C.c_void_p), ("stop_event", C.c_void_p)]
 
 
+class ar_vocab_piece(C.Structure):
+    _fields_ = [("w", C.c_void_p), ("dw", C.c_void_p), ("rows", C.c_int64), ("ld", C.c_int64), ("dld", C.c_int64)]
+
+
+class ar_vocab(C.Structure):
+    _fields_ = [("T", C.c_int64), ("H", C.c_int64), ("dtype", C.c_int32), ("P", C.c_int32), ("hidden", C.c_void_p),
+                ("ld", C.c_int64), ("pieces", C.POINTER(ar_vocab_piece)), ("temperature", C.c_float),
+                ("reduction", C.c_int32), ("token_weights", C.c_void_p), ("top", C.c_int32), ("ids_bytes", C.c_int32),
+                ("ids", C.c_void_p), ("ids_ld", C.c_int64), ("ignore", C.c_int64), ("logits", C.c_void_p),
+                ("logits_ld", C.c_int64), ("logits_dtype", C.c_int32), ("loss", C.c_void_p), ("dh", C.c_void_p),
+                ("dh_ld", C.c_int64), ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
+                ("start_event", C.c_void_p), ("stop_event", C.c_void_p)]
+
+
 # exported symbol -> (restype, argtypes)
 SIGNATURES = {
     "ar_allreduce": (C.c_int, [C.POINTER(C.c_void_p), C.c_int32, C.c_int64, C.c_int32, C.c_int32, C.c_int32,
@@ -205,6 +226,9 @@ SIGNATURES = {
                                     C.POINTER(ar_clip), C.c_void_p]),
     "ar_allreduce_clip_workspace_bytes": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32,
                                                     C.POINTER(ar_clip), C.POINTER(C.c_size_t)]),
+    "ar_vocab_loss": (C.c_int, [C.POINTER(ar_vocab), C.c_void_p]),
+    "ar_vocab_loss_grad": (C.c_int, [C.POINTER(ar_vocab), C.c_void_p]),
+    "ar_vocab_workspace_bytes": (C.c_int, [C.POINTER(ar_vocab), C.c_int32, C.POINTER(C.c_size_t)]),
     "ar_status_string": (C.c_char_p, [C.c_int]),
     "ar_last_hip_error": (C.c_int32, []),
     "ar_last_error_message": (C.c_char_p, []),
@@ -421,6 +445,34 @@ def ar_allreduce_clip_workspace_bytes(n, P, dtype, op, collective, clip: ar_clip
     _check(lib.ar_allreduce_clip_workspace_bytes(sizes.buffer_info()[0], len(sizes), int(P), _enum(DTYPES, dtype),
                                                  _enum(OPS, op), _enum(COLLECTIVES, collective), C.byref(clip),
                                                  C.byref(out)))
+    return out.value
+
+
+# ---- losses over a vocabulary in pieces ----
+def make_vocab(T, H, dtype, hidden, ld, pieces, ids, loss, dh=None, dh_ld=0, temperature=1.0, reduction="mean",
+               token_weights=None, top=0, ids_bytes=8, ids_ld=0, ignore=-100, logits=None, logits_ld=0,
+               logits_dtype="fp32", workspace=None, workspace_bytes=0, start_event=None, stop_event=None) -> ar_vocab:
+    """pieces: (w, dw, rows, ld, dld) of every rank; addresses are integers (None: NULL)."""
+    table = (ar_vocab_piece * max(len(pieces), 1))(*pieces)
+    call = ar_vocab(int(T), int(H), _enum(DTYPES, dtype), len(pieces), hidden, int(ld), table, float(temperature),
+                    _enum(REDUCTIONS, reduction), token_weights, int(top), int(ids_bytes), ids, int(ids_ld),
+                    int(ignore), logits, int(logits_ld), _enum(DTYPES, logits_dtype), loss, dh, int(dh_ld), workspace,
+                    int(workspace_bytes), _event(start_event), _event(stop_event))
+    call._pieces_keepalive = table
+    return call
+
+
+def ar_vocab_loss(call: ar_vocab, stream=None):
+    _check(lib.ar_vocab_loss(C.byref(call), _stream(stream)))
+
+
+def ar_vocab_loss_grad(call: ar_vocab, stream=None):
+    _check(lib.ar_vocab_loss_grad(C.byref(call), _stream(stream)))
+
+
+def ar_vocab_workspace_bytes(call: ar_vocab, grad=True) -> int:
+    out = C.c_size_t(0)
+    _check(lib.ar_vocab_workspace_bytes(C.byref(call), int(bool(grad)), C.byref(out)))
     return out.value
 
 

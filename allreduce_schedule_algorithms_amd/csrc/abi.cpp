@@ -11,6 +11,7 @@
 
 #include "exec.h"
 #include "grad.h"
+#include "vocab.h"
 #include "sched.h"
 
 static_assert(sizeof(ar_oprec) == sizeof(ar::OpRec), "ar_oprec layout");
@@ -263,6 +264,97 @@ ar_status grad_call(const ar_grad* grads, int32_t count, const ar_clip* clip, bo
     return AR_OK;
   }
   return finish(ar::run_grad(g.data(), int64_t(g.size()), c, scale, stream));
+}
+
+// T rows of `length` elements, ld apart: first to last byte.
+Span span_of(const void* p, int64_t rows, int64_t ld, int64_t length, int64_t bytes, bool written) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  return {at, at + uintptr_t(((rows - 1) * ld + length) * bytes), written};
+}
+
+// run: with its pointers (otherwise for the workspace's size).
+ar_status check_vocab(const ar_vocab* c, bool grad, bool run, ar::Vocab* out) {
+  if (!c) return fail(AR_INVALID_ARGUMENT, "call is NULL");
+  const auto bad = [](const std::string& why) { return fail(AR_INVALID_ARGUMENT, why); };
+  if (c->T < 0 || c->T >= (int64_t(1) << 30)) return bad("T must be in [0, 2^30)");
+  if (c->H < 1 || c->H > 65536) return bad("H must be in [1, 65536]");
+  if (!is_float(c->dtype)) return bad("dtype must be AR_FP32 or AR_BF16");
+  if (c->P < 1 || c->P > AR_MAX_RANKS) return bad("P must be in [1, " + std::to_string(AR_MAX_RANKS) + "]");
+  if (!c->pieces) return bad("pieces is NULL");
+  if (!(c->temperature > 0) || !std::isfinite(c->temperature) || !std::isfinite(1.f / c->temperature))
+    return bad("temperature must be positive and finite, and its reciprocal too");
+  if (c->reduction < AR_MEAN || c->reduction > AR_NONE) return bad("unknown reduction");
+  if (c->top < 0 || c->top > 1024) return bad("top must be in [0, 1024]");
+  if (c->ids_bytes != 4 && c->ids_bytes != 8) return bad("ids_bytes must be 4 or 8");
+  if (c->top && !is_float(c->logits_dtype)) return bad("logits_dtype must be AR_FP32 or AR_BF16");
+  const int64_t e = float_bytes(c->dtype), most = int64_t(1) << 28;
+  std::vector<Span> spans;
+  // a matrix of the call: its row distance, address and place
+  const auto matrix = [&](const char* what, const void* p, int64_t rows, int64_t ld, int64_t length, int64_t bytes, bool written) {
+    if (rows > 1 && (ld < length || ld > most)) return bad(std::string(what) + ": rows are less than their length apart, or more than 2^28");
+    if (!run || !rows) return AR_OK;
+    if (!p) return bad(std::string(what) + " is NULL");
+    if (reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes)) return bad(std::string(what) + " is not aligned to its elements");
+    spans.push_back(span_of(p, rows, ld, length, bytes, written));
+    return AR_OK;
+  };
+  ar_status st = matrix("hidden", c->hidden, c->T, c->ld, c->H, e, false);
+  if (st == AR_OK) st = matrix("ids", c->ids, c->T, c->top ? c->ids_ld : 1, std::max(c->top, 1), c->ids_bytes, false);
+  if (st == AR_OK && c->top) st = matrix("logits", c->logits, c->T, c->logits_ld, c->top, float_bytes(c->logits_dtype), false);
+  if (st == AR_OK && c->token_weights) st = matrix("token_weights", c->token_weights, c->T, 1, 1, 4, false);
+  if (st == AR_OK) st = matrix("loss", c->loss, c->reduction == AR_NONE ? c->T : 1, 1, 1, 4, true);
+  if (st == AR_OK && grad) st = matrix("dh", c->dh, c->T, c->dh_ld, c->H, e, true);
+  int64_t rows = 0, padded = 0;
+  for (int32_t p = 0; p < c->P && st == AR_OK; ++p) {
+    const ar_vocab_piece& q = c->pieces[p];
+    const std::string name = "piece " + std::to_string(p);
+    if (q.rows < 0 || q.rows > (1 << 20)) return bad(name + ": rows must be in [0, 2^20]");
+    rows += q.rows;
+    padded += (q.rows + 255) / 256 * 256;
+    st = matrix((name + "'s w").c_str(), q.w, q.rows, q.ld, c->H, e, false);
+    if (st == AR_OK && grad) st = matrix((name + "'s dw").c_str(), q.dw, q.rows, q.dld, c->H, e, true);
+    // a single row has no distance to the next
+    out->pieces.push_back({q.w, grad ? q.dw : nullptr, q.rows, q.rows > 1 ? q.ld : (c->H + 7) / 8 * 8, q.rows > 1 ? q.dld : c->H});
+  }
+  if (st != AR_OK) return st;
+  if (!rows) return bad("the vocabulary is empty");
+  if (padded > (1 << 20)) return bad("the vocabulary, its pieces rounded up to 256 rows, exceeds 2^20 rows");
+  if (run && c->workspace) {
+    const uintptr_t w = reinterpret_cast<uintptr_t>(c->workspace);
+    if (w % 16) return bad("workspace is not 16-byte aligned");
+    if (c->workspace_bytes) spans.push_back({w, w + c->workspace_bytes, true});
+  }
+  if (spans_meet(spans)) return bad("a tensor that is written overlaps another");
+  out->T = c->T;
+  out->H = c->H;
+  out->dtype = c->dtype;
+  out->hidden = c->hidden;
+  out->ld = c->ld;
+  out->temperature = c->temperature;
+  out->reduction = c->reduction;
+  out->token_weights = c->token_weights;
+  out->top = c->top;
+  out->ids = c->ids;
+  out->wide_ids = c->ids_bytes == 8;
+  out->ids_ld = c->ids_ld;
+  out->ignore = c->ignore;
+  out->logits = c->logits;
+  out->logits_dtype = c->logits_dtype;
+  out->logits_ld = c->logits_ld;
+  out->loss = c->loss;
+  out->dh = c->dh;
+  out->dh_ld = c->dh_ld;
+  out->workspace = c->workspace;
+  out->workspace_bytes = c->workspace ? c->workspace_bytes : 0;
+  out->start_event = c->start_event;
+  out->stop_event = c->stop_event;
+  return AR_OK;
+}
+
+ar_status vocab_call(const ar_vocab* call, bool grad, void* stream) {
+  ar::Vocab v;
+  const ar_status st = check_vocab(call, grad, true, &v);
+  return st == AR_OK ? finish(ar::run_vocab(v, grad, stream)) : st;
 }
 
 }  // namespace
@@ -632,6 +724,24 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
     if (st != AR_OK) return st;
     *bytes = ar::allreduce_clip_workspace(b, c);
     return AR_OK;
+  });
+}
+
+ar_status ar_vocab_loss(const ar_vocab* call, void* stream) {
+  return guarded([&] { return vocab_call(call, false, stream); });
+}
+
+ar_status ar_vocab_loss_grad(const ar_vocab* call, void* stream) {
+  return guarded([&] { return vocab_call(call, true, stream); });
+}
+
+ar_status ar_vocab_workspace_bytes(const ar_vocab* call, int32_t grad, size_t* bytes) {
+  if (!bytes) return fail(AR_INVALID_ARGUMENT, "bytes is NULL");
+  return guarded([&] {
+    ar::Vocab v;
+    const ar_status st = check_vocab(call, grad != 0, false, &v);
+    if (st == AR_OK) *bytes = ar::vocab_workspace(v, grad != 0);
+    return st;
   });
 }
 

@@ -32,7 +32,7 @@
 #include <vector>
 
 #include "kernels.h"
-#include "launch.h"
+#include "sequence.h"
 
 namespace ar {
 
@@ -740,15 +740,6 @@ __global__ __launch_bounds__(kSmallThreads) void k_bucket_small(BucketTab tab, f
 // ----------------------------------------------------------------------------
 namespace {
 
-RunResult hip_fail(hipError_t e, const char* what) {
-  RunResult r;
-  r.status = 4;  // AR_HIP_ERROR
-  r.hip_error = int(e);
-  r.message = std::string(what) + ": " + hipGetErrorString(e);
-  (void)hipGetLastError();  // reported here: not left for a later call that asks for the last error
-  return r;
-}
-
 // Workgroups of a pass over the whole call: 6 of 4 waves per compute unit. A static share wants all of them
 // resident (2048 of them ran 4-6% longer than 1536), and most passes' registers allow 6 or more. The sums of fp32
 // are the exception: 7, 8 and more ranks allow 5 workgroups on a compute unit, with the buckets' own norms 4, 6
@@ -830,32 +821,6 @@ RunResult workspace_of(const Clip& clip, size_t need, hipStream_t st, std::uniqu
   *out = static_cast<char*>(w.p);
   return r;
 }
-
-// The call's launches in order: the first records the start event, the last the stop event. Errors are
-// taken from the launch itself, not from the thread's last one, which may be another call's.
-template <typename T> struct Same { using type = T; };
-struct Sequence {
-  hipStream_t st;
-  Evs ev;
-  int64_t left;
-  bool begun = false;
-  hipError_t err = hipSuccess;
-  template <typename... A> void launch(void (*k)(A...), int64_t blocks, int threads, typename Same<A>::type... a) {
-    if (err != hipSuccess) return;
-    --left;
-    void* args[] = {static_cast<void*>(&a)...};
-    err = hipExtLaunchKernel(reinterpret_cast<const void*>(k), dim3(unsigned(blocks)), dim3(unsigned(threads)), args, 0, st,
-                             begun ? nullptr : ev.start, left ? nullptr : ev.stop, 0);
-    begun = true;
-  }
-  RunResult done() {
-    if (err == hipSuccess && !begun) {  // no launch: both events mark this point of the stream
-      if (ev.start) err = hipEventRecord(ev.start, st);
-      if (err == hipSuccess && ev.stop) err = hipEventRecord(ev.stop, st);
-    }
-    return err == hipSuccess ? RunResult{} : hip_fail(err, "launching the gradient kernels");
-  }
-};
 
 // Workgroups of a launch. Their counts of items may differ by one: as many workgroups on every compute
 // unit matter more (7 x 2^24 fp32: 175 us with 1536 workgroups of 5 or 6 items, 184 with 1366 of 6).
@@ -953,7 +918,7 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
     s.left = 1;
     if (scale) { AR_KIND(clip.norm, s.launch(k_grad_small<KIND, true>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
     else { AR_KIND(clip.norm, s.launch(k_grad_small<KIND, false>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
-    return s.done();
+    return s.done("launching the gradient kernels");
   }
   const Partials parts = place_partials(tabs);
   std::unique_lock<std::mutex> lk;
@@ -984,7 +949,7 @@ RunResult run_grad(const Grad* g, int64_t count, const Clip& clip, bool scale, v
       lim.total = nullptr;
     }
   }
-  return s.done();
+  return s.done("launching the gradient kernels");
 }
 
 namespace {
@@ -1117,7 +1082,7 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
     s.left = 1;
     if (b.dtype == D_BF16) { AR_KIND(clip.norm, s.launch(k_bucket_small<D_BF16, KIND>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
     else { AR_KIND(clip.norm, s.launch(k_bucket_small<D_FP32, KIND>, 1, kSmallThreads, t, clip.total, clip.each, clip.max_norm, clip.eps)); }
-    return s.done();
+    return s.done("launching the gradient kernels");
   }
   std::unique_lock<std::mutex> lk;
   char* ws = nullptr;
@@ -1151,7 +1116,7 @@ RunResult run_allreduce_clip(const Buckets& b, const Clip& clip, void* stream) {
     else { AR_KIND(clip.norm, launch_spread<D_FP32, KIND>(s, parts.blocks[k], pl.tabs[k], lim)); }
     lim.total = nullptr;
   }
-  return s.done();
+  return s.done("launching the gradient kernels");
 }
 
 GradCache grad_cache() {

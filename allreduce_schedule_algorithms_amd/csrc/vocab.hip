@@ -1,0 +1,1096 @@
+// Losses over a vocabulary in pieces for gfx950: softmax cross entropy and the distance
+// to a teacher's top logits, of hidden states h [T, H] against an output matrix W [V, H]
+// whose rows lie in P pieces, and their gradients.
+//
+//   z = h W^T / temperature                       (never kept as a whole)
+//   lse_t = log(sum_v exp z_tv),  p = exp(z - lse)
+//   cross entropy:  loss_t = lse_t - z_ty
+//   distillation:   q_t = softmax(teacher / temperature),
+//                   loss_t = sum_k q_tk (log q_tk - z_t,id(k) + lse_t)
+//   D = c (p - q)   with q the one-hot target for cross entropy, c_t the row's weight in
+//                   the call's loss over the temperature
+//   dh = D W,  dW = D^T h
+//
+// Rows that the targets leave out take no part: the rows that count are gathered in order
+// (k_scan, k_pack), and every product runs over as many as there are. The products are
+// matrix products of bf16 operands with fp32 sums; fp32 operands are split exactly into
+// three bf16 terms each, and the six products of the larger terms are summed (what is
+// left out is 2^-26 of a product).
+//
+// A call works on the tokens in chunks, so that its scratch is bounded: the logits' tile
+// leaves the product as exp(z - m), m the tile's largest, beside m and the tile's sum; once
+// a row's lse is known, one pass turns them into D. Nothing is added atomically: the
+// same sizes give the same bits on every run.
+#include "vocab.h"
+
+#include <hip/hip_ext.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "sequence.h"
+
+namespace ar {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+#define AR_LDS __attribute__((address_space(3)))
+
+constexpr int kBK = 64;         // depth of a tile: 128 bytes of a row
+constexpr int kPieceTab = 64;   // pieces that one launch's arguments carry
+constexpr int kUnit = 256;      // pieces and token chunks are padded to this many rows
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// One piece as the kernels see it, in the workspace. `first`: its first row in the vocabulary; `start`: the same
+// with every piece padded to kUnit rows, the coordinate that tiles, D and the ids' table use.
+struct Piece {
+  const char* w;
+  char* dw;
+  int64_t ld, dld;
+  int32_t rows, start, first, pad;
+};
+
+struct PieceTab {
+  Piece p[kPieceTab];
+  int32_t count, at;
+};
+
+struct Counts {
+  int32_t active;  // rows that take part
+  int32_t mean;    // rows that are not left out (those of weight 0 among them)
+  int32_t bad;     // rows with an id outside the vocabulary
+  int32_t pad;
+};
+
+enum Flag : uint8_t { F_OUT = 0, F_ACTIVE = 1, F_BAD = 2, F_ZERO = 3 };
+
+template <bool BY_START> __device__ __forceinline__ int piece_of(const Piece* p, int P, int32_t at) {
+  int lo = 0, hi = P;  // the last piece that begins at or before `at`
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if ((BY_START ? p[mid].start : p[mid].first) <= at) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int64_t id_at(const void* ids, bool wide, int64_t i) {
+  return wide ? static_cast<const int64_t*>(ids)[i] : int64_t(static_cast<const int32_t*>(ids)[i]);
+}
+
+__device__ __forceinline__ float logit_at(const void* p, int dtype, int64_t i) {
+  return dtype == D_BF16 ? as_f(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16) : static_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// x as a sum of three bf16 values, exactly: each is the nearest to what is left (a magnitude that would round to
+// an infinity is cut instead), and 24 bits leave at most 8 for the third.
+__device__ __forceinline__ void split3(float x, __bf16 (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    __bf16 b = __bf16(x);
+    if (__builtin_isinf(float(b)) && !__builtin_isinf(x)) b = __builtin_bit_cast(__bf16, uint16_t(as_u(x) >> 16));
+    t[i] = b;
+    x = __builtin_isfinite(float(b)) ? x - float(b) : 0.f;  // infinities and NaN stay in the first term
+  }
+}
+
+// ----------------------------------------------------------------------------
+// rows
+// ----------------------------------------------------------------------------
+__global__ void k_vocab_pieces(PieceTab tab, Piece* out) {
+  for (int i = threadIdx.x; i < tab.count; i += blockDim.x) out[tab.at + i] = tab.p[i];
+}
+
+// What a call's targets are.
+struct Targets {
+  const void* ids;
+  const void* logits;
+  const float* weights;
+  int64_t ids_ld, logits_ld, ignore, V;
+  int32_t K, logits_dtype;  // K = 0: one target a row
+  bool wide;
+  float temperature;
+};
+
+// Distillation: a wave per row finds the teacher's largest logit and the sum of exp around it.
+constexpr int kRowWaves = 4;
+__global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int64_t T, float2* stat, uint8_t* flags) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t r = int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64; r < T; r += int64_t(gridDim.x) * kRowWaves) {
+    float top = -INFINITY;
+    bool bad = false, nan = false;
+    for (int k = lane; k < t.K; k += 64) {
+      const int64_t id = id_at(t.ids, t.wide, r * t.ids_ld + k);
+      if (id < 0) continue;
+      bad |= id >= t.V;
+      const float x = logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) / t.temperature;
+      nan |= x != x;
+      top = fmaxf(top, x);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    bad = __any(bad);
+    nan = __any(nan);
+    if (nan) top = NAN;
+    float sum = 0;
+    for (int k = lane; k < t.K; k += 64)
+      if (id_at(t.ids, t.wide, r * t.ids_ld + k) >= 0)
+        sum += expf(logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) / t.temperature - top);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+    if (lane == 0) {
+      stat[r] = float2{top, sum};
+      // no entries, or none above -infinity: the row has no distribution and is left out
+      flags[r] = bad ? F_BAD : top == -INFINITY ? F_OUT : t.weights && t.weights[r] == 0 ? F_ZERO : F_ACTIVE;
+    }
+  }
+}
+
+// Rows that take part, in order, at rows[0..active); the others behind them. One workgroup.
+constexpr int kScanThreads = 1024, kScanEach = 4;
+__global__ __launch_bounds__(kScanThreads) void k_vocab_scan(Targets t, int64_t T, int32_t* rows, uint8_t* flags, Counts* counts) {
+  __shared__ int wave_n[kScanThreads / 64][kScanEach], tally[2];
+  const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
+  if (tid < 2) tally[tid] = 0;
+  int done = 0, mean = 0, bad = 0;  // active rows before this round; the thread's own tallies
+  for (int64_t base = 0; base < T; base += kScanThreads * kScanEach) {
+    uint8_t f[kScanEach];
+    uint64_t mask[kScanEach];
+#pragma unroll
+    for (int j = 0; j < kScanEach; ++j) {
+      const int64_t r = base + j * kScanThreads + tid;
+      f[j] = F_OUT;
+      if (r < T) {
+        if (t.K) {
+          f[j] = flags[r];
+        } else {
+          const int64_t id = id_at(t.ids, t.wide, r);
+          f[j] = id == t.ignore ? F_OUT : id < 0 || id >= t.V ? F_BAD : t.weights && t.weights[r] == 0 ? F_ZERO : F_ACTIVE;
+          flags[r] = f[j];
+        }
+        mean += f[j] != F_OUT;
+        bad += f[j] == F_BAD;
+      }
+      mask[j] = __ballot(f[j] == F_ACTIVE);
+      if (lane == 0) wave_n[wave][j] = __popcll(mask[j]);
+    }
+    __syncthreads();
+    int at = done;
+#pragma unroll
+    for (int j = 0; j < kScanEach; ++j) {
+      int before = 0, all = 0;
+      for (int w = 0; w < kScanThreads / 64; ++w) {
+        const int n = wave_n[w][j];
+        before += w < wave ? n : 0;
+        all += n;
+      }
+      const int64_t r = base + j * kScanThreads + tid;
+      const int mine = at + before + __popcll(mask[j] & ((uint64_t(1) << lane) - 1));  // active rows before r
+      if (r < T) {
+        if (f[j] == F_ACTIVE) rows[mine] = int32_t(r);
+        else rows[T - 1 - (r - mine)] = int32_t(r);  // r - mine others before it: from the end
+      }
+      at += all;
+    }
+    done = at;
+    __syncthreads();
+  }
+  if (mean) atomicAdd(&tally[0], mean);  // whole numbers in LDS: the order does not matter
+  if (bad) atomicAdd(&tally[1], bad);
+  __syncthreads();
+  if (tid == 0) *counts = Counts{done, tally[0], tally[1], 0};
+}
+
+// The hidden rows that take part, gathered as bf16 terms of Hp elements each, zeros behind them; their ids as padded
+// coordinates; and what the rows left out get: gradients and losses of 0 (NaN where an id is outside).
+struct PackArgs {
+  const void* hidden;
+  int64_t ld, T, Tpad;
+  int32_t H, Hp, P;
+  const Piece* pieces;
+  const int32_t* rows;
+  const uint8_t* flags;
+  const Counts* counts;
+  char* hp;
+  int32_t* idt;  // [K or 1][Tpad]
+  void* dh;      // null: no gradient
+  int64_t dh_ld;
+  float* each;   // every row's loss, or null
+};
+
+template <int DT> __device__ __forceinline__ float elem(const void* p, int64_t i) {
+  if constexpr (DT == D_BF16) return as_f(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
+  else return static_cast<const float*>(p)[i];
+}
+
+// A row of H elements into terms of Hp elements, zero behind H. Called by a whole wave.
+template <int DT> __device__ __forceinline__ void pack_row(const void* src, int64_t at, int H, int Hp, __bf16* dst, int lane) {
+  for (int c = lane * 8; c < Hp; c += 512) {
+    if constexpr (DT == D_BF16) {
+      const uint16_t* s = static_cast<const uint16_t*>(src) + at + c;
+      typedef uint16_t V __attribute__((ext_vector_type(8), aligned(2)));
+      V v;
+      if (c + 8 <= H) {
+        v = *reinterpret_cast<const V*>(s);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < H ? s[j] : uint16_t(0);
+      }
+      typedef uint16_t A __attribute__((ext_vector_type(8)));
+      *reinterpret_cast<A*>(dst + c) = v;
+    } else {
+      const float* s = static_cast<const float*>(src) + at + c;
+      bf16x8 o[3];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        __bf16 b[3];
+        split3(c + j < H ? s[j] : 0.f, b);
+        o[0][j] = b[0];
+        o[1][j] = b[1];
+        o[2][j] = b[2];
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(dst + int64_t(i) * Hp + c) = o[i];
+    }
+  }
+}
+
+template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack(PackArgs a, Targets t) {
+  constexpr int PL = DT == D_FP32 ? 3 : 1;
+  const int lane = threadIdx.x & 63;
+  const int active = a.counts->active, end = (active + kUnit - 1) / kUnit * kUnit;
+  const int K = t.K ? t.K : 1;
+  for (int64_t i = int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64; i < a.Tpad; i += int64_t(gridDim.x) * kRowWaves) {
+    const int64_t r = i < a.T ? a.rows[i] : -1;
+    __bf16* dst = reinterpret_cast<__bf16*>(a.hp) + i * PL * a.Hp;
+    if (i < active) {
+      pack_row<DT>(a.hidden, r * a.ld, a.H, a.Hp, dst, lane);
+    } else if (i < end) {
+      for (int c = lane * 8; c < PL * a.Hp; c += 512) *reinterpret_cast<bf16x8*>(dst + c) = bf16x8{};
+    }
+    if (i < end)
+      for (int k = lane; k < K; k += 64) {
+        int32_t at = -1;
+        if (i < active) {
+          const int64_t id = t.K ? id_at(t.ids, t.wide, r * t.ids_ld + k) : id_at(t.ids, t.wide, r);
+          if (id >= 0) {
+            const Piece& p = a.pieces[piece_of<false>(a.pieces, a.P, int32_t(id))];
+            at = p.start + int32_t(id) - p.first;
+          }
+        }
+        a.idt[int64_t(k) * a.Tpad + i] = at;
+      }
+    if (i >= active && r >= 0) {
+      if (a.each && lane == 0) a.each[r] = a.flags[r] == F_BAD ? NAN : 0.f;
+      if (a.dh)
+        for (int c = lane; c < a.H; c += 64) {
+          if constexpr (DT == D_BF16) static_cast<uint16_t*>(a.dh)[r * a.dh_ld + c] = 0;
+          else static_cast<float*>(a.dh)[r * a.dh_ld + c] = 0;
+        }
+    }
+  }
+}
+
+// Output matrix pieces as bf16 terms (fp32 pieces, and bf16 ones that 16-byte loads do not fit), row v of the
+// padded vocabulary at out + v * PL * Hp; `pieces` is then pointed there.
+template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack_pieces(const Piece* pieces, Piece* packed, int P, int64_t Vp, int H, int Hp, char* out) {
+  constexpr int PL = DT == D_FP32 ? 3 : 1;
+  const int lane = threadIdx.x & 63;
+  if (blockIdx.x == 0)
+    for (int p = threadIdx.x; p < P; p += kRowWaves * 64) {
+      Piece q = pieces[p];
+      q.w = out + int64_t(q.start) * PL * Hp * 2;
+      q.ld = int64_t(PL) * Hp;
+      packed[p] = q;
+    }
+  for (int64_t v = int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64; v < Vp; v += int64_t(gridDim.x) * kRowWaves) {
+    const Piece& p = pieces[piece_of<true>(pieces, P, int32_t(v))];
+    const int64_t r = v - p.start;
+    if (r < p.rows) pack_row<DT>(p.w, r * p.ld, H, Hp, reinterpret_cast<__bf16*>(out) + v * PL * Hp, lane);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// matrix products
+// ----------------------------------------------------------------------------
+// Out[n][m] = sum_k X[m][k] Y[n][k], m along the outputs' rows. Tiles of BM x BN outputs are kept by WM x WN waves
+// in the accumulators of 16 x 16 x 32 products (a lane holds four consecutive m of one n); operands come through
+// LDS in slices of kBK, loaded straight into it.
+//
+// A slice lies in LDS either as rows of 64 k (128 bytes; "along k") or as k rows of the tile's columns ("across").
+// The loads write LDS in lane order, so the swizzle that spreads the reads over the banks is in which 16
+// bytes a lane loads: along k, chunk c of row r lies at c ^ (r / 2 % 8); across, the 32 bytes c of k row r lie at
+// c ^ (r % 4 + 4 (r / 8 % 4)), and the reads transpose.
+enum Dir { S_LOGITS = 0, S_HIDDEN = 1, S_WEIGHT = 2 };
+
+template <int BM_, int BN_, int WM_, int WN_, int WAVES_> struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kThreads = WM * WN * 64;
+  static constexpr int MW = BM / WM, NW = BN / WN;  // a wave's part
+  static constexpr int FM = MW / 16, FN = NW / 16;
+  static constexpr int kWaves = WAVES_;  // of a SIMD, which bounds the registers
+  static constexpr int kX = BM * kBK * 2, kY = BN * kBK * 2, kStage = kX + kY;
+};
+using TileL = Tile<256, 256, 2, 4, 2>;
+using TileM = Tile<128, 128, 2, 2, 2>;
+using TileS = Tile<128, 32, 4, 1, 4>;
+
+struct Product {
+  const Piece* pieces;
+  const Counts* counts;
+  int32_t P, H, Hp, Vp, mtiles, planes, splits;
+  int32_t chunk, chunk_rows;  // this call's rows: [chunk, chunk + chunk_rows) of those that take part
+  int32_t kend;               // elements of a row along H that exist
+  const char* hp;             // gathered hidden rows
+  char* d;                    // [rows][planes * Vp]: exp(z - m), then D
+  // logits
+  float scale;
+  float2* stats;  // [Vp / BM][ld_stats]
+  int64_t ld_stats;
+  const int32_t* idt;
+  int64_t ld_idt;
+  int32_t K;
+  float* zt;  // [rows][K]
+  // gradients
+  const int32_t* rows;
+  void* dh;
+  int64_t dh_ld;
+  float* part;  // fp32 partials [split][n][Hp], or null: write the outputs
+  int64_t part_stride;
+  int32_t accumulate;
+};
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+
+__device__ __forceinline__ Rsrc rsrc_of(const char* base, int64_t bytes) {
+  const int64_t most = 0x7ffffff0;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, int(bytes < 0 ? 0 : bytes < most ? bytes : most), 0x00020000);
+}
+constexpr int kLoadsDone = 0x0f70;  // s_waitcnt vmcnt(0)
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: such a lane loads zeros
+
+// R rows of 128 bytes along k; of a row, `left` elements exist.
+template <int R, int THREADS> __device__ __forceinline__ void load_along(AR_LDS char* lds, Rsrc r, uint32_t ldb, int left, int tid) {
+  const int wave = tid / 64;
+  const uint32_t row = uint32_t(tid) / 8, c = (uint32_t(tid) % 8) ^ (row / 2 % 8);
+  const uint32_t off = int(c * 8) < left ? row * ldb + c * 16 : kNowhere;  // (the bounds check leaves a scalar offset out)
+#pragma unroll
+  for (int i = 0; i < (R * 8 + THREADS - 1) / THREADS; ++i)
+    if (R * 8 % THREADS == 0 || i * THREADS + wave * 64 < R * 8)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (AR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16, off + i * (THREADS / 8) * ldb, 0, 0, 0);
+}
+
+template <int R> __device__ __forceinline__ uint32_t across_swizzle(uint32_t krow) { return (krow % 4 + krow / 8 % 4 * 4) & (R / 16 - 1); }
+
+// kBK rows of R columns.
+template <int R, int THREADS> __device__ __forceinline__ void load_across(AR_LDS char* lds, Rsrc r, uint32_t ldb, int tid) {
+  const int wave = tid / 64;
+  constexpr int C = R / 8;
+#pragma unroll
+  for (int i = 0; i < (kBK * C + THREADS - 1) / THREADS; ++i)
+    if (kBK * C % THREADS == 0 || i * THREADS + wave * 64 < kBK * C) {
+      const uint32_t q = i * THREADS + tid, krow = q / C, slot = q % C;
+      const uint32_t c = ((slot / 2) ^ across_swizzle<R>(krow)) * 2 + slot % 2;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (AR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16, krow * ldb + c * 16, 0, 0, 0);
+    }
+}
+
+// The operand of one product: 16 rows from `base`, k 32 kk + 8 (lane / 16) on.
+__device__ __forceinline__ bf16x8 read_along(AR_LDS const char* lds, int base, int kk, int lane) {
+  const int row = base + lane % 16, c = (kk * 4 + lane / 16) ^ (lane % 16 / 2);
+  return *reinterpret_cast<AR_LDS const bf16x8*>(lds + row * 128 + c * 16);
+}
+template <int R> __device__ __forceinline__ bf16x8 read_across(AR_LDS char* lds, int base, int kk, int lane) {
+  const uint32_t krow = kk * 32 + lane / 16 * 8 + lane % 16 / 4;
+  AR_LDS char* p = lds + krow * (R * 2) + ((base / 16) ^ across_swizzle<R>(krow)) * 32 + lane % 4 * 8;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((AR_LDS s16x4*)p);
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((AR_LDS s16x4*)(p + 4 * R * 2));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
+}
+
+// Which terms of X and Y the passes over k multiply: the small ones first.
+__device__ __forceinline__ int plane_x(int pass, int planes) { return planes == 1 ? 0 : (0x001102 >> (pass * 4)) & 15; }
+__device__ __forceinline__ int plane_y(int pass, int planes) { return planes == 1 ? 0 : (0x010120 >> (pass * 4)) & 15; }
+
+// A value that every lane of a wave holds, where the compiler has to know it.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+  return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(x)))) | uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(x >> 32)))) << 32);
+}
+
+// Loads a product's slices into LDS, one after the other.
+template <class C, int DIR> struct Stager {
+  static constexpr bool kXAlong = DIR == S_LOGITS, kYAlong = DIR != S_WEIGHT;
+  const Product& a;
+  int m0, n0, tid, steps;  // steps of one pass over the depth
+  // the piece of the output matrix that is being read: its rows are [start, start + rows) of the padded vocabulary
+  const char* w;
+  int64_t ld;
+  int rows, start, next;
+
+  __device__ __forceinline__ void take(int p) {
+    const Piece& q = a.pieces[p];
+    w = reinterpret_cast<const char*>(uniform(reinterpret_cast<int64_t>(q.w)));
+    ld = uniform(q.ld);
+    rows = __builtin_amdgcn_readfirstlane(q.rows);
+    start = __builtin_amdgcn_readfirstlane(q.start);
+    next = p + 1 < a.P ? __builtin_amdgcn_readfirstlane(a.pieces[p + 1].start) : 0x7fffffff;
+  }
+  __device__ __forceinline__ void take_at(int32_t v) { take(__builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, v))); }
+
+  __device__ __forceinline__ void load(AR_LDS char* lds, int s) {
+    const int pass = s / steps, k = (s - pass * steps) * kBK;
+    const int px = plane_x(pass, a.planes), py = plane_y(pass, a.planes);
+    const int64_t ldh = int64_t(a.planes) * a.Hp, ldd = int64_t(a.planes) * a.Vp;
+    if constexpr (DIR == S_LOGITS) {
+      const int64_t r = m0 - start;
+      load_along<C::BM, C::kThreads>(lds, rsrc_of(w + (r * ld + int64_t(px) * a.Hp + k) * 2, ((rows - r - 1) * ld + a.kend - k) * 2), uint32_t(ld * 2), a.kend - k, tid);
+      load_along<C::BN, C::kThreads>(lds + C::kX, rsrc_of(a.hp + (int64_t(a.chunk + n0) * ldh + int64_t(py) * a.Hp + k) * 2, 0x7ffffff0), uint32_t(ldh * 2), kBK, tid);
+    } else if constexpr (DIR == S_HIDDEN) {
+      if (k < start || k >= next) take_at(k);
+      const int64_t r = k - start;
+      load_across<C::BM, C::kThreads>(lds, rsrc_of(w + (r * ld + int64_t(px) * a.Hp + m0) * 2, r < rows ? ((rows - r - 1) * ld + a.kend - m0) * 2 : 0), uint32_t(ld * 2), tid);
+      load_along<C::BN, C::kThreads>(lds + C::kX, rsrc_of(a.d + (int64_t(n0) * ldd + int64_t(py) * a.Vp + k) * 2, 0x7ffffff0), uint32_t(ldd * 2), kBK, tid);
+    } else {
+      // columns past a row's end are the next row's: they meet outputs that nothing keeps
+      load_across<C::BM, C::kThreads>(lds, rsrc_of(a.hp + (int64_t(a.chunk + k) * ldh + int64_t(px) * a.Hp + m0) * 2, (kBK * ldh - int64_t(px) * a.Hp - m0) * 2), uint32_t(ldh * 2), tid);
+      load_across<C::BN, C::kThreads>(lds + C::kX, rsrc_of(a.d + (int64_t(k) * ldd + int64_t(py) * a.Vp + n0) * 2, 0x7ffffff0), uint32_t(ldd * 2), tid);
+    }
+  }
+};
+
+template <class C, int DIR, class ACC> __device__ __forceinline__ void multiply(AR_LDS char* lds, ACC& acc, int wm, int wn, int lane) {
+  using St = Stager<C, DIR>;
+  AR_LDS char* y = lds + C::kX;
+#pragma unroll
+  for (int kk = 0; kk < kBK / 32; ++kk) {
+    bf16x8 xf[C::FM], yf[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      if constexpr (St::kYAlong) yf[j] = read_along(y, wn * C::NW + j * 16, kk, lane);
+      else yf[j] = read_across<C::BN>(y, wn * C::NW + j * 16, kk, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      if constexpr (St::kXAlong) xf[i] = read_along(lds, wm * C::MW + i * 16, kk, lane);
+      else xf[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, kk, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], yf[j], acc[i][j], 0, 0, 0);
+  }
+}
+
+// Four consecutive outputs of a row, of which `left` exist.
+template <int DT> __device__ __forceinline__ void put4(void* row, int m, f32x4 v, int left) {
+  if constexpr (DT == D_BF16) {
+    __bf16* p = static_cast<__bf16*>(row) + m;
+    const bf16x4 b = __builtin_convertvector(v, bf16x4);
+    typedef __bf16 U __attribute__((ext_vector_type(4), aligned(2)));
+    if (left >= 4) *reinterpret_cast<U*>(p) = b;
+    else
+      for (int e = 0; e < left; ++e) p[e] = b[e];
+  } else {
+    float* p = static_cast<float*>(row) + m;
+    typedef float U __attribute__((ext_vector_type(4), aligned(4)));
+    if (left >= 4) *reinterpret_cast<U*>(p) = v;
+    else
+      for (int e = 0; e < left; ++e) p[e] = v[e];
+  }
+}
+
+__device__ __forceinline__ int chunk_active(const Product& a) { return min(max(a.counts->active - a.chunk, 0), a.chunk_rows); }
+
+// KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
+// the outputs' type.
+template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
+  __shared__ __attribute__((aligned(16))) char shared[2 * C::kStage];
+  AR_LDS char* lds = (AR_LDS char*)shared;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64), wm = wave % C::WM, wn = wave / C::WM;
+  const int active = chunk_active(a);
+  const int nlen = DIR == S_WEIGHT ? a.Vp : active;
+  const int ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles;
+  const int64_t tiles = int64_t(ntiles) * mtiles;
+  const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + kBK - 1) / kBK * kBK;
+  const int passes = a.planes == 1 ? 1 : 6;
+  const int steps = depth / kBK;
+  for (int64_t t = blockIdx.x; t < tiles * a.splits; t += gridDim.x) {
+    const int split = int(t / tiles);
+    // Workgroups go to the eight dies in turn: each die gets a run of tiles, and of a run eight tiles of n share
+    // their m with the neighbours, so that both operands are found in the die's cache.
+    int64_t u = t - split * tiles;
+    {
+      const int64_t per = tiles / 8, more = tiles % 8, die = u % 8, i = u / 8;
+      u = die * per + min(die, more) + i;
+    }
+    const int64_t group = u / (8 * int64_t(mtiles));
+    const int in_group = int(u - group * 8 * mtiles), width = min(8, ntiles - int(group) * 8);
+    const int m0 = in_group / width * C::BM, n0 = (int(group) * 8 + in_group % width) * C::BN;
+
+    Stager<C, DIR> st{a, m0, n0, tid, steps};
+    st.start = st.next = 0;
+    if constexpr (DIR == S_LOGITS) st.take_at(m0);
+    const int all = steps * passes;
+    const int s0 = int(int64_t(all) * split / a.splits), s1 = int(int64_t(all) * (split + 1) / a.splits);
+
+    f32x4 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    if (s0 < s1) {
+      st.load(lds, s0);
+      for (int s = s0; s < s1; ++s) {
+        __builtin_amdgcn_s_waitcnt(kLoadsDone);
+        __syncthreads();  // this slice is in LDS, the other one has been read
+        if (s + 1 < s1) st.load(lds + ((s + 1 - s0) & 1) * C::kStage, s + 1);
+        multiply<C, DIR>(lds + ((s - s0) & 1) * C::kStage, acc, wm, wn, lane);
+      }
+    }
+    __syncthreads();
+
+    if constexpr (DIR == S_LOGITS) {
+      AR_LDS float* top = (AR_LDS float*)lds;         // [WM][BN]
+      AR_LDS float* sum = top + C::WM * C::BN;        // [WM][BN]
+      const int left = st.rows - (m0 - st.start) - wm * C::MW - lane / 16 * 4;
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = i * 16 + e < left ? acc[i][j][e] * a.scale : -INFINITY;
+      // the logits of the rows' own ids
+      const int wn0 = n0 + wn * C::NW, wm0 = m0 + wm * C::MW;
+      for (int k = 0; k < a.K; ++k) {
+        int rel = -1;
+        if (lane < C::NW && wn0 + lane < active) rel = a.idt[k * a.ld_idt + a.chunk + wn0 + lane] - wm0;
+        uint64_t hit = __ballot(rel >= 0 && rel < C::MW);
+        while (hit) {
+          const int src = __builtin_ctzll(hit);
+          hit &= hit - 1;
+          const int r = __builtin_amdgcn_readlane(rel, src);
+          float v = 0;
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+              if (r / 16 == i && src / 16 == j) {
+                const f32x4 x = acc[i][j];
+                v = r % 4 == 0 ? x[0] : r % 4 == 1 ? x[1] : r % 4 == 2 ? x[2] : x[3];
+              }
+          if (lane == r % 16 / 4 * 16 + src % 16) a.zt[int64_t(wn0 + src) * a.K + k] = v;
+        }
+      }
+      float mx[C::FN];
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
+        m = fmaxf(m, __shfl_xor(m, 16));
+        m = fmaxf(m, __shfl_xor(m, 32));
+        if (lane < 16) top[wm * C::BN + wn * C::NW + j * 16 + lane] = m;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < C::WM; ++w) m = fmaxf(m, top[w * C::BN + wn * C::NW + j * 16 + lane % 16]);
+        mx[j] = m == -INFINITY ? 0.f : m;  // a tile without rows of the vocabulary: exponentials of 0
+        float s = 0;
+        const int64_t n = n0 + wn * C::NW + j * 16 + lane % 16;
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+          f32x4 x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[e] = exp_of(acc[i][j][e] - mx[j]);
+            s += x[e];
+          }
+          const int64_t at = int64_t(n) * a.Vp + wm0 + i * 16 + lane / 16 * 4;
+          if constexpr (KEEP == D_BF16) *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(a.d) + at) = __builtin_convertvector(x, bf16x4);
+          if constexpr (KEEP == D_FP32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.part) + at) = x;
+        }
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (lane < 16) sum[wm * C::BN + wn * C::NW + j * 16 + lane] = s;
+      }
+      __syncthreads();
+      if (wm == 0 && lane < 16)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) {
+          const int n = wn * C::NW + j * 16 + lane;
+          float s = 0;
+#pragma unroll
+          for (int w = 0; w < C::WM; ++w) s += sum[w * C::BN + n];
+          a.stats[int64_t(m0 / C::BM) * a.ld_stats + n0 + n] = float2{mx[j], s};
+        }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) {
+        const int n = n0 + wn * C::NW + j * 16 + lane % 16;
+        if (n >= nlen) continue;
+        char* row = nullptr;
+        if (!a.part) {
+          constexpr int e = KEEP == D_BF16 ? 2 : 4;
+          if constexpr (DIR == S_HIDDEN) {
+            row = static_cast<char*>(a.dh) + int64_t(a.rows[a.chunk + n]) * a.dh_ld * e;
+          } else {
+            const Piece& p = a.pieces[piece_of<true>(a.pieces, a.P, n)];
+            if (n - p.start >= p.rows) continue;
+            row = p.dw + int64_t(n - p.start) * p.dld * e;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+          const int m = m0 + wm * C::MW + i * 16 + lane / 16 * 4;
+          if (a.part) {
+            if (m < a.Hp) {
+              f32x4* q = reinterpret_cast<f32x4*>(a.part + split * a.part_stride + int64_t(n) * a.Hp + m);
+              *q = a.accumulate ? *q + acc[i][j] : acc[i][j];
+            }
+          } else if (m < a.H) {
+            put4<KEEP>(row, m, acc[i][j], a.H - m);
+          }
+        }
+      }
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------
+// softmax statistics, D, losses
+// ----------------------------------------------------------------------------
+struct Soft {
+  const Counts* counts;
+  const int32_t* rows;
+  const float* weights;
+  const float2* stats;
+  int64_t ld_stats;
+  int32_t blocks, chunk, chunk_rows, reduction;
+  int32_t planes, block;  // block: columns a statistic covers
+  int64_t Vp;
+  float temperature;
+  float* lse;    // [chunk rows]
+  float* coef;   // [chunk rows]: the row's weight in the loss over the temperature; 0 behind the rows
+  float* exps;   // fp32: exp(z - m)
+  char* d;
+};
+
+// 16 rows a workgroup: a wave's lanes are 16 rows x 4 statistics, and its 16 waves share the statistics.
+constexpr int kJoinThreads = 1024, kJoinRows = 16;
+__global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a) {
+  __shared__ float2 part[kJoinThreads / 16][kJoinRows];
+  const int row = threadIdx.x % 16, slice = threadIdx.x / 16;
+  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + kUnit - 1) / kUnit * kUnit;
+  for (int r0 = blockIdx.x * kJoinRows; r0 < end; r0 += gridDim.x * kJoinRows) {
+    const int r = r0 + row;
+    float m = -INFINITY, s = 0;
+    if (r < active)
+      for (int b = slice; b < a.blocks; b += kJoinThreads / 16) {
+        const float2 x = a.stats[int64_t(b) * a.ld_stats + r];
+        if (x.y == 0) continue;
+        const float top = fmaxf(m, x.x);  // a NaN sum stays one
+        s = (m == top ? s : s * expf(m - top)) + (x.x == top ? x.y : x.y * expf(x.x - top));
+        m = top;
+      }
+    part[slice][row] = float2{m, s};
+    __syncthreads();
+    if (threadIdx.x < kJoinRows) {
+      float lse = 0, coef = 0;
+      if (r < active) {
+        float top = -INFINITY;
+        for (int w = 0; w < kJoinThreads / 16; ++w) top = fmaxf(top, part[w][row].x);
+        float all = 0;
+        for (int w = 0; w < kJoinThreads / 16; ++w) {
+          const float2 x = part[w][row];
+          if (x.y != 0) all += x.y * expf(x.x - top);
+        }
+        lse = top + logf(all);
+        coef = 1.f / a.temperature;
+        if (a.weights) coef *= a.weights[a.rows[a.chunk + r]];
+        if (a.reduction == R_MEAN) coef /= float(a.counts->mean);
+      }
+      a.lse[r] = lse;
+      a.coef[r] = coef;
+    }
+    __syncthreads();
+  }
+}
+
+// exp(z - m) -> c p, 64 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
+constexpr int kNormThreads = 256, kNormRows = 64, kNormCols = 512;
+template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a) {
+  constexpr int kBlocks = kNormCols / 128;
+  __shared__ float factor[kNormRows][kBlocks];
+  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + kNormRows - 1) / kNormRows;
+  const int64_t cols = (a.Vp + kNormCols - 1) / kNormCols, tiles = cols * end;
+  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const int r0 = int(t / cols) * kNormRows;
+    const int64_t c0 = (t % cols) * kNormCols;
+    {
+      const int r = threadIdx.x % kNormRows, b = threadIdx.x / kNormRows;
+      const int64_t c = c0 + b * 128;
+      float f = 0;
+      const float w = a.coef[r0 + r];
+      if (w != 0 && c < a.Vp) f = exp_of(a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r]) * w;
+      factor[r][b] = f;
+    }
+    __syncthreads();
+    constexpr int kLanes = kNormCols / 8;
+    const int c8 = threadIdx.x % kLanes * 8;
+    if (c0 + c8 < a.Vp)
+      for (int r = threadIdx.x / kLanes; r < kNormRows; r += kNormThreads / kLanes) {
+        const float f = factor[r][c8 / 128];
+        const bool there = r0 + r < active;
+        if constexpr (DT == D_BF16) {
+          bf16x8* p = reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8);
+          bf16x8 v = {};
+          if (there) {
+            v = *p;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __bf16(float(v[j]) * f);
+          }
+          *p = v;
+        } else {
+          const float* s = a.exps + int64_t(r0 + r) * a.Vp + c0 + c8;
+          bf16x8 o[3];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            __bf16 b[3];
+            split3(there ? s[j] * f : 0.f, b);
+            o[0][j] = b[0];
+            o[1][j] = b[1];
+            o[2][j] = b[2];
+          }
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + (int64_t(r0 + r) * 3 + i) * a.Vp + c0 + c8) = o[i];
+        }
+      }
+    __syncthreads();
+  }
+}
+
+// A wave per row: the row's loss, and D at the row's own ids: c (p - q), q summed over equal ids.
+struct Ends {
+  const float2* teacher;  // by original row
+  const int32_t* idt;
+  int64_t ld_idt;
+  const float* zt;
+  float* row_loss;  // [rows that take part], weighted
+  float* each;      // by original row, or null
+  bool grad;
+};
+template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_targets(Soft a, Ends e, Targets t) {
+  const int lane = threadIdx.x & 63, active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows);
+  const int K = t.K ? t.K : 1;
+  for (int i = blockIdx.x * kRowWaves + threadIdx.x / 64; i < active; i += gridDim.x * kRowWaves) {
+    const int64_t r = a.rows[a.chunk + i];
+    const float lse = a.lse[i], coef = a.coef[i];
+    float2 stat = {0, 1};
+    if (t.K) stat = e.teacher[r];
+    auto q_of = [&](int k, float* x) {
+      if (!t.K) return 1.f;
+      *x = logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) / t.temperature - stat.x;
+      return expf(*x) / stat.y;
+    };
+    float loss = 0;
+    for (int k = lane; k < K; k += 64) {
+      const int32_t id = e.idt[k * e.ld_idt + a.chunk + i];
+      if (id < 0) continue;
+      const float z = e.zt[int64_t(i) * K + k];
+      float x = 0;
+      const float q = q_of(k, &x);
+      if (q != 0) loss += q * ((t.K ? x - logf(stat.y) : 0.f) + (lse - z));
+      if (e.grad) {
+        float all = q;
+        if (t.K) {
+          all = 0;
+          for (int l = 0; l < K; ++l) {
+            float y;
+            if (e.idt[l * e.ld_idt + a.chunk + i] == id) all += q_of(l, &y);
+          }
+        }
+        const float d = coef * (expf(z - lse) - all);
+        __bf16* row = reinterpret_cast<__bf16*>(a.d) + (DT == D_BF16 ? int64_t(i) * a.Vp : int64_t(i) * 3 * a.Vp);
+        if constexpr (DT == D_BF16) {
+          row[id] = __bf16(d);
+        } else {
+          __bf16 b[3];
+          split3(d, b);
+#pragma unroll
+          for (int j = 0; j < 3; ++j) row[j * a.Vp + id] = b[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
+    if (lane == 0) {
+      if (a.weights) loss *= a.weights[r];
+      if (e.each) e.each[r] = loss;
+      else e.row_loss[a.chunk + i] = loss;
+    }
+  }
+}
+
+// The call's loss: the rows' in 64 bits, in an order that their number fixes.
+__global__ __launch_bounds__(1024) void k_vocab_loss(const float* row_loss, const Counts* counts, int reduction, float* out) {
+  __shared__ double wave[16];
+  double s = 0;
+  for (int i = threadIdx.x; i < counts->active; i += 1024) s += double(row_loss[i]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) s += __shfl_down(s, d);
+  if (threadIdx.x % 64 == 0) wave[threadIdx.x / 64] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0;
+    for (int w = 0; w < 16; ++w) s += wave[w];
+    if (reduction == R_MEAN && counts->mean) s /= counts->mean;
+    *out = counts->bad ? NAN : float(s);
+  }
+}
+
+// Partial gradients [splits][n][Hp] joined in order, into the outputs.
+template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Product a) {
+  const int n_end = DIR == S_WEIGHT ? a.Vp : chunk_active(a), per = a.Hp / 4;
+  const int64_t all = int64_t(n_end) * per;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
+    const int n = int(i / per), m = int(i % per) * 4;
+    if (m >= a.H) continue;
+    char* row;
+    constexpr int e = DT == D_BF16 ? 2 : 4;
+    if constexpr (DIR == S_HIDDEN) {
+      row = static_cast<char*>(a.dh) + int64_t(a.rows[a.chunk + n]) * a.dh_ld * e;
+    } else {
+      const Piece& p = a.pieces[piece_of<true>(a.pieces, a.P, n)];
+      if (n - p.start >= p.rows) continue;
+      row = p.dw + int64_t(n - p.start) * p.dld * e;
+    }
+    f32x4 s = {0, 0, 0, 0};
+    for (int k = 0; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(a.part + k * a.part_stride + int64_t(n) * a.Hp + m);
+    put4<DT>(row, m, s, a.H - m);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// host
+// ----------------------------------------------------------------------------
+size_t up(size_t n, size_t unit = 256) { return (n + unit - 1) / unit * unit; }
+int64_t blocks_of(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(n, std::min<int64_t>(launch_blocks(), int64_t(1) << 22))); }
+
+enum Size { Z_S = 0, Z_M = 1, Z_L = 2 };
+
+// Scratch of D and the exponentials that one chunk of tokens may take.
+constexpr int64_t kChunkBytes = int64_t(4) << 30;
+constexpr int kUnits = 256;  // compute units
+
+struct Plan {
+  int planes, Hp, K;
+  int64_t V = 0, Vp = 0, Tpad, Tc, chunks;
+  bool packed;
+  Size logits, hidden, weight;
+  int hidden_splits = 1, weight_splits = 1;
+  int block;  // columns a statistic covers
+  // offsets in the workspace
+  size_t counts, pieces, packed_pieces, rows, flags, teacher, idt, hp, wp, lse, coef, row_loss, zt, stats, exps, d, part, bytes;
+};
+
+int64_t tiles_of(Size z, int64_t m, int64_t n) {
+  const int64_t bm = z == Z_L ? 256 : 128, bn = z == Z_L ? 256 : z == Z_M ? 128 : 32;
+  return ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
+}
+
+Size size_for(int64_t m, int64_t n, int64_t splits) {
+  if (n <= 64) return Z_S;
+  return tiles_of(Z_L, m, n) * splits >= kUnits * 3 / 4 ? Z_L : Z_M;
+}
+
+// How often a product's depth is split so that its tiles fill the device.
+int splits_for(int64_t tiles, int64_t steps, int64_t part_bytes) {
+  const int64_t want = (2 * kUnits) / std::max<int64_t>(tiles, 1), most = std::min<int64_t>(steps / 4, (int64_t(256) << 20) / std::max<int64_t>(part_bytes, 1));
+  return int(std::max<int64_t>(1, std::min(want, most)));
+}
+
+Plan plan_of(const Vocab& v, bool grad) {
+  Plan p{};
+  p.planes = v.dtype == D_FP32 ? 3 : 1;
+  p.Hp = int(up(size_t(v.H), kBK));
+  p.K = std::max(1, v.top);
+  p.packed = v.dtype == D_FP32 || v.H % 8;
+  for (const VocabPiece& q : v.pieces) {
+    p.V += q.rows;
+    p.Vp += int64_t(up(size_t(q.rows), kUnit));
+    if (reinterpret_cast<uintptr_t>(q.w) % 16 || q.ld % 8 || q.ld >= (1 << 21)) p.packed = true;
+  }
+  p.Tpad = int64_t(up(size_t(std::max<int64_t>(v.T, 1)), kUnit));
+  // a chunk's scratch: statistics at their finest, and with gradients the exponentials and D
+  const int64_t per = p.Vp / 128 * 8 + (grad ? (v.dtype == D_FP32 ? 10 : 2) * p.Vp : 0);
+  p.Tc = std::min(p.Tpad, std::max<int64_t>(kUnit, kChunkBytes / per / kUnit * kUnit));
+  p.chunks = (p.Tpad + p.Tc - 1) / p.Tc;
+  const int64_t n = std::min(p.Tc, v.T), passes = p.planes == 1 ? 1 : 6;
+  p.logits = size_for(p.Vp, n, 1);
+  p.block = p.logits == Z_L ? 256 : 128;
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t o = at; at += up(bytes); return o; };
+  p.counts = take(sizeof(Counts));
+  p.pieces = take(sizeof(Piece) * v.pieces.size());
+  p.packed_pieces = take(p.packed ? sizeof(Piece) * v.pieces.size() : 0);
+  p.rows = take(size_t(p.Tpad) * 4);
+  p.flags = take(size_t(p.Tpad));
+  p.teacher = take(v.top ? size_t(p.Tpad) * 8 : 0);
+  p.idt = take(size_t(p.K) * size_t(p.Tpad) * 4);
+  p.hp = take(size_t(p.Tpad) * size_t(p.planes) * size_t(p.Hp) * 2);
+  p.wp = take(p.packed ? size_t(p.Vp) * size_t(p.planes) * size_t(p.Hp) * 2 : 0);
+  p.lse = take(size_t(p.Tc) * 4);
+  p.coef = take(size_t(p.Tc) * 4);
+  p.row_loss = take(size_t(p.Tpad) * 4);
+  p.zt = take(size_t(p.Tc) * size_t(p.K) * 4);
+  p.stats = take(size_t(p.Vp / p.block) * size_t(p.Tc) * 8);
+  if (grad) {
+    p.exps = take(v.dtype == D_FP32 ? size_t(p.Tc) * size_t(p.Vp) * 4 : 0);
+    p.d = take(size_t(p.Tc) * size_t(p.Vp) * size_t(p.planes) * 2);
+    p.hidden = size_for(v.H, n, p.Vp / kBK * passes / 8);
+    p.hidden_splits = splits_for(tiles_of(p.hidden, v.H, n), p.Vp / kBK * passes, n * p.Hp * 4);
+    p.weight = size_for(v.H, p.Vp, 1);
+    if (p.chunks == 1) p.weight_splits = splits_for(tiles_of(p.weight, v.H, p.Vp), (n + kBK - 1) / kBK * passes, p.Vp * p.Hp * 4);
+    const size_t dh = p.hidden_splits > 1 ? size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp) * 4 : 0;
+    const size_t dw = p.weight_splits > 1 || p.chunks > 1 ? size_t(p.weight_splits) * size_t(p.Vp) * size_t(p.Hp) * 4 : 0;
+    p.part = take(p.chunks > 1 ? dh + dw : std::max(dh, dw));  // chunks add to dW's across dh's
+  }
+  p.bytes = at;
+  return p;
+}
+
+template <int DIR, int KEEP> void launch_product(Sequence& s, Size z, int64_t blocks, Product a) {
+  if (z == Z_L) s.launch(k_vocab_product<TileL, DIR, KEEP>, blocks, TileL::kThreads, a);
+  else if (z == Z_M) s.launch(k_vocab_product<TileM, DIR, KEEP>, blocks, TileM::kThreads, a);
+  else if constexpr (DIR != S_WEIGHT) s.launch(k_vocab_product<TileS, DIR, KEEP>, blocks, TileS::kThreads, a);
+}
+
+template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, hipStream_t st) {
+  char* ws = static_cast<char*>(v.workspace);
+  Sequence s{st, {static_cast<hipEvent_t>(v.start_event), static_cast<hipEvent_t>(v.stop_event)}, 0};
+  const int64_t P = int64_t(v.pieces.size());
+  const bool each = v.reduction == R_NONE;
+  const int64_t per_chunk = 3 + (grad ? 3 + (p.hidden_splits > 1) + (p.chunks == 1 && p.weight_splits > 1) : 0);
+  s.left = (P + kPieceTab - 1) / kPieceTab + (v.top ? 1 : 0) + 2 + (p.packed ? 1 : 0) + p.chunks * per_chunk +
+           (grad && p.chunks > 1 ? 1 : 0) + (each ? 0 : 1);
+  Piece* pieces = reinterpret_cast<Piece*>(ws + p.pieces);
+  Counts* counts = reinterpret_cast<Counts*>(ws + p.counts);
+  int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
+  uint8_t* flags = reinterpret_cast<uint8_t*>(ws + p.flags);
+  float2* teacher = reinterpret_cast<float2*>(ws + p.teacher);
+  int64_t first = 0, start = 0;
+  for (int64_t i0 = 0; i0 < P; i0 += kPieceTab) {
+    PieceTab tab;
+    tab.at = int32_t(i0);
+    tab.count = int32_t(std::min<int64_t>(kPieceTab, P - i0));
+    for (int i = 0; i < tab.count; ++i) {
+      const VocabPiece& q = v.pieces[size_t(i0 + i)];
+      tab.p[i] = Piece{static_cast<const char*>(q.w), static_cast<char*>(q.dw), q.ld, q.dld, int32_t(q.rows), int32_t(start), int32_t(first), 0};
+      first += q.rows;
+      start += int64_t(up(size_t(q.rows), kUnit));
+    }
+    s.launch(k_vocab_pieces, 1, 64, tab, pieces);
+  }
+  const Targets t{v.ids, v.logits, v.token_weights, v.ids_ld, v.logits_ld, v.ignore, p.V, v.top, v.logits_dtype, v.wide_ids, v.temperature};
+  const int64_t row_blocks = (p.Tpad + kRowWaves - 1) / kRowWaves;
+  if (v.top) s.launch(k_vocab_teacher, blocks_of(row_blocks), kRowWaves * 64, t, v.T, teacher, flags);
+  s.launch(k_vocab_scan, 1, kScanThreads, t, v.T, rows, flags, counts);
+  const PackArgs pa{v.hidden, v.ld, v.T, p.Tpad, int32_t(v.H), p.Hp, int32_t(P), pieces, rows, flags, counts, ws + p.hp,
+                    reinterpret_cast<int32_t*>(ws + p.idt), grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
+  s.launch(k_vocab_pack<DT>, blocks_of(row_blocks), kRowWaves * 64, pa, t);
+  if (p.packed) {
+    Piece* packed = reinterpret_cast<Piece*>(ws + p.packed_pieces);
+    s.launch(k_vocab_pack_pieces<DT>, blocks_of(p.Vp / kRowWaves), kRowWaves * 64, pieces, packed, int(P), p.Vp, int(v.H), p.Hp, ws + p.wp);
+    pieces = packed;
+  }
+  Product a{};
+  a.pieces = pieces;
+  a.counts = counts;
+  a.P = int32_t(P);
+  a.H = int32_t(v.H);
+  a.Hp = p.Hp;
+  a.Vp = int32_t(p.Vp);
+  a.planes = p.planes;
+  a.kend = p.packed ? p.Hp : int32_t(v.H);
+  a.hp = ws + p.hp;
+  a.d = ws + p.d;
+  a.scale = 1.f / v.temperature;
+  a.stats = reinterpret_cast<float2*>(ws + p.stats);
+  a.ld_stats = p.Tc;
+  a.idt = pa.idt;
+  a.ld_idt = p.Tpad;
+  a.K = p.K;
+  a.zt = reinterpret_cast<float*>(ws + p.zt);
+  a.rows = rows;
+  a.dh = v.dh;
+  a.dh_ld = v.dh_ld;
+  Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
+         v.temperature, reinterpret_cast<float*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
+  const Ends ends{teacher, pa.idt, p.Tpad, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, grad};
+  float* dh_part = reinterpret_cast<float*>(ws + p.part);
+  float* dw_part = dh_part;
+  if (p.chunks > 1 && p.hidden_splits > 1) dw_part += size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp);
+  for (int64_t c = 0; c < p.chunks; ++c) {
+    a.chunk = f.chunk = int32_t(c * p.Tc);
+    a.chunk_rows = f.chunk_rows = int32_t(std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)));
+    const int64_t n = a.chunk_rows, npad = int64_t(up(size_t(n), kUnit));
+    a.mtiles = int32_t(p.Vp / p.block);
+    a.splits = 1;
+    a.part = f.exps;
+    const int64_t lb = blocks_of(tiles_of(p.logits, p.Vp, n));
+    if (grad) launch_product<S_LOGITS, DT>(s, p.logits, lb, a);
+    else launch_product<S_LOGITS, 0>(s, p.logits, lb, a);
+    s.launch(k_vocab_join, blocks_of(npad / kJoinRows), kJoinThreads, f);
+    if (grad) s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f);
+    s.launch(k_vocab_targets<DT>, blocks_of((n + kRowWaves - 1) / kRowWaves), kRowWaves * 64, f, ends, t);
+    if (!grad) continue;
+    const auto mtiles = [&](Size z) { return int32_t(tiles_of(z, v.H, 1)); };
+    a.mtiles = mtiles(p.hidden);
+    a.splits = p.hidden_splits;
+    a.part = a.splits > 1 ? dh_part : nullptr;
+    a.part_stride = p.Tc * p.Hp;
+    a.accumulate = 0;
+    launch_product<S_HIDDEN, DT>(s, p.hidden, blocks_of(tiles_of(p.hidden, v.H, n) * a.splits), a);
+    if (a.splits > 1) s.launch(k_vocab_sum<S_HIDDEN, DT>, blocks_of((n * p.Hp / 4 + 255) / 256), 256, a);
+    a.mtiles = mtiles(p.weight);
+    a.splits = p.weight_splits;
+    a.part = a.splits > 1 || p.chunks > 1 ? dw_part : nullptr;
+    a.part_stride = p.Vp * p.Hp;
+    a.accumulate = c > 0;
+    launch_product<S_WEIGHT, DT>(s, p.weight, blocks_of(tiles_of(p.weight, v.H, p.Vp) * a.splits), a);
+    if (a.part && c + 1 == p.chunks) s.launch(k_vocab_sum<S_WEIGHT, DT>, blocks_of((p.Vp * p.Hp / 4 + 255) / 256), 256, a);
+  }
+  if (!each) s.launch(k_vocab_loss, 1, 1024, ends.row_loss, counts, v.reduction, v.loss);
+  return s.done("launching the vocabulary kernels");
+}
+
+}  // namespace
+
+size_t vocab_workspace(const Vocab& v, bool grad) { return plan_of(v, grad).bytes; }
+
+RunResult run_vocab(const Vocab& v, bool grad, void* stream) {
+  const Plan p = plan_of(v, grad);
+  if (v.workspace_bytes < p.bytes) {
+    RunResult r;
+    r.status = 3;
+    r.message = "workspace too small: need " + std::to_string(p.bytes) + " bytes";
+    return r;
+  }
+  const hipStream_t st = static_cast<hipStream_t>(stream);
+  return v.dtype == D_FP32 ? run_typed<D_FP32>(v, grad, p, st) : run_typed<D_BF16>(v, grad, p, st);
+}
+
+}  // namespace ar

@@ -400,6 +400,81 @@ ar_status ar_allreduce_clip(void* const* bufs, const int64_t* n, int32_t buckets
 ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, int32_t P, int32_t dtype,
                                             int32_t op, int32_t collective, const ar_clip* clip, size_t* bytes);
 
+/* ---- losses over a vocabulary in pieces ----
+ * The output layer of a model whose vocabulary is spread over P ranks, with its loss and gradients: hidden
+ * states h [T, H] against an output matrix W [V, H] whose rows (the vocabulary) lie in P pieces in rank order.
+ *   z_t  = h_t W^T / temperature        (V logits a token; never kept as a whole)
+ *   l_t  = log(sum_v exp(z_tv)),  p_t = exp(z_t - l_t)
+ *   cross entropy (top = 0), target y_t:       loss_t = w_t (l_t - z_ty)
+ *   distillation (top = K >= 1), a teacher's K logits and their ids a token: q_t = softmax of its logits /
+ *     temperature over the entries whose id is not negative,
+ *                                              loss_t = w_t sum_k q_tk (log q_tk - z_t,id(k) + l_t)
+ *   gradients of sum_t s loss_t:  d_t = s w_t (p_t - q_t) / temperature  (q_t at y_t or the ids; equal ids add up),
+ *     dh = d W (the sum over all pieces),  dW_p = d_p^T h;  s = 1 / N for AR_MEAN, 1 otherwise
+ *  - Rows left out: a target equal to `ignore`; a teacher's list whose ids are all negative or whose logits are all
+ *    -infinity. Their loss and their row of dh are 0, and their hidden states are not read (neither are those of
+ *    rows of weight 0, whose loss and gradients are 0 too). N counts the rows that are not left out, whatever
+ *    their weight; with N = 0 the loss is 0. Negative ids' logits are not used. An id outside the vocabulary
+ *    (>= V; for cross entropy also a negative one that is not `ignore`) makes its row's loss, and so the
+ *    call's, NaN, and gives no gradient.
+ *  - Precision: logits, softmax and losses are fp32 (a call's loss is summed in 64 bits). bf16: products of the
+ *    bf16 operands are exact and their sums fp32; d is rounded to bf16 twice (2^-8 of it together) before the
+ *    gradients' products, whose fp32 sums are rounded to bf16 once. fp32: operands are split into three bf16 terms
+ *    and six products of them summed, 2^-24 or so of a product. The order of every sum is fixed by the sizes, the
+ *    alignment, the device and ar_set_launch_blocks(), so a call gives the same bits on every run.
+ *  - Stream, errors, capture: as for the gradient calls. The tables of pieces travel as kernel arguments.
+ *  - Workspace: device scratch of ar_vocab_workspace_bytes() bytes, 16-byte aligned, contents unprepared. It is
+ *    bounded in T but for the gathered hidden states (logits are worked on 4 GiB at a time), and the library keeps
+ *    none of its own for these calls: NULL is too small.
+ *  - Memory: rows are contiguous, ld apart (>= their length), at any address that is a multiple of the element
+ *    size; 16-byte aligned rows of bf16 with H and ld multiples of 8 are read in place, others are first copied into
+ *    the workspace. What a call writes (loss, dh, dw, workspace) must not overlap, first to last element, anything
+ *    else of it.
+ *  - Limits: T < 2^30, H <= 65536, top <= 1024, P <= AR_MAX_RANKS, and V with every piece rounded up to a
+ *    multiple of 256 rows at most 2^20. */
+typedef enum { AR_MEAN = 0, AR_TOTAL = 1, AR_NONE = 2 } ar_reduction;
+
+typedef struct ar_vocab_piece {
+  const void* w;  /* [rows, H] */
+  void* dw;       /* ar_vocab_loss_grad: receives the piece's gradient [rows, H]; otherwise ignored */
+  int64_t rows;   /* >= 0 */
+  int64_t ld;     /* elements from one row of w to the next */
+  int64_t dld;    /* the same of dw */
+} ar_vocab_piece;
+
+typedef struct ar_vocab {
+  int64_t T, H;
+  int32_t dtype;  /* AR_FP32 or AR_BF16: of hidden, every w, dh and every dw */
+  int32_t P;
+  const void* hidden;
+  int64_t ld;
+  const ar_vocab_piece* pieces; /* host array of P */
+  float temperature;            /* > 0, finite */
+  int32_t reduction;            /* ar_reduction */
+  const float* token_weights;   /* device, T of them, or NULL: 1 */
+  int32_t top;                  /* 0: cross entropy with targets ids[T]; K: distillation with ids [T, K] */
+  int32_t ids_bytes;            /* 4 (int32) or 8 (int64) */
+  const void* ids;              /* device */
+  int64_t ids_ld;               /* elements from one token's ids to the next (top > 0) */
+  int64_t ignore;               /* top = 0: the target of rows left out; customarily -100 */
+  const void* logits;           /* device, the teacher's [T, K] (top > 0) */
+  int64_t logits_ld;
+  int32_t logits_dtype;         /* AR_FP32 or AR_BF16 */
+  float* loss;                  /* device: one value, or T of them (AR_NONE) */
+  void* dh;                     /* ar_vocab_loss_grad: receives [T, H]; otherwise ignored */
+  int64_t dh_ld;
+  void* workspace;
+  size_t workspace_bytes;
+  void* start_event;            /* as in ar_call */
+  void* stop_event;
+} ar_vocab;
+
+ar_status ar_vocab_loss(const ar_vocab* call, void* stream);
+/* The loss and the gradients. */
+ar_status ar_vocab_loss_grad(const ar_vocab* call, void* stream);
+/* The workspace of one or the other (grad != 0). Of the pointers only the pieces' alignment counts. */
+ar_status ar_vocab_workspace_bytes(const ar_vocab* call, int32_t grad, size_t* bytes);
+
 /* ---- schedules on the host (no GPU needed) ---- */
 typedef struct ar_schedule ar_schedule;
 
