@@ -364,38 +364,45 @@ struct Product {
   int32_t accumulate;
 };
 
-typedef __amdgpu_buffer_rsrc_t Rsrc;
+typedef int32_t Rsrc __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ Rsrc rsrc_of(const char* base, int64_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
   const int64_t most = 0x7ffffff0;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), 0, int(bytes < 0 ? 0 : bytes < most ? bytes : most), 0x00020000);
+  return Rsrc{int32_t(p), int32_t(p >> 32) & 0xffff, int32_t(bytes < 0 ? 0 : bytes < most ? bytes : most), 0x00020000};
 }
-constexpr int kLoadsDone = 0x0f70;  // s_waitcnt vmcnt(0)
+constexpr int kLoadsDone = 0x0f70, kAllDone = 0x0070;  // s_waitcnt vmcnt(0), and lgkmcnt(0) with it
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: such a lane loads zeros
+
+// 16 bytes a lane straight into LDS, lane after lane. Written out because the compiler, where it knows of such a
+// load, has every transposing read of LDS wait for it; here the barriers do. Nothing is written to registers.
+__device__ __forceinline__ void load_lds(AR_LDS char* lds, Rsrc r, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uint32_t(reinterpret_cast<uintptr_t>(lds))), "v"(off), "s"(r) : "memory", "m0");
+}
 
 // R rows of 128 bytes along k; of a row, `left` elements exist.
 template <int R, int THREADS> __device__ __forceinline__ void load_along(AR_LDS char* lds, Rsrc r, uint32_t ldb, int left, int tid) {
-  const int wave = tid / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const uint32_t row = uint32_t(tid) / 8, c = (uint32_t(tid) % 8) ^ (row / 2 % 8);
   const uint32_t off = int(c * 8) < left ? row * ldb + c * 16 : kNowhere;  // (the bounds check leaves a scalar offset out)
 #pragma unroll
   for (int i = 0; i < (R * 8 + THREADS - 1) / THREADS; ++i)
     if (R * 8 % THREADS == 0 || i * THREADS + wave * 64 < R * 8)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (AR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16, off + i * (THREADS / 8) * ldb, 0, 0, 0);
+      load_lds(lds + (i * THREADS + wave * 64) * 16, r, off + i * (THREADS / 8) * ldb);
 }
 
 template <int R> __device__ __forceinline__ uint32_t across_swizzle(uint32_t krow) { return (krow % 4 + krow / 8 % 4 * 4) & (R / 16 - 1); }
 
 // kBK rows of R columns.
 template <int R, int THREADS> __device__ __forceinline__ void load_across(AR_LDS char* lds, Rsrc r, uint32_t ldb, int tid) {
-  const int wave = tid / 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   constexpr int C = R / 8;
 #pragma unroll
   for (int i = 0; i < (kBK * C + THREADS - 1) / THREADS; ++i)
     if (kBK * C % THREADS == 0 || i * THREADS + wave * 64 < kBK * C) {
       const uint32_t q = i * THREADS + tid, krow = q / C, slot = q % C;
       const uint32_t c = ((slot / 2) ^ across_swizzle<R>(krow)) * 2 + slot % 2;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (AR_LDS void*)(lds + (i * THREADS + wave * 64) * 16), 16, krow * ldb + c * 16, 0, 0, 0);
+      load_lds(lds + (i * THREADS + wave * 64) * 16, r, krow * ldb + c * 16);
     }
 }
 
@@ -422,7 +429,7 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
   return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(x)))) | uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(x >> 32)))) << 32);
 }
 
-// Loads a product's slices into LDS, one after the other.
+// Where a product's slices come from, and the loads that bring them into LDS.
 template <class C, int DIR> struct Stager {
   static constexpr bool kXAlong = DIR == S_LOGITS, kYAlong = DIR != S_WEIGHT;
   const Product& a;
@@ -431,8 +438,13 @@ template <class C, int DIR> struct Stager {
   const char* w;
   int64_t ld;
   int rows, start, next;
+  // the next slice
+  const char *xp, *yp;
+  int64_t xbytes, ybytes;
+  int left;
 
-  __device__ __forceinline__ void take(int p) {
+  __device__ __forceinline__ void take_at(int32_t v) {
+    const int p = __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, v));
     const Piece& q = a.pieces[p];
     w = reinterpret_cast<const char*>(uniform(reinterpret_cast<int64_t>(q.w)));
     ld = uniform(q.ld);
@@ -440,49 +452,87 @@ template <class C, int DIR> struct Stager {
     start = __builtin_amdgcn_readfirstlane(q.start);
     next = p + 1 < a.P ? __builtin_amdgcn_readfirstlane(a.pieces[p + 1].start) : 0x7fffffff;
   }
-  __device__ __forceinline__ void take_at(int32_t v) { take(__builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, v))); }
 
-  __device__ __forceinline__ void load(AR_LDS char* lds, int s) {
+  // Points the loads at slice s, or at nothing (zeros) behind the last one.
+  __device__ __forceinline__ void seek(int s, int end) {
     const int pass = s / steps, k = (s - pass * steps) * kBK;
     const int px = plane_x(pass, a.planes), py = plane_y(pass, a.planes);
     const int64_t ldh = int64_t(a.planes) * a.Hp, ldd = int64_t(a.planes) * a.Vp;
+    ybytes = 0x7ffffff0;
     if constexpr (DIR == S_LOGITS) {
       const int64_t r = m0 - start;
-      load_along<C::BM, C::kThreads>(lds, rsrc_of(w + (r * ld + int64_t(px) * a.Hp + k) * 2, ((rows - r - 1) * ld + a.kend - k) * 2), uint32_t(ld * 2), a.kend - k, tid);
-      load_along<C::BN, C::kThreads>(lds + C::kX, rsrc_of(a.hp + (int64_t(a.chunk + n0) * ldh + int64_t(py) * a.Hp + k) * 2, 0x7ffffff0), uint32_t(ldh * 2), kBK, tid);
+      xp = w + (r * ld + int64_t(px) * a.Hp + k) * 2;
+      left = a.kend - k;
+      xbytes = ((rows - r - 1) * ld + left) * 2;
+      yp = a.hp + (int64_t(a.chunk + n0) * ldh + int64_t(py) * a.Hp + k) * 2;
     } else if constexpr (DIR == S_HIDDEN) {
-      if (k < start || k >= next) take_at(k);
+      if (s < end && (k < start || k >= next)) take_at(k);
       const int64_t r = k - start;
-      load_across<C::BM, C::kThreads>(lds, rsrc_of(w + (r * ld + int64_t(px) * a.Hp + m0) * 2, r < rows ? ((rows - r - 1) * ld + a.kend - m0) * 2 : 0), uint32_t(ld * 2), tid);
-      load_along<C::BN, C::kThreads>(lds + C::kX, rsrc_of(a.d + (int64_t(n0) * ldd + int64_t(py) * a.Vp + k) * 2, 0x7ffffff0), uint32_t(ldd * 2), kBK, tid);
+      xp = w + (r * ld + int64_t(px) * a.Hp + m0) * 2;
+      xbytes = r < rows ? ((rows - r - 1) * ld + a.kend - m0) * 2 : 0;
+      yp = a.d + (int64_t(n0) * ldd + int64_t(py) * a.Vp + k) * 2;
     } else {
       // columns past a row's end are the next row's: they meet outputs that nothing keeps
-      load_across<C::BM, C::kThreads>(lds, rsrc_of(a.hp + (int64_t(a.chunk + k) * ldh + int64_t(px) * a.Hp + m0) * 2, (kBK * ldh - int64_t(px) * a.Hp - m0) * 2), uint32_t(ldh * 2), tid);
-      load_across<C::BN, C::kThreads>(lds + C::kX, rsrc_of(a.d + (int64_t(k) * ldd + int64_t(py) * a.Vp + n0) * 2, 0x7ffffff0), uint32_t(ldd * 2), tid);
+      xp = a.hp + (int64_t(a.chunk + k) * ldh + int64_t(px) * a.Hp + m0) * 2;
+      xbytes = (kBK * ldh - int64_t(px) * a.Hp - m0) * 2;
+      yp = a.d + (int64_t(k) * ldd + int64_t(py) * a.Vp + n0) * 2;
+    }
+    if (s >= end) xbytes = ybytes = 0;
+  }
+
+  __device__ __forceinline__ void load(AR_LDS char* lds) {
+    const uint32_t ldh = uint32_t(a.planes) * uint32_t(a.Hp) * 2, ldd = uint32_t(a.planes) * uint32_t(a.Vp) * 2;
+    const Rsrc x = rsrc_of(xp, xbytes), y = rsrc_of(yp, ybytes);
+    if constexpr (DIR == S_LOGITS) {
+      load_along<C::BM, C::kThreads>(lds, x, uint32_t(ld * 2), left, tid);
+      load_along<C::BN, C::kThreads>(lds + C::kX, y, ldh, kBK, tid);
+    } else if constexpr (DIR == S_HIDDEN) {
+      load_across<C::BM, C::kThreads>(lds, x, uint32_t(ld * 2), tid);
+      load_along<C::BN, C::kThreads>(lds + C::kX, y, ldd, kBK, tid);
+    } else {
+      load_across<C::BM, C::kThreads>(lds, x, ldh, tid);
+      load_across<C::BN, C::kThreads>(lds + C::kX, y, ldd, tid);
     }
   }
 };
 
-template <class C, int DIR, class ACC> __device__ __forceinline__ void multiply(AR_LDS char* lds, ACC& acc, int wm, int wn, int lane) {
-  using St = Stager<C, DIR>;
-  AR_LDS char* y = lds + C::kX;
-#pragma unroll
-  for (int kk = 0; kk < kBK / 32; ++kk) {
-    bf16x8 xf[C::FM], yf[C::FN];
+// A wave's operands of half a slice, and the products of them.
+template <class C, int DIR> struct Operands {
+  bf16x8 x[C::FM], y[C::FN];
+  __device__ __forceinline__ void read(AR_LDS char* lds, int kk, int wm, int wn, int lane) {
+    using St = Stager<C, DIR>;
 #pragma unroll
     for (int j = 0; j < C::FN; ++j) {
-      if constexpr (St::kYAlong) yf[j] = read_along(y, wn * C::NW + j * 16, kk, lane);
-      else yf[j] = read_across<C::BN>(y, wn * C::NW + j * 16, kk, lane);
+      if constexpr (St::kYAlong) y[j] = read_along(lds + C::kX, wn * C::NW + j * 16, kk, lane);
+      else y[j] = read_across<C::BN>(lds + C::kX, wn * C::NW + j * 16, kk, lane);
     }
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
-      if constexpr (St::kXAlong) xf[i] = read_along(lds, wm * C::MW + i * 16, kk, lane);
-      else xf[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, kk, lane);
+      if constexpr (St::kXAlong) x[i] = read_along(lds, wm * C::MW + i * 16, kk, lane);
+      else x[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, kk, lane);
     }
+  }
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[C::FM][C::FN]) const {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], yf[j], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
+  }
+};
+
+// The order in which a phase issues: LOADS loads and READS reads of LDS spread over the first three quarters of
+// PRODUCTS products, so that the last reads return while the rest multiplies.
+template <int LOADS, int READS, int PRODUCTS> __device__ __forceinline__ void interleave() {
+  constexpr int kGroups = PRODUCTS * 3 / 4 / 3 > 0 ? PRODUCTS * 3 / 4 / 3 : 1;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    if ((g + 1) * READS / kGroups - g * READS / kGroups == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    if ((g + 1) * READS / kGroups - g * READS / kGroups == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if ((g + 1) * READS / kGroups - g * READS / kGroups == 3) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+    if ((g + 1) * READS / kGroups - g * READS / kGroups == 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+    if ((g + 1) * LOADS / kGroups - g * LOADS / kGroups == 1) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
+    if ((g + 1) * LOADS / kGroups - g * LOADS / kGroups == 2) __builtin_amdgcn_sched_group_barrier(0x20, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
   }
 }
 
@@ -532,7 +582,8 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     const int in_group = int(u - group * 8 * mtiles), width = min(8, ntiles - int(group) * 8);
     const int m0 = in_group / width * C::BM, n0 = (int(group) * 8 + in_group % width) * C::BN;
 
-    Stager<C, DIR> st{a, m0, n0, tid, steps};
+    using St = Stager<C, DIR>;
+    St st{a, m0, n0, tid, steps};
     st.start = st.next = 0;
     if constexpr (DIR == S_LOGITS) st.take_at(m0);
     const int all = steps * passes;
@@ -544,14 +595,39 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
+    // Half a slice is multiplied while the next half is read from LDS, and a slice is loaded a whole slice before
+    // it is read, into the one that has just been: one barrier a slice.
     if (s0 < s1) {
-      st.load(lds, s0);
+      constexpr int kReads = (St::kXAlong ? C::FM : 2 * C::FM) + (St::kYAlong ? C::FN : 2 * C::FN);
+      constexpr int kProducts = C::FM * C::FN;
+      Operands<C, DIR> f0, f1;
+      st.seek(s0, s1);
+      st.load(lds);
+      st.seek(s0 + 1, s1);
+      st.load(lds + C::kStage);
+      __builtin_amdgcn_s_waitcnt(kLoadsDone);
+      __syncthreads();
+      f0.read(lds, 0, wm, wn, lane);
+      AR_LDS char *here = lds, *there = lds + C::kStage;
       for (int s = s0; s < s1; ++s) {
-        __builtin_amdgcn_s_waitcnt(kLoadsDone);
-        __syncthreads();  // this slice is in LDS, the other one has been read
-        if (s + 1 < s1) st.load(lds + ((s + 1 - s0) & 1) * C::kStage, s + 1);
-        multiply<C, DIR>(lds + ((s - s0) & 1) * C::kStage, acc, wm, wn, lane);
+        st.seek(s + 2, s1);
+        f1.read(here, 1, wm, wn, lane);
+        f0.multiply(acc);
+        interleave<0, kReads, kProducts>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(kAllDone);  // this wave has read the slice, and its loads of the next are in LDS
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        st.load(here);
+        f0.read(there, 0, wm, wn, lane);
+        f1.multiply(acc);
+        interleave<0, kReads, kProducts>();
+        AR_LDS char* t2 = here;
+        here = there;
+        there = t2;
       }
+      __builtin_amdgcn_s_waitcnt(kAllDone);
     }
     __syncthreads();
 
