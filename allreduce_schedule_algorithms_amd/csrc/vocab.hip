@@ -380,31 +380,32 @@ __device__ __forceinline__ void load_lds(AR_LDS char* lds, Rsrc r, uint32_t off)
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uint32_t(reinterpret_cast<uintptr_t>(lds))), "v"(off), "s"(r) : "memory", "m0");
 }
 
-// R rows of 128 bytes along k; of a row, `left` elements exist.
-template <int R, int THREADS> __device__ __forceinline__ void load_along(AR_LDS char* lds, Rsrc r, uint32_t ldb, int left, int tid) {
-  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const uint32_t row = uint32_t(tid) / 8, c = (uint32_t(tid) % 8) ^ (row / 2 % 8);
-  const uint32_t off = int(c * 8) < left ? row * ldb + c * 16 : kNowhere;  // (the bounds check leaves a scalar offset out)
-#pragma unroll
-  for (int i = 0; i < (R * 8 + THREADS - 1) / THREADS; ++i)
-    if (R * 8 % THREADS == 0 || i * THREADS + wave * 64 < R * 8)
-      load_lds(lds + (i * THREADS + wave * 64) * 16, r, off + i * (THREADS / 8) * ldb);
-}
-
 template <int R> __device__ __forceinline__ uint32_t across_swizzle(uint32_t krow) { return (krow % 4 + krow / 8 % 4 * 4) & (R / 16 - 1); }
 
-// kBK rows of R columns.
-template <int R, int THREADS> __device__ __forceinline__ void load_across(AR_LDS char* lds, Rsrc r, uint32_t ldb, int tid) {
-  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  constexpr int C = R / 8;
+// How a workgroup loads a slice of R rows along k, or of R columns across: load i brings rows `kStep` further on, at
+// an offset that alternates where the swizzle does.
+template <int R, int THREADS, bool ALONG> struct Loads {
+  static constexpr int kCount = R * kBK * 2 / (THREADS * 16), kStep = ALONG ? THREADS / 8 : THREADS / (R / 8);
+  static_assert(kStep % 16 == 0 && (kCount == 1 || R * kBK * 2 % (THREADS * 16) == 0), "the swizzle repeats");
+  uint32_t off[2], c;
+
+  __device__ __forceinline__ void set(uint32_t ldb, int tid) {
+    if constexpr (ALONG) {
+      const uint32_t row = uint32_t(tid) / 8;
+      c = (uint32_t(tid) % 8) ^ (row / 2 % 8);
+      off[0] = off[1] = row * ldb + c * 16;
+    } else {
+      const uint32_t krow = uint32_t(tid) / (R / 8), slot = uint32_t(tid) % (R / 8);
 #pragma unroll
-  for (int i = 0; i < (kBK * C + THREADS - 1) / THREADS; ++i)
-    if (kBK * C % THREADS == 0 || i * THREADS + wave * 64 < kBK * C) {
-      const uint32_t q = i * THREADS + tid, krow = q / C, slot = q % C;
-      const uint32_t c = ((slot / 2) ^ across_swizzle<R>(krow)) * 2 + slot % 2;
-      load_lds(lds + (i * THREADS + wave * 64) * 16, r, krow * ldb + c * 16);
+      for (int i = 0; i < 2; ++i) off[i] = krow * ldb + (((slot / 2) ^ across_swizzle<R>(krow + i * kStep)) * 2 + slot % 2) * 16;
     }
-}
+  }
+  // Of a row along k, `left` elements exist.
+  __device__ __forceinline__ uint32_t at(int i, uint32_t ldb, int left) const {
+    const uint32_t o = off[kStep % 32 ? i & 1 : 0] + i * kStep * ldb;
+    return !ALONG || int(c * 8) < left ? o : kNowhere;
+  }
+};
 
 // The operand of one product: 16 rows from `base`, k 32 kk + 8 (lane / 16) on.
 __device__ __forceinline__ bf16x8 read_along(AR_LDS const char* lds, int base, int kk, int lane) {
@@ -432,6 +433,9 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 // Where a product's slices come from, and the loads that bring them into LDS.
 template <class C, int DIR> struct Stager {
   static constexpr bool kXAlong = DIR == S_LOGITS, kYAlong = DIR != S_WEIGHT;
+  using LX = Loads<C::BM, C::kThreads, kXAlong>;
+  using LY = Loads<C::BN, C::kThreads, kYAlong>;
+  static constexpr int kLoads = LX::kCount + LY::kCount;
   const Product& a;
   int m0, n0, tid, steps;  // steps of one pass over the depth
   // the piece of the output matrix that is being read: its rows are [start, start + rows) of the padded vocabulary
@@ -439,8 +443,10 @@ template <class C, int DIR> struct Stager {
   int64_t ld;
   int rows, start, next;
   // the next slice
-  const char *xp, *yp;
-  int64_t xbytes, ybytes;
+  Rsrc x, y;
+  LX lx;
+  LY ly;
+  uint32_t ldx, ldy;  // bytes
   int left;
 
   __device__ __forceinline__ void take_at(int32_t v) {
@@ -451,6 +457,19 @@ template <class C, int DIR> struct Stager {
     rows = __builtin_amdgcn_readfirstlane(q.rows);
     start = __builtin_amdgcn_readfirstlane(q.start);
     next = p + 1 < a.P ? __builtin_amdgcn_readfirstlane(a.pieces[p + 1].start) : 0x7fffffff;
+    ldx = uint32_t(ld * 2);
+    lx.set(ldx, tid);
+  }
+
+  __device__ __forceinline__ void begin(int m, int n) {
+    m0 = m;
+    n0 = n;
+    start = next = 0;
+    left = kBK;
+    if constexpr (DIR == S_LOGITS) take_at(m0);
+    if constexpr (DIR == S_WEIGHT) lx.set(ldx = uint32_t(a.planes) * uint32_t(a.Hp) * 2, tid);
+    ldy = DIR == S_LOGITS ? uint32_t(a.planes) * uint32_t(a.Hp) * 2 : uint32_t(a.planes) * uint32_t(a.Vp) * 2;
+    ly.set(ldy, tid);
   }
 
   // Points the loads at slice s, or at nothing (zeros) behind the last one.
@@ -458,7 +477,8 @@ template <class C, int DIR> struct Stager {
     const int pass = s / steps, k = (s - pass * steps) * kBK;
     const int px = plane_x(pass, a.planes), py = plane_y(pass, a.planes);
     const int64_t ldh = int64_t(a.planes) * a.Hp, ldd = int64_t(a.planes) * a.Vp;
-    ybytes = 0x7ffffff0;
+    int64_t xbytes, ybytes = s < end ? 0x7ffffff0 : 0;
+    const char *xp, *yp;
     if constexpr (DIR == S_LOGITS) {
       const int64_t r = m0 - start;
       xp = w + (r * ld + int64_t(px) * a.Hp + k) * 2;
@@ -477,63 +497,57 @@ template <class C, int DIR> struct Stager {
       xbytes = (kBK * ldh - int64_t(px) * a.Hp - m0) * 2;
       yp = a.d + (int64_t(k) * ldd + int64_t(py) * a.Vp + n0) * 2;
     }
-    if (s >= end) xbytes = ybytes = 0;
+    x = rsrc_of(xp, s < end ? xbytes : 0);
+    y = rsrc_of(yp, ybytes);
   }
 
-  __device__ __forceinline__ void load(AR_LDS char* lds) {
-    const uint32_t ldh = uint32_t(a.planes) * uint32_t(a.Hp) * 2, ldd = uint32_t(a.planes) * uint32_t(a.Vp) * 2;
-    const Rsrc x = rsrc_of(xp, xbytes), y = rsrc_of(yp, ybytes);
-    if constexpr (DIR == S_LOGITS) {
-      load_along<C::BM, C::kThreads>(lds, x, uint32_t(ld * 2), left, tid);
-      load_along<C::BN, C::kThreads>(lds + C::kX, y, ldh, kBK, tid);
-    } else if constexpr (DIR == S_HIDDEN) {
-      load_across<C::BM, C::kThreads>(lds, x, uint32_t(ld * 2), tid);
-      load_along<C::BN, C::kThreads>(lds + C::kX, y, ldd, kBK, tid);
-    } else {
-      load_across<C::BM, C::kThreads>(lds, x, ldh, tid);
-      load_across<C::BN, C::kThreads>(lds + C::kX, y, ldd, tid);
-    }
+  template <int I> __device__ __forceinline__ void load(AR_LDS char* lds) {
+    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+    if constexpr (I < LX::kCount) load_lds(lds + (I * C::kThreads + wave * 64) * 16, x, lx.at(I, ldx, left));
+    else load_lds(lds + C::kX + ((I - LX::kCount) * C::kThreads + wave * 64) * 16, y, ly.at(I - LX::kCount, ldy, kBK));
   }
 };
 
-// A wave's operands of half a slice, and the products of them.
+// A wave's operands of half a slice.
 template <class C, int DIR> struct Operands {
+  static constexpr int kReads = C::FM + C::FN;
   bf16x8 x[C::FM], y[C::FN];
-  __device__ __forceinline__ void read(AR_LDS char* lds, int kk, int wm, int wn, int lane) {
+  template <int R> __device__ __forceinline__ void read(AR_LDS char* lds, int kk, int wm, int wn, int lane) {
     using St = Stager<C, DIR>;
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) {
-      if constexpr (St::kYAlong) y[j] = read_along(lds + C::kX, wn * C::NW + j * 16, kk, lane);
-      else y[j] = read_across<C::BN>(lds + C::kX, wn * C::NW + j * 16, kk, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
+    if constexpr (R < C::FN) {
+      if constexpr (St::kYAlong) y[R] = read_along(lds + C::kX, wn * C::NW + R * 16, kk, lane);
+      else y[R] = read_across<C::BN>(lds + C::kX, wn * C::NW + R * 16, kk, lane);
+    } else {
+      constexpr int i = R - C::FN;
       if constexpr (St::kXAlong) x[i] = read_along(lds, wm * C::MW + i * 16, kk, lane);
       else x[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, kk, lane);
     }
   }
-  __device__ __forceinline__ void multiply(f32x4 (&acc)[C::FM][C::FN]) const {
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[i], y[j], acc[i][j], 0, 0, 0);
-  }
 };
 
-// The order in which a phase issues: LOADS loads and READS reads of LDS spread over the first three quarters of
-// PRODUCTS products, so that the last reads return while the rest multiplies.
-template <int LOADS, int READS, int PRODUCTS> __device__ __forceinline__ void interleave() {
-  constexpr int kGroups = PRODUCTS * 3 / 4 / 3 > 0 ? PRODUCTS * 3 / 4 / 3 : 1;
-#pragma unroll
-  for (int g = 0; g < kGroups; ++g) {
-    if ((g + 1) * READS / kGroups - g * READS / kGroups == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-    if ((g + 1) * READS / kGroups - g * READS / kGroups == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    if ((g + 1) * READS / kGroups - g * READS / kGroups == 3) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-    if ((g + 1) * READS / kGroups - g * READS / kGroups == 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-    if ((g + 1) * LOADS / kGroups - g * LOADS / kGroups == 1) __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);
-    if ((g + 1) * LOADS / kGroups - g * LOADS / kGroups == 2) __builtin_amdgcn_sched_group_barrier(0x20, 2, 0);
-    __builtin_amdgcn_sched_group_barrier(0x8, 3, 0);
+template <int I, int N, class F> __device__ __forceinline__ void each_of(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each_of<I + 1, N>(f);
   }
+}
+
+// Half a slice: the products of `now`, with the reads of `then` from `from` and (LOAD) the loads of a slice into `to`
+// between them, in this order: a wave issues in order, and a run of loads would hold its products up.
+template <class C, int DIR, bool LOAD> __device__ __forceinline__ void half(Stager<C, DIR>& st, const Operands<C, DIR>& now, Operands<C, DIR>& then, AR_LDS char* from, int kk,
+                                                                            AR_LDS char* to, f32x4 (&acc)[C::FM][C::FN], int wm, int wn, int lane) {
+  using O = Operands<C, DIR>;
+  constexpr int kLoads = Stager<C, DIR>::kLoads, kProducts = C::FM * C::FN, kParts = kProducts < 8 ? kProducts : 8;
+  each_of<0, kParts>([&](auto part) {
+    constexpr int g = part, early = kParts > 4 ? kParts * 3 / 4 : kParts;  // the reads come in the first parts, and have the last to return
+    if constexpr (LOAD) each_of<kLoads * g / kParts, kLoads * (g + 1) / kParts>([&](auto i) { st.template load<i>(to); });
+    if constexpr (g < early) each_of<O::kReads * g / early, O::kReads * (g + 1) / early>([&](auto i) { then.template read<i>(from, kk, wm, wn, lane); });
+    each_of<kProducts * g / kParts, kProducts * (g + 1) / kParts>([&](auto p) {
+      constexpr int i = p / C::FN, j = p % C::FN;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.x[i], now.y[j], acc[i][j], 0, 0, 0);
+    });
+    __builtin_amdgcn_sched_barrier(0);
+  });
 }
 
 // Four consecutive outputs of a row, of which `left` exist.
@@ -569,6 +583,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + kBK - 1) / kBK * kBK;
   const int passes = a.planes == 1 ? 1 : 6;
   const int steps = depth / kBK;
+  Stager<C, DIR> st{a, 0, 0, tid, steps};
   for (int64_t t = blockIdx.x; t < tiles * a.splits; t += gridDim.x) {
     const int split = int(t / tiles);
     // Workgroups go to the eight dies in turn: each die gets a run of tiles, and of a run eight tiles of n share
@@ -582,10 +597,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     const int in_group = int(u - group * 8 * mtiles), width = min(8, ntiles - int(group) * 8);
     const int m0 = in_group / width * C::BM, n0 = (int(group) * 8 + in_group % width) * C::BN;
 
-    using St = Stager<C, DIR>;
-    St st{a, m0, n0, tid, steps};
-    st.start = st.next = 0;
-    if constexpr (DIR == S_LOGITS) st.take_at(m0);
+    st.begin(m0, n0);
     const int all = steps * passes;
     const int s0 = int(int64_t(all) * split / a.splits), s1 = int(int64_t(all) * (split + 1) / a.splits);
 
@@ -598,31 +610,26 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     // Half a slice is multiplied while the next half is read from LDS, and a slice is loaded a whole slice before
     // it is read, into the one that has just been: one barrier a slice.
     if (s0 < s1) {
-      constexpr int kReads = (St::kXAlong ? C::FM : 2 * C::FM) + (St::kYAlong ? C::FN : 2 * C::FN);
-      constexpr int kProducts = C::FM * C::FN;
       Operands<C, DIR> f0, f1;
+      constexpr int kLoads = Stager<C, DIR>::kLoads;
       st.seek(s0, s1);
-      st.load(lds);
+      each_of<0, kLoads>([&](auto i) { st.template load<i>(lds); });
       st.seek(s0 + 1, s1);
-      st.load(lds + C::kStage);
+      each_of<0, kLoads>([&](auto i) { st.template load<i>(lds + C::kStage); });
       __builtin_amdgcn_s_waitcnt(kLoadsDone);
       __syncthreads();
-      f0.read(lds, 0, wm, wn, lane);
+      each_of<0, Operands<C, DIR>::kReads>([&](auto i) { f0.template read<i>(lds, 0, wm, wn, lane); });
       AR_LDS char *here = lds, *there = lds + C::kStage;
       for (int s = s0; s < s1; ++s) {
         st.seek(s + 2, s1);
-        f1.read(here, 1, wm, wn, lane);
-        f0.multiply(acc);
-        interleave<0, kReads, kProducts>();
+        __builtin_amdgcn_sched_barrier(0);
+        half<C, DIR, false>(st, f0, f1, here, 1, nullptr, acc, wm, wn, lane);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(kAllDone);  // this wave has read the slice, and its loads of the next are in LDS
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
-        st.load(here);
-        f0.read(there, 0, wm, wn, lane);
-        f1.multiply(acc);
-        interleave<0, kReads, kProducts>();
+        half<C, DIR, true>(st, f1, f0, there, 0, here, acc, wm, wn, lane);
         AR_LDS char* t2 = here;
         here = there;
         there = t2;
