@@ -39,7 +39,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 #define AR_LDS __attribute__((address_space(3)))
 
-constexpr int kBK = 64;         // depth of a tile: 128 bytes of a row
+constexpr int kBK = 32;         // depth of a slice: one product's, 64 bytes of a row
 constexpr int kPieceTab = 64;   // pieces that one launch's arguments carry
 constexpr int kUnit = 256;      // pieces and token chunks are padded to this many rows
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -322,22 +322,23 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
 // in the accumulators of 16 x 16 x 32 products (a lane holds four consecutive m of one n); operands come through
 // LDS in slices of kBK, loaded straight into it.
 //
-// A slice lies in LDS either as rows of 64 k (128 bytes; "along k") or as k rows of the tile's columns ("across").
+// A slice lies in LDS either as rows of 32 k (64 bytes; "along k") or as k rows of the tile's columns ("across").
 // The loads write LDS in lane order, so the swizzle that spreads the reads over the banks is in which 16
-// bytes a lane loads: along k, chunk c of row r lies at c ^ (r / 2 % 8); across, the 32 bytes c of k row r lie at
+// bytes a lane loads: along k, chunk c of row r lies at c ^ {0, 2, 3, 1}[r / 4 % 4]; across, the 32 bytes c of k row r lie at
 // c ^ (r % 4 + 4 (r / 8 % 4)), and the reads transpose.
 enum Dir { S_LOGITS = 0, S_HIDDEN = 1, S_WEIGHT = 2 };
 
-template <int BM_, int BN_, int WM_, int WN_, int WAVES_> struct Tile {
+template <int BM_, int BN_, int WM_, int WN_, int WAVES_, int STAGES_> struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kThreads = WM * WN * 64;
   static constexpr int MW = BM / WM, NW = BN / WN;  // a wave's part
   static constexpr int FM = MW / 16, FN = NW / 16;
   static constexpr int kWaves = WAVES_;  // of a SIMD, which bounds the registers
+  static constexpr int kStages = STAGES_;  // slices in LDS, an even number
   static constexpr int kX = BM * kBK * 2, kY = BN * kBK * 2, kStage = kX + kY;
 };
-using TileL = Tile<256, 256, 2, 4, 2>;
-using TileM = Tile<128, 128, 2, 2, 2>;
-using TileS = Tile<128, 32, 4, 1, 4>;
+using TileL = Tile<256, 256, 2, 4, 2, 4>;
+using TileM = Tile<128, 128, 2, 2, 2, 4>;
+using TileS = Tile<128, 64, 4, 1, 2, 6>;
 
 struct Product {
   const Piece* pieces;
@@ -366,12 +367,12 @@ struct Product {
 
 typedef int32_t Rsrc __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ Rsrc rsrc_of(const char* base, int64_t bytes) {
+__device__ __forceinline__ Rsrc rsrc_of(const char* base, int bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
-  const int64_t most = 0x7ffffff0;
-  return Rsrc{int32_t(p), int32_t(p >> 32) & 0xffff, int32_t(bytes < 0 ? 0 : bytes < most ? bytes : most), 0x00020000};
+  return Rsrc{int32_t(p), int32_t(p >> 32) & 0xffff, bytes, 0x00020000};
 }
-constexpr int kLoadsDone = 0x0f70, kAllDone = 0x0070;  // s_waitcnt vmcnt(0), and lgkmcnt(0) with it
+// s_waitcnt: every LDS operation done, and all but the last n vector memory operations.
+constexpr int waits(int n) { return (n & 15) | (n >> 4) << 14 | 0x70; }
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: such a lane loads zeros
 
 // 16 bytes a lane straight into LDS, lane after lane. Written out because the compiler, where it knows of such a
@@ -380,19 +381,25 @@ __device__ __forceinline__ void load_lds(AR_LDS char* lds, Rsrc r, uint32_t off)
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(uint32_t(reinterpret_cast<uintptr_t>(lds))), "v"(off), "s"(r) : "memory", "m0");
 }
 
+// A read of 16 bytes a lane serves four rows of four lanes at a time, those of q = r / 4 % 4 and chunk (0, 0), (3, 0),
+// (1, 1), (2, 1) or the like: with c ^ q two of them met in the same banks.
+__device__ __forceinline__ uint32_t along_swizzle(uint32_t row) {
+  const uint32_t q = row / 4 % 4;
+  return q / 2 | ((q ^ q / 2) & 1) * 2;
+}
 template <int R> __device__ __forceinline__ uint32_t across_swizzle(uint32_t krow) { return (krow % 4 + krow / 8 % 4 * 4) & (R / 16 - 1); }
 
 // How a workgroup loads a slice of R rows along k, or of R columns across: load i brings rows `kStep` further on, at
 // an offset that alternates where the swizzle does.
 template <int R, int THREADS, bool ALONG> struct Loads {
-  static constexpr int kCount = R * kBK * 2 / (THREADS * 16), kStep = ALONG ? THREADS / 8 : THREADS / (R / 8);
-  static_assert(kStep % 16 == 0 && (kCount == 1 || R * kBK * 2 % (THREADS * 16) == 0), "the swizzle repeats");
+  static constexpr int kCount = R * kBK * 2 / (THREADS * 16), kStep = ALONG ? THREADS / 4 : THREADS / (R / 8);
+  static_assert(kStep % 16 == 0 && R * kBK * 2 % (THREADS * 16) == 0, "the swizzle repeats");
   uint32_t off[2], c;
 
   __device__ __forceinline__ void set(uint32_t ldb, int tid) {
     if constexpr (ALONG) {
-      const uint32_t row = uint32_t(tid) / 8;
-      c = (uint32_t(tid) % 8) ^ (row / 2 % 8);
+      const uint32_t row = uint32_t(tid) / 4;
+      c = (uint32_t(tid) % 4) ^ along_swizzle(row);
       off[0] = off[1] = row * ldb + c * 16;
     } else {
       const uint32_t krow = uint32_t(tid) / (R / 8), slot = uint32_t(tid) % (R / 8);
@@ -407,13 +414,13 @@ template <int R, int THREADS, bool ALONG> struct Loads {
   }
 };
 
-// The operand of one product: 16 rows from `base`, k 32 kk + 8 (lane / 16) on.
-__device__ __forceinline__ bf16x8 read_along(AR_LDS const char* lds, int base, int kk, int lane) {
-  const int row = base + lane % 16, c = (kk * 4 + lane / 16) ^ (lane % 16 / 2);
-  return *reinterpret_cast<AR_LDS const bf16x8*>(lds + row * 128 + c * 16);
+// The operand of one product: 16 rows from `base`, k 8 (lane / 16) on.
+__device__ __forceinline__ bf16x8 read_along(AR_LDS const char* lds, int base, int lane) {
+  const int row = base + lane % 16, c = (lane / 16) ^ along_swizzle(lane);
+  return *reinterpret_cast<AR_LDS const bf16x8*>(lds + row * 64 + c * 16);
 }
-template <int R> __device__ __forceinline__ bf16x8 read_across(AR_LDS char* lds, int base, int kk, int lane) {
-  const uint32_t krow = kk * 32 + lane / 16 * 8 + lane % 16 / 4;
+template <int R> __device__ __forceinline__ bf16x8 read_across(AR_LDS char* lds, int base, int lane) {
+  const uint32_t krow = lane / 16 * 8 + lane % 16 / 4;
   AR_LDS char* p = lds + krow * (R * 2) + ((base / 16) ^ across_swizzle<R>(krow)) * 32 + lane % 4 * 8;
   const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((AR_LDS s16x4*)p);
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((AR_LDS s16x4*)(p + 4 * R * 2));
@@ -443,6 +450,9 @@ template <class C, int DIR> struct Stager {
   int64_t ld;
   int rows, start, next;
   // the next slice
+  int wave, pass, k, stop, slices;  // stop: the depth at which the addresses break off; slices: how many there are from it on
+  const char *xp, *yp;
+  int xrec;  // bytes from xp that may be read
   Rsrc x, y;
   LX lx;
   LY ly;
@@ -472,55 +482,85 @@ template <class C, int DIR> struct Stager {
     ly.set(ldy, tid);
   }
 
-  // Points the loads at slice s, or at nothing (zeros) behind the last one.
+  // Points the loads at slice s of [.., end); behind the last they bring zeros.
   __device__ __forceinline__ void seek(int s, int end) {
-    const int pass = s / steps, k = (s - pass * steps) * kBK;
+    pass = s / steps;
+    k = (s - pass * steps) * kBK;
+    slices = end - s;
+    find();
+  }
+  __device__ __forceinline__ void find() {
     const int px = plane_x(pass, a.planes), py = plane_y(pass, a.planes);
     const int64_t ldh = int64_t(a.planes) * a.Hp, ldd = int64_t(a.planes) * a.Vp;
-    int64_t xbytes, ybytes = s < end ? 0x7ffffff0 : 0;
-    const char *xp, *yp;
+    stop = steps * kBK;
     if constexpr (DIR == S_LOGITS) {
       const int64_t r = m0 - start;
       xp = w + (r * ld + int64_t(px) * a.Hp + k) * 2;
       left = a.kend - k;
-      xbytes = ((rows - r - 1) * ld + left) * 2;
+      xrec = r < rows ? (min(rows - int(r), C::BM) - 1) * int(ldx) + left * 2 : 0;
       yp = a.hp + (int64_t(a.chunk + n0) * ldh + int64_t(py) * a.Hp + k) * 2;
     } else if constexpr (DIR == S_HIDDEN) {
-      if (s < end && (k < start || k >= next)) take_at(k);
-      const int64_t r = k - start;
-      xp = w + (r * ld + int64_t(px) * a.Hp + m0) * 2;
-      xbytes = r < rows ? ((rows - r - 1) * ld + a.kend - m0) * 2 : 0;
+      if (k < start || k >= next) take_at(k);
+      stop = min(stop, next);
+      xp = w + (int64_t(k - start) * ld + int64_t(px) * a.Hp + m0) * 2;
       yp = a.d + (int64_t(n0) * ldd + int64_t(py) * a.Vp + k) * 2;
     } else {
       // columns past a row's end are the next row's: they meet outputs that nothing keeps
       xp = a.hp + (int64_t(a.chunk + k) * ldh + int64_t(px) * a.Hp + m0) * 2;
-      xbytes = (kBK * ldh - int64_t(px) * a.Hp - m0) * 2;
+      xrec = kBK * int(ldx) - (px * a.Hp + m0) * 2;
       yp = a.d + (int64_t(k) * ldd + int64_t(py) * a.Vp + n0) * 2;
     }
-    x = rsrc_of(xp, s < end ? xbytes : 0);
-    y = rsrc_of(yp, ybytes);
+    describe();
+  }
+  __device__ __forceinline__ void describe() {
+    if constexpr (DIR == S_HIDDEN) {
+      const int there = min(rows - (k - start), kBK);
+      xrec = there > 0 ? (there - 1) * int(ldx) + (a.kend - m0) * 2 : 0;
+    }
+    x = rsrc_of(xp, slices > 0 ? max(xrec, 0) : 0);  // (below 0: a tile without rows, further along its depth)
+    y = rsrc_of(yp, slices > 0 ? 0x7ffffff0 : 0);
+  }
+  // On to the next slice; turn() has to follow wherever the addresses may break off, after every second slice (pieces
+  // and passes are whole pairs of them).
+  __device__ __forceinline__ void advance() {
+    k += kBK;
+    --slices;
+    xp += DIR == S_LOGITS ? kBK * 2 : kBK * ldx;
+    yp += DIR == S_WEIGHT ? kBK * ldy : kBK * 2;
+    if constexpr (DIR == S_LOGITS) {
+      xrec -= kBK * 2;
+      left -= kBK;
+    }
+    describe();
+  }
+  __device__ __forceinline__ void turn() {
+    if (k != stop || slices <= 0) return;
+    if (k == steps * kBK) {
+      k = 0;
+      ++pass;
+    }
+    find();
   }
 
   template <int I> __device__ __forceinline__ void load(AR_LDS char* lds) {
-    const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
     if constexpr (I < LX::kCount) load_lds(lds + (I * C::kThreads + wave * 64) * 16, x, lx.at(I, ldx, left));
     else load_lds(lds + C::kX + ((I - LX::kCount) * C::kThreads + wave * 64) * 16, y, ly.at(I - LX::kCount, ldy, kBK));
   }
 };
 
-// A wave's operands of half a slice.
+// A wave's operands of a slice.
 template <class C, int DIR> struct Operands {
   static constexpr int kReads = C::FM + C::FN;
   bf16x8 x[C::FM], y[C::FN];
-  template <int R> __device__ __forceinline__ void read(AR_LDS char* lds, int kk, int wm, int wn, int lane) {
+  template <int R> __device__ __forceinline__ void read(AR_LDS char* lds, int wm, int wn, int lane) {
     using St = Stager<C, DIR>;
     if constexpr (R < C::FN) {
-      if constexpr (St::kYAlong) y[R] = read_along(lds + C::kX, wn * C::NW + R * 16, kk, lane);
-      else y[R] = read_across<C::BN>(lds + C::kX, wn * C::NW + R * 16, kk, lane);
+      if constexpr (St::kYAlong) y[R] = read_along(lds + C::kX, wn * C::NW + R * 16, lane);
+      else y[R] = read_across<C::BN>(lds + C::kX, wn * C::NW + R * 16, lane);
     } else {
       constexpr int i = R - C::FN;
-      if constexpr (St::kXAlong) x[i] = read_along(lds, wm * C::MW + i * 16, kk, lane);
-      else x[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, kk, lane);
+      if constexpr (St::kXAlong) x[i] = read_along(lds, wm * C::MW + i * 16, lane);
+      else x[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, lane);
     }
   }
 };
@@ -532,16 +572,17 @@ template <int I, int N, class F> __device__ __forceinline__ void each_of(F&& f) 
   }
 }
 
-// Half a slice: the products of `now`, with the reads of `then` from `from` and (LOAD) the loads of a slice into `to`
-// between them, in this order: a wave issues in order, and a run of loads would hold its products up.
-template <class C, int DIR, bool LOAD> __device__ __forceinline__ void half(Stager<C, DIR>& st, const Operands<C, DIR>& now, Operands<C, DIR>& then, AR_LDS char* from, int kk,
-                                                                            AR_LDS char* to, f32x4 (&acc)[C::FM][C::FN], int wm, int wn, int lane) {
+// One slice: the products of `now`, with the reads of the next one, `then`, from `from` and the loads of another into
+// `to` between them, in this order: a wave issues in order, and a run of loads would hold its products up.
+template <class C, int DIR> __device__ __forceinline__ void slice(Stager<C, DIR>& st, const Operands<C, DIR>& now, Operands<C, DIR>& then, AR_LDS char* from,
+                                                                  AR_LDS char* to, f32x4 (&acc)[C::FM][C::FN], int wm, int wn, int lane) {
   using O = Operands<C, DIR>;
-  constexpr int kLoads = Stager<C, DIR>::kLoads, kProducts = C::FM * C::FN, kParts = kProducts < 8 ? kProducts : 8;
+  constexpr int kLoads = Stager<C, DIR>::kLoads, kProducts = C::FM * C::FN, kParts = 4, kEarly = 3;  // the last reads have a part to return
   each_of<0, kParts>([&](auto part) {
-    constexpr int g = part, early = kParts > 4 ? kParts * 3 / 4 : kParts;  // the reads come in the first parts, and have the last to return
-    if constexpr (LOAD) each_of<kLoads * g / kParts, kLoads * (g + 1) / kParts>([&](auto i) { st.template load<i>(to); });
-    if constexpr (g < early) each_of<O::kReads * g / early, O::kReads * (g + 1) / early>([&](auto i) { then.template read<i>(from, kk, wm, wn, lane); });
+    constexpr int g = part;
+    each_of<kLoads * g / kParts, kLoads * (g + 1) / kParts>([&](auto i) { st.template load<i>(to); });
+    if constexpr (g == kParts - 1) st.advance();
+    if constexpr (g < kEarly) each_of<O::kReads * g / kEarly, O::kReads * (g + 1) / kEarly>([&](auto i) { then.template read<i>(from, wm, wn, lane); });
     each_of<kProducts * g / kParts, kProducts * (g + 1) / kParts>([&](auto p) {
       constexpr int i = p / C::FN, j = p % C::FN;
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.x[i], now.y[j], acc[i][j], 0, 0, 0);
@@ -573,17 +614,18 @@ __device__ __forceinline__ int chunk_active(const Product& a) { return min(max(a
 // KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
 // the outputs' type.
 template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
-  __shared__ __attribute__((aligned(16))) char shared[2 * C::kStage];
+  __shared__ __attribute__((aligned(512))) char shared[C::kStages * C::kStage];
   AR_LDS char* lds = (AR_LDS char*)shared;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64), wm = wave % C::WM, wn = wave / C::WM;
   const int active = chunk_active(a);
   const int nlen = DIR == S_WEIGHT ? a.Vp : active;
   const int ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles;
   const int64_t tiles = int64_t(ntiles) * mtiles;
-  const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + kBK - 1) / kBK * kBK;
+  const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK;
   const int passes = a.planes == 1 ? 1 : 6;
   const int steps = depth / kBK;
   Stager<C, DIR> st{a, 0, 0, tid, steps};
+  st.wave = wave;
   for (int64_t t = blockIdx.x; t < tiles * a.splits; t += gridDim.x) {
     const int split = int(t / tiles);
     // Workgroups go to the eight dies in turn: each die gets a run of tiles, and of a run eight tiles of n share
@@ -599,7 +641,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 
     st.begin(m0, n0);
     const int all = steps * passes;
-    const int s0 = int(int64_t(all) * split / a.splits), s1 = int(int64_t(all) * (split + 1) / a.splits);
+    const int s0 = int(int64_t(all / 2) * split / a.splits) * 2, s1 = int(int64_t(all / 2) * (split + 1) / a.splits) * 2;
 
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
@@ -607,34 +649,38 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    // Half a slice is multiplied while the next half is read from LDS, and a slice is loaded a whole slice before
-    // it is read, into the one that has just been: one barrier a slice.
+    // A slice is multiplied from registers while the next is read from LDS and another loaded into LDS, kStages
+    // ahead, where the slice itself has been: one barrier a slice. Two at a time, for the two sets of registers.
     if (s0 < s1) {
-      Operands<C, DIR> f0, f1;
       constexpr int kLoads = Stager<C, DIR>::kLoads;
+      Operands<C, DIR> f0, f1;
+      __builtin_amdgcn_s_waitcnt(waits(0));
       st.seek(s0, s1);
-      each_of<0, kLoads>([&](auto i) { st.template load<i>(lds); });
-      st.seek(s0 + 1, s1);
-      each_of<0, kLoads>([&](auto i) { st.template load<i>(lds + C::kStage); });
-      __builtin_amdgcn_s_waitcnt(kLoadsDone);
+      for (int i = 0; i < C::kStages; ++i) {
+        each_of<0, kLoads>([&](auto l) { st.template load<l>(lds + i * C::kStage); });
+        st.advance();
+        if (i & 1) st.turn();
+      }
+      __builtin_amdgcn_s_waitcnt(waits((C::kStages - 1) * kLoads));
       __syncthreads();
-      each_of<0, Operands<C, DIR>::kReads>([&](auto i) { f0.template read<i>(lds, 0, wm, wn, lane); });
+      each_of<0, Operands<C, DIR>::kReads>([&](auto i) { f0.template read<i>(lds, wm, wn, lane); });
       AR_LDS char *here = lds, *there = lds + C::kStage;
-      for (int s = s0; s < s1; ++s) {
-        st.seek(s + 2, s1);
-        __builtin_amdgcn_sched_barrier(0);
-        half<C, DIR, false>(st, f0, f1, here, 1, nullptr, acc, wm, wn, lane);
+      const auto step = [&](const Operands<C, DIR>& now, Operands<C, DIR>& then) {
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(kAllDone);  // this wave has read the slice, and its loads of the next are in LDS
+        __builtin_amdgcn_s_waitcnt(waits((C::kStages - 2) * kLoads));  // this wave has read `here`, and its loads are in `there`
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
-        half<C, DIR, true>(st, f1, f0, there, 0, here, acc, wm, wn, lane);
-        AR_LDS char* t2 = here;
+        slice<C, DIR>(st, now, then, there, here, acc, wm, wn, lane);
         here = there;
-        there = t2;
+        there = there == lds + (C::kStages - 1) * C::kStage ? lds : there + C::kStage;
+      };
+      for (int s = s0; s < s1; s += 2) {
+        step(f0, f1);
+        step(f1, f0);
+        st.turn();
       }
-      __builtin_amdgcn_s_waitcnt(kAllDone);
+      __builtin_amdgcn_s_waitcnt(waits(0));
     }
     __syncthreads();
 
@@ -990,7 +1036,7 @@ struct Plan {
 };
 
 int64_t tiles_of(Size z, int64_t m, int64_t n) {
-  const int64_t bm = z == Z_L ? 256 : 128, bn = z == Z_L ? 256 : z == Z_M ? 128 : 32;
+  const int64_t bm = z == Z_L ? 256 : 128, bn = z == Z_L ? 256 : z == Z_M ? 128 : 64;
   return ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
 }
 
@@ -1008,7 +1054,7 @@ int splits_for(int64_t tiles, int64_t steps, int64_t part_bytes) {
 Plan plan_of(const Vocab& v, bool grad) {
   Plan p{};
   p.planes = v.dtype == D_FP32 ? 3 : 1;
-  p.Hp = int(up(size_t(v.H), kBK));
+  p.Hp = int(up(size_t(v.H), 2 * kBK));
   p.K = std::max(1, v.top);
   p.packed = v.dtype == D_FP32 || v.H % 8;
   for (const VocabPiece& q : v.pieces) {
