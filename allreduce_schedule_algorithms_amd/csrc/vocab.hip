@@ -331,14 +331,15 @@ enum Dir { S_LOGITS = 0, S_HIDDEN = 1, S_WEIGHT = 2 };
 template <int BM_, int BN_, int WM_, int WN_, int WAVES_, int STAGES_> struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, kThreads = WM * WN * 64;
   static constexpr int MW = BM / WM, NW = BN / WN;  // a wave's part
+  static_assert(NW <= 64, "a lane looks after one of a wave's n");
   static constexpr int FM = MW / 16, FN = NW / 16;
   static constexpr int kWaves = WAVES_;  // of a SIMD, which bounds the registers
-  static constexpr int kStages = STAGES_;  // slices in LDS, an even number
+  static constexpr int kStages = STAGES_;  // slices in LDS, an odd number
   static constexpr int kX = BM * kBK * 2, kY = BN * kBK * 2, kStage = kX + kY;
 };
-using TileL = Tile<256, 256, 2, 4, 2, 4>;
-using TileM = Tile<128, 128, 2, 2, 2, 4>;
-using TileS = Tile<128, 64, 4, 1, 2, 6>;
+using TileL = Tile<256, 256, 2, 4, 2, 5>;
+using TileM = Tile<128, 128, 2, 2, 2, 5>;
+using TileS = Tile<128, 64, 4, 1, 2, 5>;
 
 struct Product {
   const Piece* pieces;
@@ -371,8 +372,8 @@ __device__ __forceinline__ Rsrc rsrc_of(const char* base, int bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
   return Rsrc{int32_t(p), int32_t(p >> 32) & 0xffff, bytes, 0x00020000};
 }
-// s_waitcnt: every LDS operation done, and all but the last n vector memory operations.
-constexpr int waits(int n) { return (n & 15) | (n >> 4) << 14 | 0x70; }
+// s_waitcnt: all but the last n vector memory operations done, and (lds) every LDS operation.
+constexpr int waits(int n, bool lds = true) { return (n & 15) | (n >> 4) << 14 | 0x70 | (lds ? 0 : 0xf00); }
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: such a lane loads zeros
 
 // 16 bytes a lane straight into LDS, lane after lane. Written out because the compiler, where it knows of such a
@@ -393,23 +394,24 @@ template <int R> __device__ __forceinline__ uint32_t across_swizzle(uint32_t kro
 // an offset that alternates where the swizzle does.
 template <int R, int THREADS, bool ALONG> struct Loads {
   static constexpr int kCount = R * kBK * 2 / (THREADS * 16), kStep = ALONG ? THREADS / 4 : THREADS / (R / 8);
-  static_assert(kStep % 16 == 0 && R * kBK * 2 % (THREADS * 16) == 0, "the swizzle repeats");
-  uint32_t off[2], c;
+  static constexpr int kOffsets = ALONG || kStep >= 32 ? 1 : 32 / kStep;
+  static_assert(kStep % (ALONG ? 16 : 8) == 0 && R * kBK * 2 % (THREADS * 16) == 0, "the swizzle repeats");
+  uint32_t off[kOffsets], c;
 
   __device__ __forceinline__ void set(uint32_t ldb, int tid) {
     if constexpr (ALONG) {
       const uint32_t row = uint32_t(tid) / 4;
       c = (uint32_t(tid) % 4) ^ along_swizzle(row);
-      off[0] = off[1] = row * ldb + c * 16;
+      off[0] = row * ldb + c * 16;
     } else {
       const uint32_t krow = uint32_t(tid) / (R / 8), slot = uint32_t(tid) % (R / 8);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) off[i] = krow * ldb + (((slot / 2) ^ across_swizzle<R>(krow + i * kStep)) * 2 + slot % 2) * 16;
+      for (int i = 0; i < kOffsets; ++i) off[i] = krow * ldb + (((slot / 2) ^ across_swizzle<R>(krow + i * kStep)) * 2 + slot % 2) * 16;
     }
   }
   // Of a row along k, `left` elements exist.
   __device__ __forceinline__ uint32_t at(int i, uint32_t ldb, int left) const {
-    const uint32_t o = off[kStep % 32 ? i & 1 : 0] + i * kStep * ldb;
+    const uint32_t o = off[i % kOffsets] + i * kStep * ldb;
     return !ALONG || int(c * 8) < left ? o : kNowhere;
   }
 };
@@ -548,20 +550,19 @@ template <class C, int DIR> struct Stager {
   }
 };
 
-// A wave's operands of a slice.
+// A wave's operands: a whole slice's of y, and a ring of x that is read kAhead products' rows ahead.
 template <class C, int DIR> struct Operands {
-  static constexpr int kReads = C::FM + C::FN;
-  bf16x8 x[C::FM], y[C::FN];
-  template <int R> __device__ __forceinline__ void read(AR_LDS char* lds, int wm, int wn, int lane) {
-    using St = Stager<C, DIR>;
-    if constexpr (R < C::FN) {
-      if constexpr (St::kYAlong) y[R] = read_along(lds + C::kX, wn * C::NW + R * 16, lane);
-      else y[R] = read_across<C::BN>(lds + C::kX, wn * C::NW + R * 16, lane);
-    } else {
-      constexpr int i = R - C::FN;
-      if constexpr (St::kXAlong) x[i] = read_along(lds, wm * C::MW + i * 16, lane);
-      else x[i] = read_across<C::BM>(lds, wm * C::MW + i * 16, lane);
-    }
+  static constexpr int kRing = 4, kAhead = C::FM < kRing ? C::FM : kRing - 1;
+  static_assert(2 * C::FM % kRing == 0, "two slices go round the ring");
+  bf16x8 x[kRing], y[2][C::FN];
+  int wm, wn, lane;
+  template <int I, int SLOT> __device__ __forceinline__ void read_x(AR_LDS char* lds) {
+    if constexpr (Stager<C, DIR>::kXAlong) x[SLOT % kRing] = read_along(lds, wm * C::MW + I * 16, lane);
+    else x[SLOT % kRing] = read_across<C::BM>(lds, wm * C::MW + I * 16, lane);
+  }
+  template <int J, int SET> __device__ __forceinline__ void read_y(AR_LDS char* lds) {
+    if constexpr (Stager<C, DIR>::kYAlong) y[SET][J] = read_along(lds + C::kX, wn * C::NW + J * 16, lane);
+    else y[SET][J] = read_across<C::BN>(lds + C::kX, wn * C::NW + J * 16, lane);
   }
 };
 
@@ -572,20 +573,22 @@ template <int I, int N, class F> __device__ __forceinline__ void each_of(F&& f) 
   }
 }
 
-// One slice: the products of `now`, with the reads of the next one, `then`, from `from` and the loads of another into
-// `to` between them, in this order: a wave issues in order, and a run of loads would hold its products up.
-template <class C, int DIR> __device__ __forceinline__ void slice(Stager<C, DIR>& st, const Operands<C, DIR>& now, Operands<C, DIR>& then, AR_LDS char* from,
-                                                                  AR_LDS char* to, f32x4 (&acc)[C::FM][C::FN], int wm, int wn, int lane) {
+// The products of the slice in `here` (the SET-th of two), with the reads of the next one's y from `there`, of x a
+// little ahead, and the loads of another slice into `to` between them, in this order: a wave issues in order, and a run
+// of loads would hold its products up.
+template <class C, int DIR, int SET> __device__ __forceinline__ void slice(Stager<C, DIR>& st, Operands<C, DIR>& o, AR_LDS char* here, AR_LDS char* there, AR_LDS char* to,
+                                                                           f32x4 (&acc)[C::FM][C::FN]) {
   using O = Operands<C, DIR>;
-  constexpr int kLoads = Stager<C, DIR>::kLoads, kProducts = C::FM * C::FN, kParts = 4, kEarly = 3;  // the last reads have a part to return
-  each_of<0, kParts>([&](auto part) {
-    constexpr int g = part;
-    each_of<kLoads * g / kParts, kLoads * (g + 1) / kParts>([&](auto i) { st.template load<i>(to); });
-    if constexpr (g == kParts - 1) st.advance();
-    if constexpr (g < kEarly) each_of<O::kReads * g / kEarly, O::kReads * (g + 1) / kEarly>([&](auto i) { then.template read<i>(from, wm, wn, lane); });
-    each_of<kProducts * g / kParts, kProducts * (g + 1) / kParts>([&](auto p) {
-      constexpr int i = p / C::FN, j = p % C::FN;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.x[i], now.y[j], acc[i][j], 0, 0, 0);
+  constexpr int kLoads = Stager<C, DIR>::kLoads, kEarly = C::FM * 3 / 4;  // the last of y have some products' time to return
+  each_of<0, C::FM>([&](auto row) {
+    constexpr int i = row, ahead = i + O::kAhead;
+    each_of<kLoads * i / C::FM, kLoads * (i + 1) / C::FM>([&](auto l) { st.template load<l>(to); });
+    if constexpr (i == C::FM - 1) st.advance();
+    if constexpr (ahead < C::FM) o.template read_x<ahead, SET * C::FM + ahead>(here);
+    else o.template read_x<ahead - C::FM, SET * C::FM + ahead>(there);
+    if constexpr (i < kEarly) each_of<C::FN * i / kEarly, C::FN * (i + 1) / kEarly>([&](auto j) { o.template read_y<j, 1 - SET>(there); });
+    each_of<0, C::FN>([&](auto j) {
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o.x[(SET * C::FM + i) % O::kRing], o.y[SET][j], acc[i][j], 0, 0, 0);
     });
     __builtin_amdgcn_sched_barrier(0);
   });
@@ -649,35 +652,42 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    // A slice is multiplied from registers while the next is read from LDS and another loaded into LDS, kStages
-    // ahead, where the slice itself has been: one barrier a slice. Two at a time, for the two sets of registers.
+    // While a slice is multiplied, the next one's y (and the first of its x) are read from LDS and another is loaded
+    // into LDS, kStages - 1 ahead, where the one before has been: one barrier a slice. Two at a time, for the two
+    // sets of y.
     if (s0 < s1) {
       constexpr int kLoads = Stager<C, DIR>::kLoads;
-      Operands<C, DIR> f0, f1;
+      using O = Operands<C, DIR>;
+      O o;
+      o.wm = wm;
+      o.wn = wn;
+      o.lane = lane;
       __builtin_amdgcn_s_waitcnt(waits(0));
       st.seek(s0, s1);
-      for (int i = 0; i < C::kStages; ++i) {
+      for (int i = 0; i < C::kStages - 1; ++i) {
         each_of<0, kLoads>([&](auto l) { st.template load<l>(lds + i * C::kStage); });
         st.advance();
         if (i & 1) st.turn();
       }
-      __builtin_amdgcn_s_waitcnt(waits((C::kStages - 1) * kLoads));
+      __builtin_amdgcn_s_waitcnt(waits((C::kStages - 2) * kLoads));
       __syncthreads();
-      each_of<0, Operands<C, DIR>::kReads>([&](auto i) { f0.template read<i>(lds, wm, wn, lane); });
-      AR_LDS char *here = lds, *there = lds + C::kStage;
-      const auto step = [&](const Operands<C, DIR>& now, Operands<C, DIR>& then) {
+      each_of<0, C::FN>([&](auto j) { o.template read_y<j, 0>(lds); });
+      each_of<0, O::kAhead>([&](auto i) { o.template read_x<i, i>(lds); });
+      AR_LDS char *last = lds + (C::kStages - 1) * C::kStage, *to = last, *here = lds, *there = lds + C::kStage;
+      const auto step = [&](auto set) {
         asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_waitcnt(waits((C::kStages - 2) * kLoads));  // this wave has read `here`, and its loads are in `there`
-        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_s_waitcnt(waits((C::kStages - 3) * kLoads, false));  // this wave's loads of `there` have arrived
+        __builtin_amdgcn_s_barrier();                                         // all waves' have, and `to` has been read
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
-        slice<C, DIR>(st, now, then, there, here, acc, wm, wn, lane);
+        slice<C, DIR, set>(st, o, here, there, to, acc);
+        to = here;
         here = there;
-        there = there == lds + (C::kStages - 1) * C::kStage ? lds : there + C::kStage;
+        there = there == last ? lds : there + C::kStage;
       };
       for (int s = s0; s < s1; s += 2) {
-        step(f0, f1);
-        step(f1, f0);
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
         st.turn();
       }
       __builtin_amdgcn_s_waitcnt(waits(0));
