@@ -18,7 +18,7 @@
 // left out is 2^-26 of a product).
 //
 // A call works on the tokens in chunks, so that its scratch is bounded: the logits' tile
-// leaves the product as exp(z - m), m the tile's largest, beside m and the tile's sum; once
+// leaves the product as exp(z - m), m the row's largest of the tile, beside m and the tile's sum; once
 // a row's lse is known, one pass turns them into D. Nothing is added atomically: the
 // same sizes give the same bits on every run.
 #include "vocab.h"
@@ -42,7 +42,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kBK = 32;         // depth of a slice: one product's, 64 bytes of a row
 constexpr int kPieceTab = 64;   // pieces that one launch's arguments carry
 constexpr int kUnit = 256;      // pieces and token chunks are padded to this many rows
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;  // softmax statistics are in units of it
 
 // One piece as the kernels see it, in the workspace. `first`: its first row in the vocabulary; `start`: the same
 // with every piece padded to kUnit rows, the coordinate that tiles, D and the ids' table use.
@@ -84,8 +84,6 @@ __device__ __forceinline__ int64_t id_at(const void* ids, bool wide, int64_t i) 
 __device__ __forceinline__ float logit_at(const void* p, int dtype, int64_t i) {
   return dtype == D_BF16 ? as_f(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16) : static_cast<const float*>(p)[i];
 }
-
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // x as a sum of three bf16 values, exactly: each is the nearest to what is left (a magnitude that would round to
 // an infinity is cut instead), and 24 bits leave at most 8 for the third.
@@ -217,7 +215,8 @@ struct PackArgs {
   const uint8_t* flags;
   const Counts* counts;
   char* hp;
-  int32_t* idt;  // [K or 1][Tpad]
+  int32_t* idt;  // [Tpad][Kp], -1 behind a row's ids
+  int32_t Kp;
   void* dh;      // null: no gradient
   int64_t dh_ld;
   float* each;   // every row's loss, or null
@@ -274,16 +273,16 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
       for (int c = lane * 8; c < PL * a.Hp; c += 512) *reinterpret_cast<bf16x8*>(dst + c) = bf16x8{};
     }
     if (i < end)
-      for (int k = lane; k < K; k += 64) {
+      for (int k = lane; k < a.Kp; k += 64) {
         int32_t at = -1;
-        if (i < active) {
+        if (i < active && k < K) {
           const int64_t id = t.K ? id_at(t.ids, t.wide, r * t.ids_ld + k) : id_at(t.ids, t.wide, r);
           if (id >= 0) {
             const Piece& p = a.pieces[piece_of<false>(a.pieces, a.P, int32_t(id))];
             at = p.start + int32_t(id) - p.first;
           }
         }
-        a.idt[int64_t(k) * a.Tpad + i] = at;
+        a.idt[i * a.Kp + k] = at;
       }
     if (i >= active && r >= 0) {
       if (a.each && lane == 0) a.each[r] = a.flags[r] == F_BAD ? NAN : 0.f;
@@ -350,13 +349,12 @@ struct Product {
   const char* hp;             // gathered hidden rows
   char* d;                    // [rows][planes * Vp]: exp(z - m), then D
   // logits
-  float scale;
+  float scale;  // log2(e) / temperature
   float2* stats;  // [Vp / BM][ld_stats]
   int64_t ld_stats;
-  const int32_t* idt;
-  int64_t ld_idt;
-  int32_t K;
-  float* zt;  // [rows][K]
+  const int32_t* idt;  // [rows][ld_idt], as zt
+  int32_t ld_idt;
+  float* zt;  // the logits at those ids, times log2(e)
   // gradients
   const int32_t* rows;
   void* dh;
@@ -374,6 +372,7 @@ __device__ __forceinline__ Rsrc rsrc_of(const char* base, int bytes) {
 }
 // s_waitcnt: all but the last n vector memory operations done, and (lds) every LDS operation.
 constexpr int waits(int n, bool lds = true) { return (n & 15) | (n >> 4) << 14 | 0x70 | (lds ? 0 : 0xf00); }
+constexpr int kLdsDone = 0xc07f;  // every LDS operation and scalar load done
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer: such a lane loads zeros
 
 // 16 bytes a lane straight into LDS, lane after lane. Written out because the compiler, where it knows of such a
@@ -542,6 +541,8 @@ template <class C, int DIR> struct Stager {
       ++pass;
     }
     find();
+    // no scalar load may be under way where the paths meet: the reads of LDS there could not be told from it
+    __builtin_amdgcn_s_waitcnt(kLdsDone);
   }
 
   template <int I> __device__ __forceinline__ void load(AR_LDS char* lds) {
@@ -594,58 +595,115 @@ template <class C, int DIR, int SET> __device__ __forceinline__ void slice(Stage
   });
 }
 
-// Four consecutive outputs of a row, of which `left` exist.
-template <int DT> __device__ __forceinline__ void put4(void* row, int m, f32x4 v, int left) {
-  if constexpr (DT == D_BF16) {
-    __bf16* p = static_cast<__bf16*>(row) + m;
-    const bf16x4 b = __builtin_convertvector(v, bf16x4);
-    typedef __bf16 U __attribute__((ext_vector_type(4), aligned(2)));
-    if (left >= 4) *reinterpret_cast<U*>(p) = b;
-    else
-      for (int e = 0; e < left; ++e) p[e] = b[e];
+// Consecutive outputs of a row, of which `left` exist, at any address.
+template <class E, class V> __device__ __forceinline__ void put(E* p, V v, int left) {
+  constexpr int kN = sizeof(V) / sizeof(E);
+  typedef E U __attribute__((ext_vector_type(kN), aligned(sizeof(E))));
+  if (left >= kN) {
+    *reinterpret_cast<U*>(p) = v;
   } else {
-    float* p = static_cast<float*>(row) + m;
-    typedef float U __attribute__((ext_vector_type(4), aligned(4)));
-    if (left >= 4) *reinterpret_cast<U*>(p) = v;
-    else
-      for (int e = 0; e < left; ++e) p[e] = v[e];
+#pragma unroll
+    for (int e = 0; e < kN - 1; ++e)
+      if (e < left) p[e] = v[e];
   }
 }
 
+// Two products' registers, m 4 (lane / 16) on of 16 each, rounded and exchanged between the quarters of the wave: m
+// 8 (lane / 16) on of the 32.
+__device__ __forceinline__ bf16x8 eight_of(f32x4 a, f32x4 b) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const u32x2 x = __builtin_bit_cast(u32x2, __builtin_convertvector(a, bf16x4)), y = __builtin_bit_cast(u32x2, __builtin_convertvector(b, bf16x4));
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto p = __builtin_amdgcn_permlane32_swap(x[i], y[i], false, false);  // quarters (a0, a1, b0, b1) and (a2, a3, b2, b3)
+    const auto q = __builtin_amdgcn_permlane16_swap(p[0], p[1], false, false);  // (a0, a2, b0, b2) and (a1, a3, b1, b3)
+    r[i] = q[0];
+    r[2 + i] = q[1];
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// A barrier for what the workgroup leaves in LDS, which waits for no load or store of global memory.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(kLdsDone);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 __device__ __forceinline__ int chunk_active(const Product& a) { return min(max(a.counts->active - a.chunk, 0), a.chunk_rows); }
+
+// Where a workgroup's tile t lies, and which slices of the depth it takes.
+struct Place {
+  int m0, n0, split, s0, s1;
+};
 
 // KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
 // the outputs' type.
 template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
   __shared__ __attribute__((aligned(512))) char shared[C::kStages * C::kStage];
-  AR_LDS char* lds = (AR_LDS char*)shared;
+  using St = Stager<C, DIR>;
+  using O = Operands<C, DIR>;
+  constexpr int kLoads = St::kLoads;
+  AR_LDS char *lds = (AR_LDS char*)shared, *last = lds + (C::kStages - 1) * C::kStage;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64), wm = wave % C::WM, wn = wave / C::WM;
   const int active = chunk_active(a);
   const int nlen = DIR == S_WEIGHT ? a.Vp : active;
   const int ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles;
   const int64_t tiles = int64_t(ntiles) * mtiles;
   const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK;
-  const int passes = a.planes == 1 ? 1 : 6;
-  const int steps = depth / kBK;
-  Stager<C, DIR> st{a, 0, 0, tid, steps};
+  const int steps = depth / kBK, all = steps * (a.planes == 1 ? 1 : 6);
+  St st{a, 0, 0, tid, steps};
   st.wave = wave;
-  for (int64_t t = blockIdx.x; t < tiles * a.splits; t += gridDim.x) {
-    const int split = int(t / tiles);
+  O o;
+  o.wm = wm;
+  o.wn = wn;
+  o.lane = lane;
+
+  const auto place = [&](int64_t t) {
+    Place p;
+    p.split = int(t / tiles);
     // Workgroups go to the eight dies in turn: each die gets a run of tiles, and of a run eight tiles of n share
     // their m with the neighbours, so that both operands are found in the die's cache.
-    int64_t u = t - split * tiles;
-    {
-      const int64_t per = tiles / 8, more = tiles % 8, die = u % 8, i = u / 8;
-      u = die * per + min(die, more) + i;
-    }
+    int64_t u = t - p.split * tiles;
+    const int64_t per = tiles / 8, more = tiles % 8, die = u % 8, i = u / 8;
+    u = die * per + min(die, more) + i;
     const int64_t group = u / (8 * int64_t(mtiles));
     const int in_group = int(u - group * 8 * mtiles), width = min(8, ntiles - int(group) * 8);
-    const int m0 = in_group / width * C::BM, n0 = (int(group) * 8 + in_group % width) * C::BN;
+    p.m0 = in_group / width * C::BM;
+    p.n0 = (int(group) * 8 + in_group % width) * C::BN;
+    p.s0 = int(int64_t(all / 2) * p.split / a.splits) * 2;
+    p.s1 = int(int64_t(all / 2) * (p.split + 1) / a.splits) * 2;
+    return p;
+  };
+  // The first kStages - 1 slices of a tile, on their way into LDS.
+  const auto start = [&](const Place& p) {
+    st.begin(p.m0, p.n0);
+    if (p.s0 >= p.s1) return;
+    st.seek(p.s0, p.s1);
+    for (int i = 0; i < C::kStages - 1; ++i) {
+      each_of<0, kLoads>([&](auto l) { st.template load<l>(lds + i * C::kStage); });
+      st.advance();
+      if (i & 1) st.turn();
+    }
+  };
 
-    st.begin(m0, n0);
-    const int all = steps * passes;
-    const int s0 = int(int64_t(all / 2) * split / a.splits) * 2, s1 = int(int64_t(all / 2) * (split + 1) / a.splits) * 2;
-
+  int64_t t = blockIdx.x;
+  if (t >= tiles * a.splits) return;
+  Place at = place(t);
+  start(at);
+  while (true) {
+    const int wn0 = at.n0 + wn * C::NW, wm0 = at.m0 + wm * C::MW;
+    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+    i32x4 ids = {-1, -1, -1, -1};  // of row wn0 + lane: the first four
+    const i32x4* id_row = nullptr;
+    if constexpr (DIR == S_LOGITS)
+      if (lane < C::NW && wn0 + lane < active) {
+        id_row = reinterpret_cast<const i32x4*>(a.idt + int64_t(a.chunk + wn0 + lane) * a.ld_idt);
+        ids = id_row[0];
+      }
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
@@ -655,25 +713,12 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     // While a slice is multiplied, the next one's y (and the first of its x) are read from LDS and another is loaded
     // into LDS, kStages - 1 ahead, where the one before has been: one barrier a slice. Two at a time, for the two
     // sets of y.
-    if (s0 < s1) {
-      constexpr int kLoads = Stager<C, DIR>::kLoads;
-      using O = Operands<C, DIR>;
-      O o;
-      o.wm = wm;
-      o.wn = wn;
-      o.lane = lane;
-      __builtin_amdgcn_s_waitcnt(waits(0));
-      st.seek(s0, s1);
-      for (int i = 0; i < C::kStages - 1; ++i) {
-        each_of<0, kLoads>([&](auto l) { st.template load<l>(lds + i * C::kStage); });
-        st.advance();
-        if (i & 1) st.turn();
-      }
+    if (at.s0 < at.s1) {
       __builtin_amdgcn_s_waitcnt(waits((C::kStages - 2) * kLoads));
       __syncthreads();
       each_of<0, C::FN>([&](auto j) { o.template read_y<j, 0>(lds); });
       each_of<0, O::kAhead>([&](auto i) { o.template read_x<i, i>(lds); });
-      AR_LDS char *last = lds + (C::kStages - 1) * C::kStage, *to = last, *here = lds, *there = lds + C::kStage;
+      AR_LDS char *to = last, *here = lds, *there = lds + C::kStage;
       const auto step = [&](auto set) {
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(waits((C::kStages - 3) * kLoads, false));  // this wave's loads of `there` have arrived
@@ -685,47 +730,70 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
         here = there;
         there = there == last ? lds : there + C::kStage;
       };
-      for (int s = s0; s < s1; s += 2) {
+      for (int s = at.s0; s < at.s1; s += 2) {
         step(std::integral_constant<int, 0>{});
         step(std::integral_constant<int, 1>{});
         st.turn();
       }
-      __builtin_amdgcn_s_waitcnt(waits(0));
     }
+    __builtin_amdgcn_s_waitcnt(waits(0));
     __syncthreads();
 
+    const int piece_left = DIR == S_LOGITS ? st.rows - (at.m0 - st.start) : 0;  // rows of the piece from the tile's first on
     if constexpr (DIR == S_LOGITS) {
-      AR_LDS float* top = (AR_LDS float*)lds;         // [WM][BN]
-      AR_LDS float* sum = top + C::WM * C::BN;        // [WM][BN]
-      const int left = st.rows - (m0 - st.start) - wm * C::MW - lane / 16 * 4;
+      // Everything is in units of log 2 from here on: x = z log2(e) is one product with the sum, and 2^(x - m) one
+      // more operation. (a.scale carries a rounding of 2^-24 of x, the same for all.)
+      if (piece_left < C::BM) {
+        const int left = piece_left - wm * C::MW - lane / 16 * 4;
 #pragma unroll
-      for (int i = 0; i < C::FM; ++i)
+        for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
+          for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = i * 16 + e < left ? acc[i][j][e] * a.scale : -INFINITY;
-      // the logits of the rows' own ids
-      const int wn0 = n0 + wn * C::NW, wm0 = m0 + wm * C::MW;
-      for (int k = 0; k < a.K; ++k) {
-        int rel = -1;
-        if (lane < C::NW && wn0 + lane < active) rel = a.idt[k * a.ld_idt + a.chunk + wn0 + lane] - wm0;
-        uint64_t hit = __ballot(rel >= 0 && rel < C::MW);
-        while (hit) {
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = i * 16 + e < left ? acc[i][j][e] : -INFINITY;
+      }
+      // the logits of the rows' own ids: a lane compares its row's, the wave takes the hits one by one
+      for (int k = 0; k < a.ld_idt; k += k ? 16 : 4) {
+        i32x4 batch[4] = {ids, {-1, -1, -1, -1}, {-1, -1, -1, -1}, {-1, -1, -1, -1}};
+        if (k) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) batch[q] = id_row && k + 4 * q < a.ld_idt ? id_row[k / 4 + q] : i32x4{-1, -1, -1, -1};
+        }
+        uint32_t mine = 0;  // which of the sixteen are in the wave's part of the tile
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mine |= uint32_t(batch[e / 4][e % 4] - wm0) < uint32_t(C::MW) ? 1u << e : 0u;
+        for (uint64_t hit = __ballot(mine != 0); hit; hit = __ballot(mine != 0)) {
           const int src = __builtin_ctzll(hit);
-          hit &= hit - 1;
-          const int r = __builtin_amdgcn_readlane(rel, src);
-          float v = 0;
+          const int which = __builtin_ctz(__builtin_amdgcn_readlane(int(mine), src));
+          int32_t id = 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) id = which == e ? batch[e / 4][e % 4] : id;
+          const int r = __builtin_amdgcn_readlane(id, src) - wm0;
+          f32x4 x = {0, 0, 0, 0};
 #pragma unroll
           for (int i = 0; i < C::FM; ++i)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
-              if (r / 16 == i && src / 16 == j) {
-                const f32x4 x = acc[i][j];
-                v = r % 4 == 0 ? x[0] : r % 4 == 1 ? x[1] : r % 4 == 2 ? x[2] : x[3];
-              }
-          if (lane == r % 16 / 4 * 16 + src % 16) a.zt[int64_t(wn0 + src) * a.K + k] = v;
+              if (r / 16 == i && src / 16 == j) x = acc[i][j];
+          const float v = r % 4 == 0 ? x[0] : r % 4 == 1 ? x[1] : r % 4 == 2 ? x[2] : x[3];
+          if (lane == r % 16 / 4 * 16 + src % 16) a.zt[int64_t(wn0 + src) * a.ld_idt + k + which] = v * a.scale;
+          if (lane == src) mine &= mine - 1;
         }
       }
+    }
+    // The next tile's first slices travel while this one's results are written; `last` is free of them until the
+    // next tile's first barrier.
+    const Place done = at;
+    t += gridDim.x;
+    const bool more = t < tiles * a.splits;
+    if (more) {
+      at = place(t);
+      start(at);
+    }
+
+    if constexpr (DIR == S_LOGITS) {
+      AR_LDS float* top = (AR_LDS float*)last;  // [WM][BN]
+      AR_LDS float* sum = top + C::WM * C::BN;  // [WM][BN]
       float mx[C::FN];
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) {
@@ -733,37 +801,36 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 #pragma unroll
         for (int i = 0; i < C::FM; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) m = fmaxf(m, acc[i][j][e]);
+          for (int e = 0; e < 4; e += 2) m = fmaxf(fmaxf(m, acc[i][j][e]), acc[i][j][e + 1]);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
         if (lane < 16) top[wm * C::BN + wn * C::NW + j * 16 + lane] = m;
       }
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) {
         float m = -INFINITY;
 #pragma unroll
         for (int w = 0; w < C::WM; ++w) m = fmaxf(m, top[w * C::BN + wn * C::NW + j * 16 + lane % 16]);
-        mx[j] = m == -INFINITY ? 0.f : m;  // a tile without rows of the vocabulary: exponentials of 0
+        mx[j] = m == -INFINITY ? 0.f : m * a.scale;  // a tile without rows of the vocabulary: exponentials of 0
         float s = 0;
-        const int64_t n = n0 + wn * C::NW + j * 16 + lane % 16;
+        const int64_t row = int64_t(wn0 + j * 16 + lane % 16) * a.Vp + wm0;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
-          f32x4 x;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[e] = exp_of(acc[i][j][e] - mx[j]);
-            s += x[e];
+            acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.scale, -mx[j]));
+            s += acc[i][j][e];
           }
-          const int64_t at = int64_t(n) * a.Vp + wm0 + i * 16 + lane / 16 * 4;
-          if constexpr (KEEP == D_BF16) *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(a.d) + at) = __builtin_convertvector(x, bf16x4);
-          if constexpr (KEEP == D_FP32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.part) + at) = x;
+          if constexpr (KEEP == D_BF16)
+            if (i & 1) *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + row + (i - 1) * 16 + lane / 16 * 8) = eight_of(acc[i - 1][j], acc[i][j]);
+          if constexpr (KEEP == D_FP32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.part) + row + i * 16 + lane / 16 * 4) = acc[i][j];
         }
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (lane < 16) sum[wm * C::BN + wn * C::NW + j * 16 + lane] = s;
       }
-      __syncthreads();
+      lds_barrier();
       if (wm == 0 && lane < 16)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j) {
@@ -771,39 +838,47 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
           float s = 0;
 #pragma unroll
           for (int w = 0; w < C::WM; ++w) s += sum[w * C::BN + n];
-          a.stats[int64_t(m0 / C::BM) * a.ld_stats + n0 + n] = float2{mx[j], s};
+          a.stats[int64_t(done.m0 / C::BM) * a.ld_stats + done.n0 + n] = float2{mx[j], s};
         }
-      __syncthreads();
     } else {
+      constexpr int kBytes = KEEP == D_BF16 ? 2 : 4;
+      // a tile of the vocabulary lies in one piece
+      const Piece* p = nullptr;
+      if constexpr (DIR == S_WEIGHT) p = a.pieces + __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, done.n0));
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) {
-        const int n = n0 + wn * C::NW + j * 16 + lane % 16;
-        if (n >= nlen) continue;
+        const int n = wn0 + j * 16 + lane % 16;
         char* row = nullptr;
+        bool there = n < nlen;
         if (!a.part) {
-          constexpr int e = KEEP == D_BF16 ? 2 : 4;
           if constexpr (DIR == S_HIDDEN) {
-            row = static_cast<char*>(a.dh) + int64_t(a.rows[a.chunk + n]) * a.dh_ld * e;
+            if (there) row = static_cast<char*>(a.dh) + int64_t(a.rows[a.chunk + n]) * a.dh_ld * kBytes;
           } else {
-            const Piece& p = a.pieces[piece_of<true>(a.pieces, a.P, n)];
-            if (n - p.start >= p.rows) continue;
-            row = p.dw + int64_t(n - p.start) * p.dld * e;
+            there = n - p->start < p->rows;
+            row = p->dw + int64_t(n - p->start) * p->dld * kBytes;
           }
         }
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
-          const int m = m0 + wm * C::MW + i * 16 + lane / 16 * 4;
+          const int m = wm0 + i * 16 + lane / 16 * 4;
           if (a.part) {
-            if (m < a.Hp) {
-              f32x4* q = reinterpret_cast<f32x4*>(a.part + split * a.part_stride + int64_t(n) * a.Hp + m);
+            if (there && m < a.Hp) {
+              f32x4* q = reinterpret_cast<f32x4*>(a.part + done.split * a.part_stride + int64_t(n) * a.Hp + m);
               *q = a.accumulate ? *q + acc[i][j] : acc[i][j];
             }
-          } else if (m < a.H) {
-            put4<KEEP>(row, m, acc[i][j], a.H - m);
+          } else if constexpr (KEEP == D_BF16) {
+            if (i & 1) {
+              const int m8 = wm0 + (i - 1) * 16 + lane / 16 * 8;
+              const bf16x8 v = eight_of(acc[i - 1][j], acc[i][j]);
+              if (there && m8 < a.H) put(reinterpret_cast<__bf16*>(row) + m8, v, a.H - m8);
+            }
+          } else {
+            if (there && m < a.H) put(reinterpret_cast<float*>(row) + m, acc[i][j], a.H - m);
           }
         }
       }
     }
+    if (!more) return;
   }
 }
 
@@ -820,7 +895,7 @@ struct Soft {
   int32_t planes, block;  // block: columns a statistic covers
   int64_t Vp;
   float temperature;
-  float* lse;    // [chunk rows]
+  float* lse;    // [chunk rows], times log2(e), as the statistics
   float* coef;   // [chunk rows]: the row's weight in the loss over the temperature; 0 behind the rows
   float* exps;   // fp32: exp(z - m)
   char* d;
@@ -840,7 +915,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a) {
         const float2 x = a.stats[int64_t(b) * a.ld_stats + r];
         if (x.y == 0) continue;
         const float top = fmaxf(m, x.x);  // a NaN sum stays one
-        s = (m == top ? s : s * expf(m - top)) + (x.x == top ? x.y : x.y * expf(x.x - top));
+        s = (m == top ? s : s * exp2f(m - top)) + (x.x == top ? x.y : x.y * exp2f(x.x - top));
         m = top;
       }
     part[slice][row] = float2{m, s};
@@ -853,9 +928,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a) {
         float all = 0;
         for (int w = 0; w < kJoinThreads / 16; ++w) {
           const float2 x = part[w][row];
-          if (x.y != 0) all += x.y * expf(x.x - top);
+          if (x.y != 0) all += x.y * exp2f(x.x - top);
         }
-        lse = top + logf(all);
+        lse = top + log2f(all);
         coef = 1.f / a.temperature;
         if (a.weights) coef *= a.weights[a.rows[a.chunk + r]];
         if (a.reduction == R_MEAN) coef /= float(a.counts->mean);
@@ -882,7 +957,7 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
       const int64_t c = c0 + b * 128;
       float f = 0;
       const float w = a.coef[r0 + r];
-      if (w != 0 && c < a.Vp) f = exp_of(a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r]) * w;
+      if (w != 0 && c < a.Vp) f = exp2f(a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r]) * w;
       factor[r][b] = f;
     }
     __syncthreads();
@@ -925,7 +1000,7 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
 struct Ends {
   const float2* teacher;  // by original row
   const int32_t* idt;
-  int64_t ld_idt;
+  int32_t ld_idt;
   const float* zt;
   float* row_loss;  // [rows that take part], weighted
   float* each;      // by original row, or null
@@ -937,6 +1012,7 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_targ
   for (int i = blockIdx.x * kRowWaves + threadIdx.x / 64; i < active; i += gridDim.x * kRowWaves) {
     const int64_t r = a.rows[a.chunk + i];
     const float lse = a.lse[i], coef = a.coef[i];
+    const int32_t* ids = e.idt + (a.chunk + i) * int64_t(e.ld_idt);
     float2 stat = {0, 1};
     if (t.K) stat = e.teacher[r];
     auto q_of = [&](int k, float* x) {
@@ -946,22 +1022,22 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_targ
     };
     float loss = 0;
     for (int k = lane; k < K; k += 64) {
-      const int32_t id = e.idt[k * e.ld_idt + a.chunk + i];
+      const int32_t id = ids[k];
       if (id < 0) continue;
-      const float z = e.zt[int64_t(i) * K + k];
+      const float z = e.zt[int64_t(i) * e.ld_idt + k];
       float x = 0;
       const float q = q_of(k, &x);
-      if (q != 0) loss += q * ((t.K ? x - logf(stat.y) : 0.f) + (lse - z));
+      if (q != 0) loss += q * ((t.K ? x - logf(stat.y) : 0.f) + (lse - z) * kLn2);
       if (e.grad) {
         float all = q;
         if (t.K) {
           all = 0;
           for (int l = 0; l < K; ++l) {
             float y;
-            if (e.idt[l * e.ld_idt + a.chunk + i] == id) all += q_of(l, &y);
+            if (ids[l] == id) all += q_of(l, &y);
           }
         }
-        const float d = coef * (expf(z - lse) - all);
+        const float d = coef * (exp2f(z - lse) - all);
         __bf16* row = reinterpret_cast<__bf16*>(a.d) + (DT == D_BF16 ? int64_t(i) * a.Vp : int64_t(i) * 3 * a.Vp);
         if constexpr (DT == D_BF16) {
           row[id] = __bf16(d);
@@ -1018,7 +1094,8 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
     }
     f32x4 s = {0, 0, 0, 0};
     for (int k = 0; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(a.part + k * a.part_stride + int64_t(n) * a.Hp + m);
-    put4<DT>(row, m, s, a.H - m);
+    if constexpr (DT == D_BF16) put(reinterpret_cast<__bf16*>(row) + m, __builtin_convertvector(s, bf16x4), a.H - m);
+    else put(reinterpret_cast<float*>(row) + m, s, a.H - m);
   }
 }
 
@@ -1035,7 +1112,7 @@ constexpr int64_t kChunkBytes = int64_t(4) << 30;
 constexpr int kUnits = 256;  // compute units
 
 struct Plan {
-  int planes, Hp, K;
+  int planes, Hp, Kp;  // Kp: ids of a row, whole vectors of them
   int64_t V = 0, Vp = 0, Tpad, Tc, chunks;
   bool packed;
   Size logits, hidden, weight;
@@ -1065,7 +1142,7 @@ Plan plan_of(const Vocab& v, bool grad) {
   Plan p{};
   p.planes = v.dtype == D_FP32 ? 3 : 1;
   p.Hp = int(up(size_t(v.H), 2 * kBK));
-  p.K = std::max(1, v.top);
+  p.Kp = int(up(size_t(std::max(1, v.top)), 4));
   p.packed = v.dtype == D_FP32 || v.H % 8;
   for (const VocabPiece& q : v.pieces) {
     p.V += q.rows;
@@ -1088,13 +1165,13 @@ Plan plan_of(const Vocab& v, bool grad) {
   p.rows = take(size_t(p.Tpad) * 4);
   p.flags = take(size_t(p.Tpad));
   p.teacher = take(v.top ? size_t(p.Tpad) * 8 : 0);
-  p.idt = take(size_t(p.K) * size_t(p.Tpad) * 4);
+  p.idt = take(size_t(p.Kp) * size_t(p.Tpad) * 4);
   p.hp = take(size_t(p.Tpad) * size_t(p.planes) * size_t(p.Hp) * 2);
   p.wp = take(p.packed ? size_t(p.Vp) * size_t(p.planes) * size_t(p.Hp) * 2 : 0);
   p.lse = take(size_t(p.Tc) * 4);
   p.coef = take(size_t(p.Tc) * 4);
   p.row_loss = take(size_t(p.Tpad) * 4);
-  p.zt = take(size_t(p.Tc) * size_t(p.K) * 4);
+  p.zt = take(size_t(p.Tc) * size_t(p.Kp) * 4);
   p.stats = take(size_t(p.Vp / p.block) * size_t(p.Tc) * 8);
   if (grad) {
     p.exps = take(v.dtype == D_FP32 ? size_t(p.Tc) * size_t(p.Vp) * 4 : 0);
@@ -1111,7 +1188,9 @@ Plan plan_of(const Vocab& v, bool grad) {
   return p;
 }
 
-template <int DIR, int KEEP> void launch_product(Sequence& s, Size z, int64_t blocks, Product a) {
+template <int DIR, int KEEP> void launch_product(Sequence& s, Size z, int64_t tiles, Product a) {
+  const int64_t most = std::min<int64_t>(launch_blocks(), kUnits * (z == Z_L ? 1 : 2));  // as many as stay resident
+  const int64_t blocks = std::max<int64_t>(1, std::min(tiles * a.splits, most));
   if (z == Z_L) s.launch(k_vocab_product<TileL, DIR, KEEP>, blocks, TileL::kThreads, a);
   else if (z == Z_M) s.launch(k_vocab_product<TileM, DIR, KEEP>, blocks, TileM::kThreads, a);
   else if constexpr (DIR != S_WEIGHT) s.launch(k_vocab_product<TileS, DIR, KEEP>, blocks, TileS::kThreads, a);
@@ -1148,7 +1227,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   if (v.top) s.launch(k_vocab_teacher, blocks_of(row_blocks), kRowWaves * 64, t, v.T, teacher, flags);
   s.launch(k_vocab_scan, 1, kScanThreads, t, v.T, rows, flags, counts);
   const PackArgs pa{v.hidden, v.ld, v.T, p.Tpad, int32_t(v.H), p.Hp, int32_t(P), pieces, rows, flags, counts, ws + p.hp,
-                    reinterpret_cast<int32_t*>(ws + p.idt), grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
+                    reinterpret_cast<int32_t*>(ws + p.idt), p.Kp, grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
   s.launch(k_vocab_pack<DT>, blocks_of(row_blocks), kRowWaves * 64, pa, t);
   if (p.packed) {
     Piece* packed = reinterpret_cast<Piece*>(ws + p.packed_pieces);
@@ -1166,19 +1245,18 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.kend = p.packed ? p.Hp : int32_t(v.H);
   a.hp = ws + p.hp;
   a.d = ws + p.d;
-  a.scale = 1.f / v.temperature;
+  a.scale = float(1.4426950408889634 / double(v.temperature));
   a.stats = reinterpret_cast<float2*>(ws + p.stats);
   a.ld_stats = p.Tc;
   a.idt = pa.idt;
-  a.ld_idt = p.Tpad;
-  a.K = p.K;
+  a.ld_idt = p.Kp;
   a.zt = reinterpret_cast<float*>(ws + p.zt);
   a.rows = rows;
   a.dh = v.dh;
   a.dh_ld = v.dh_ld;
   Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
          v.temperature, reinterpret_cast<float*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
-  const Ends ends{teacher, pa.idt, p.Tpad, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, grad};
+  const Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, grad};
   float* dh_part = reinterpret_cast<float*>(ws + p.part);
   float* dw_part = dh_part;
   if (p.chunks > 1 && p.hidden_splits > 1) dw_part += size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp);
@@ -1189,9 +1267,9 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     a.mtiles = int32_t(p.Vp / p.block);
     a.splits = 1;
     a.part = f.exps;
-    const int64_t lb = blocks_of(tiles_of(p.logits, p.Vp, n));
-    if (grad) launch_product<S_LOGITS, DT>(s, p.logits, lb, a);
-    else launch_product<S_LOGITS, 0>(s, p.logits, lb, a);
+    const int64_t tiles = tiles_of(p.logits, p.Vp, n);
+    if (grad) launch_product<S_LOGITS, DT>(s, p.logits, tiles, a);
+    else launch_product<S_LOGITS, 0>(s, p.logits, tiles, a);
     s.launch(k_vocab_join, blocks_of(npad / kJoinRows), kJoinThreads, f);
     if (grad) s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f);
     s.launch(k_vocab_targets<DT>, blocks_of((n + kRowWaves - 1) / kRowWaves), kRowWaves * 64, f, ends, t);
@@ -1202,14 +1280,14 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     a.part = a.splits > 1 ? dh_part : nullptr;
     a.part_stride = p.Tc * p.Hp;
     a.accumulate = 0;
-    launch_product<S_HIDDEN, DT>(s, p.hidden, blocks_of(tiles_of(p.hidden, v.H, n) * a.splits), a);
+    launch_product<S_HIDDEN, DT>(s, p.hidden, tiles_of(p.hidden, v.H, n), a);
     if (a.splits > 1) s.launch(k_vocab_sum<S_HIDDEN, DT>, blocks_of((n * p.Hp / 4 + 255) / 256), 256, a);
     a.mtiles = mtiles(p.weight);
     a.splits = p.weight_splits;
     a.part = a.splits > 1 || p.chunks > 1 ? dw_part : nullptr;
     a.part_stride = p.Vp * p.Hp;
     a.accumulate = c > 0;
-    launch_product<S_WEIGHT, DT>(s, p.weight, blocks_of(tiles_of(p.weight, v.H, p.Vp) * a.splits), a);
+    launch_product<S_WEIGHT, DT>(s, p.weight, tiles_of(p.weight, v.H, p.Vp), a);
     if (a.part && c + 1 == p.chunks) s.launch(k_vocab_sum<S_WEIGHT, DT>, blocks_of((p.Vp * p.Hp / 4 + 255) / 256), 256, a);
   }
   if (!each) s.launch(k_vocab_loss, 1, 1024, ends.row_loss, counts, v.reduction, v.loss);
