@@ -27,10 +27,14 @@ struct Sequence {
   bool begun = false;
   hipError_t err = hipSuccess;
   template <typename... A> void launch(void (*k)(A...), int64_t blocks, int threads, typename Same<A>::type... a) {
+    launch_lds(k, blocks, threads, 0, a...);
+  }
+  // The same with dynamic LDS.
+  template <typename... A> void launch_lds(void (*k)(A...), int64_t blocks, int threads, size_t lds, typename Same<A>::type... a) {
     if (err != hipSuccess) return;
     --left;
     void* args[] = {static_cast<void*>(&a)...};
-    err = hipExtLaunchKernel(reinterpret_cast<const void*>(k), dim3(unsigned(blocks)), dim3(unsigned(threads)), args, 0, st,
+    err = hipExtLaunchKernel(reinterpret_cast<const void*>(k), dim3(unsigned(blocks)), dim3(unsigned(threads)), args, lds, st,
                              begun ? nullptr : ev.start, left ? nullptr : ev.stop, 0);
     begun = true;
   }

@@ -295,6 +295,50 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
   }
 }
 
+// More ids a row than kFewIds are sorted by the tile of logits that they lie in, so that a tile finds its own: one
+// workgroup for the rows of a tile counts them, adds the counts up and deals the entries out. (Where an entry lies
+// among its tile's does not show in any result.)
+constexpr int kFewIds = 4, kSortThreads = 1024;
+__global__ __launch_bounds__(kSortThreads) void k_vocab_sort(const int32_t* idt, int ld_idt, int bn, int bm, int mtiles, int64_t row_tiles, const Counts* counts, int32_t* starts, uint32_t* entries) {
+  extern __shared__ int32_t place[];  // [mtiles + 1]
+  __shared__ int32_t wave_sum[kSortThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  for (int64_t t = blockIdx.x; t < row_tiles && t * bn < counts->active; t += gridDim.x) {
+    for (int i = tid; i <= mtiles; i += kSortThreads) place[i] = 0;
+    __syncthreads();
+    const int32_t* ids = idt + t * bn * ld_idt;
+    const int all = bn * ld_idt;
+    for (int i = tid; i < all; i += kSortThreads)
+      if (ids[i] >= 0) atomicAdd(&place[ids[i] / bm], 1);
+    __syncthreads();
+    const int per = (mtiles + 1 + kSortThreads - 1) / kSortThreads, i0 = min(tid * per, mtiles + 1), i1 = min(i0 + per, mtiles + 1);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += place[i];
+    int before = mine;  // this thread's and the earlier ones' of the wave
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(before, d);
+      before += lane >= d ? o : 0;
+    }
+    if (lane == 63) wave_sum[tid / 64] = before;
+    __syncthreads();
+    int at = before - mine;
+    for (int w = 0; w < tid / 64; ++w) at += wave_sum[w];
+    for (int i = i0; i < i1; ++i) {
+      const int n = place[i];
+      place[i] = at;
+      starts[t * (mtiles + 1) + i] = at;
+      at += n;
+    }
+    __syncthreads();
+    for (int i = tid; i < all; i += kSortThreads) {
+      const int32_t id = ids[i];
+      if (id >= 0) entries[t * all + atomicAdd(&place[id / bm], 1)] = uint32_t(id % bm) | uint32_t(i / ld_idt) << 8 | uint32_t(i % ld_idt) << 16;
+    }
+    __syncthreads();
+  }
+}
+
 // Output matrix pieces as bf16 terms (fp32 pieces, and bf16 ones that 16-byte loads do not fit), row v of the
 // padded vocabulary at out + v * PL * Hp; `pieces` is then pointed there.
 template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack_pieces(const Piece* pieces, Piece* packed, int P, int64_t Vp, int H, int Hp, char* out) {
@@ -355,6 +399,9 @@ struct Product {
   const int32_t* idt;  // [rows][ld_idt], as zt
   int32_t ld_idt;
   float* zt;  // the logits at those ids, times log2(e)
+  const int32_t* starts;    // more than kFewIds: where each tile's entries begin, [row tiles][mtiles + 1]
+  const uint32_t* entries;  // [row tiles][BN ids], m | n << 8 | k << 16 within the tile
+  int32_t entries_ld;
   // gradients
   const int32_t* rows;
   void* dh;
@@ -697,13 +744,22 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   while (true) {
     const int wn0 = at.n0 + wn * C::NW, wm0 = at.m0 + wm * C::MW;
     typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-    i32x4 ids = {-1, -1, -1, -1};  // of row wn0 + lane: the first four
-    const i32x4* id_row = nullptr;
-    if constexpr (DIR == S_LOGITS)
-      if (lane < C::NW && wn0 + lane < active) {
-        id_row = reinterpret_cast<const i32x4*>(a.idt + int64_t(a.chunk + wn0 + lane) * a.ld_idt);
-        ids = id_row[0];
+    // What the tile's pick will ask for: row wn0 + lane's ids where they are few, or the first of the tile's entries.
+    i32x4 ids = {-1, -1, -1, -1};
+    const uint32_t* entries = nullptr;
+    int first = 0, last_entry = 0;
+    if constexpr (DIR == S_LOGITS) {
+      if (a.ld_idt <= kFewIds) {
+        if (lane < C::NW && wn0 + lane < active) ids = *reinterpret_cast<const i32x4*>(a.idt + int64_t(a.chunk + wn0 + lane) * kFewIds);
+      } else {
+        const int tile = (a.chunk + at.n0) / C::BN;
+        const int32_t* at_m = a.starts + int64_t(tile) * (mtiles + 1) + at.m0 / C::BM;
+        first = __builtin_amdgcn_readfirstlane(at_m[0]);
+        last_entry = __builtin_amdgcn_readfirstlane(at_m[1]);
+        entries = a.entries + int64_t(tile) * a.entries_ld;
+        if (first + lane < last_entry) ids[0] = int32_t(entries[first + lane]);
       }
+    }
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
@@ -752,32 +808,36 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][j][e] = i * 16 + e < left ? acc[i][j][e] : -INFINITY;
       }
-      // the logits of the rows' own ids: a lane compares its row's, the wave takes the hits one by one
-      for (int k = 0; k < a.ld_idt; k += k ? 16 : 4) {
-        i32x4 batch[4] = {ids, {-1, -1, -1, -1}, {-1, -1, -1, -1}, {-1, -1, -1, -1}};
-        if (k) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) batch[q] = id_row && k + 4 * q < a.ld_idt ? id_row[k / 4 + q] : i32x4{-1, -1, -1, -1};
-        }
-        uint32_t mine = 0;  // which of the sixteen are in the wave's part of the tile
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mine |= uint32_t(batch[e / 4][e % 4] - wm0) < uint32_t(C::MW) ? 1u << e : 0u;
-        for (uint64_t hit = __ballot(mine != 0); hit; hit = __ballot(mine != 0)) {
+      // the logits of the rows' own ids: every lane has one that may lie in the wave's part of the tile, and the wave
+      // takes those that do one by one
+      const auto pick = [&](uint32_t m, uint32_t n, uint32_t k) {
+        const uint32_t r = m - wm * C::MW, c = n - wn * C::NW;
+        for (uint64_t hit = __ballot(r < uint32_t(C::MW) && c < uint32_t(C::NW)); hit; hit &= hit - 1) {
           const int src = __builtin_ctzll(hit);
-          const int which = __builtin_ctz(__builtin_amdgcn_readlane(int(mine), src));
-          int32_t id = 0;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) id = which == e ? batch[e / 4][e % 4] : id;
-          const int r = __builtin_amdgcn_readlane(id, src) - wm0;
+          const int row = __builtin_amdgcn_readlane(int(r), src), col = __builtin_amdgcn_readlane(int(c), src), which = __builtin_amdgcn_readlane(int(k), src);
           f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-          for (int i = 0; i < C::FM; ++i)
+          for (int j = 0; j < C::FN; ++j)
+            if (col / 16 == j) {
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-              if (r / 16 == i && src / 16 == j) x = acc[i][j];
-          const float v = r % 4 == 0 ? x[0] : r % 4 == 1 ? x[1] : r % 4 == 2 ? x[2] : x[3];
-          if (lane == r % 16 / 4 * 16 + src % 16) a.zt[int64_t(wn0 + src) * a.ld_idt + k + which] = v * a.scale;
-          if (lane == src) mine &= mine - 1;
+              for (int i = 0; i < C::FM; ++i)
+                if (row / 16 == i) x = acc[i][j];
+            }
+          const float v = row % 4 == 0 ? x[0] : row % 4 == 1 ? x[1] : row % 4 == 2 ? x[2] : x[3];
+          if (lane == row % 16 / 4 * 16 + col % 16) a.zt[int64_t(wn0 + col) * a.ld_idt + which] = v * a.scale;
+        }
+      };
+      if (a.ld_idt <= kFewIds) {
+#pragma unroll 1
+        for (int e = 0; e < kFewIds; ++e) {
+          const int32_t id = e == 0 ? ids[0] : e == 1 ? ids[1] : e == 2 ? ids[2] : ids[3];
+          pick(uint32_t(id - at.m0), id >= 0 ? uint32_t(wn * C::NW + lane) : ~0u, uint32_t(e));
+        }
+      } else {
+#pragma unroll 1
+        for (int e = first; e < last_entry; e += 64) {
+          const uint32_t x = e == first ? uint32_t(ids[0]) : e + lane < last_entry ? entries[e + lane] : ~0u;
+          pick(x == ~0u ? ~0u : x & 255, x >> 8 & 255, x >> 16);
         }
       }
     }
@@ -1117,9 +1177,10 @@ struct Plan {
   bool packed;
   Size logits, hidden, weight;
   int hidden_splits = 1, weight_splits = 1;
-  int block;  // columns a statistic covers
+  int block;  // columns a statistic covers: a logits tile's
+  int tile_rows;  // rows of a logits tile
   // offsets in the workspace
-  size_t counts, pieces, packed_pieces, rows, flags, teacher, idt, hp, wp, lse, coef, row_loss, zt, stats, exps, d, part, bytes;
+  size_t counts, pieces, packed_pieces, rows, flags, teacher, idt, hp, wp, lse, coef, row_loss, zt, starts, entries, stats, exps, d, part, bytes;
 };
 
 int64_t tiles_of(Size z, int64_t m, int64_t n) {
@@ -1157,6 +1218,7 @@ Plan plan_of(const Vocab& v, bool grad) {
   const int64_t n = std::min(p.Tc, v.T), passes = p.planes == 1 ? 1 : 6;
   p.logits = size_for(p.Vp, n, 1);
   p.block = p.logits == Z_L ? 256 : 128;
+  p.tile_rows = p.logits == Z_L ? 256 : p.logits == Z_M ? 128 : 64;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += up(bytes); return o; };
   p.counts = take(sizeof(Counts));
@@ -1172,6 +1234,9 @@ Plan plan_of(const Vocab& v, bool grad) {
   p.coef = take(size_t(p.Tc) * 4);
   p.row_loss = take(size_t(p.Tpad) * 4);
   p.zt = take(size_t(p.Tc) * size_t(p.Kp) * 4);
+  const bool sorted = p.Kp > kFewIds;
+  p.starts = take(sorted ? size_t(p.Tpad / p.tile_rows) * size_t(p.Vp / p.block + 1) * 4 : 0);
+  p.entries = take(sorted ? size_t(p.Tpad) * size_t(p.Kp) * 4 : 0);
   p.stats = take(size_t(p.Vp / p.block) * size_t(p.Tc) * 8);
   if (grad) {
     p.exps = take(v.dtype == D_FP32 ? size_t(p.Tc) * size_t(p.Vp) * 4 : 0);
@@ -1202,7 +1267,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   const int64_t P = int64_t(v.pieces.size());
   const bool each = v.reduction == R_NONE;
   const int64_t per_chunk = 3 + (grad ? 3 + (p.hidden_splits > 1) + (p.chunks == 1 && p.weight_splits > 1) : 0);
-  s.left = (P + kPieceTab - 1) / kPieceTab + (v.top ? 1 : 0) + 2 + (p.packed ? 1 : 0) + p.chunks * per_chunk +
+  s.left = (P + kPieceTab - 1) / kPieceTab + (v.top ? 1 : 0) + 2 + (p.packed ? 1 : 0) + (p.Kp > kFewIds ? 1 : 0) + p.chunks * per_chunk +
            (grad && p.chunks > 1 ? 1 : 0) + (each ? 0 : 1);
   Piece* pieces = reinterpret_cast<Piece*>(ws + p.pieces);
   Counts* counts = reinterpret_cast<Counts*>(ws + p.counts);
@@ -1229,6 +1294,11 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   const PackArgs pa{v.hidden, v.ld, v.T, p.Tpad, int32_t(v.H), p.Hp, int32_t(P), pieces, rows, flags, counts, ws + p.hp,
                     reinterpret_cast<int32_t*>(ws + p.idt), p.Kp, grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
   s.launch(k_vocab_pack<DT>, blocks_of(row_blocks), kRowWaves * 64, pa, t);
+  if (p.Kp > kFewIds) {
+    const int64_t row_tiles = p.Tpad / p.tile_rows;
+    s.launch_lds(k_vocab_sort, std::min<int64_t>(row_tiles, launch_blocks()), kSortThreads, size_t(p.Vp / p.block + 1) * 4, pa.idt, p.Kp, p.tile_rows, p.block,
+                 int(p.Vp / p.block), row_tiles, counts, reinterpret_cast<int32_t*>(ws + p.starts), reinterpret_cast<uint32_t*>(ws + p.entries));
+  }
   if (p.packed) {
     Piece* packed = reinterpret_cast<Piece*>(ws + p.packed_pieces);
     s.launch(k_vocab_pack_pieces<DT>, blocks_of(p.Vp / kRowWaves), kRowWaves * 64, pieces, packed, int(P), p.Vp, int(v.H), p.Hp, ws + p.wp);
@@ -1251,6 +1321,9 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.idt = pa.idt;
   a.ld_idt = p.Kp;
   a.zt = reinterpret_cast<float*>(ws + p.zt);
+  a.starts = reinterpret_cast<const int32_t*>(ws + p.starts);
+  a.entries = reinterpret_cast<const uint32_t*>(ws + p.entries);
+  a.entries_ld = p.tile_rows * p.Kp;
   a.rows = rows;
   a.dh = v.dh;
   a.dh_ld = v.dh_ld;
