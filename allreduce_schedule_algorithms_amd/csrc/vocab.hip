@@ -37,6 +37,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 #define AR_LDS __attribute__((address_space(3)))
 
 constexpr int kBK = 32;         // depth of a slice: one product's, 64 bytes of a row
@@ -62,7 +63,7 @@ struct Counts {
   int32_t active;  // rows that take part
   int32_t mean;    // rows that are not left out (those of weight 0 among them)
   int32_t bad;     // rows with an id outside the vocabulary
-  int32_t pad;
+  uint32_t joined; // workgroups that have left their rows' losses
 };
 
 enum Flag : uint8_t { F_OUT = 0, F_ACTIVE = 1, F_BAD = 2, F_ZERO = 3 };
@@ -100,10 +101,6 @@ __device__ __forceinline__ void split3(float x, __bf16 (&t)[3]) {
 // ----------------------------------------------------------------------------
 // rows
 // ----------------------------------------------------------------------------
-__global__ void k_vocab_pieces(PieceTab tab, Piece* out) {
-  for (int i = threadIdx.x; i < tab.count; i += blockDim.x) out[tab.at + i] = tab.p[i];
-}
-
 // What a call's targets are.
 struct Targets {
   const void* ids;
@@ -151,8 +148,8 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int
 
 // Rows that take part, in order, at rows[0..active); the others behind them. One workgroup.
 constexpr int kScanThreads = 1024, kScanEach = 4;
-__global__ __launch_bounds__(kScanThreads) void k_vocab_scan(Targets t, int64_t T, int32_t* rows, uint8_t* flags, Counts* counts) {
-  __shared__ int wave_n[kScanThreads / 64][kScanEach], tally[2];
+__device__ __forceinline__ void scan_rows(const Targets& t, int64_t T, int32_t* rows, uint8_t* flags, Counts* counts) {
+  __shared__ int wave_n[kScanThreads / 64][kScanEach], tally[2], round;
   const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
   if (tid < 2) tally[tid] = 0;
   int done = 0, mean = 0, bad = 0;  // active rows before this round; the thread's own tallies
@@ -178,30 +175,36 @@ __global__ __launch_bounds__(kScanThreads) void k_vocab_scan(Targets t, int64_t 
       if (lane == 0) wave_n[wave][j] = __popcll(mask[j]);
     }
     __syncthreads();
-    int at = done;
+    if (wave == 0) {  // a lane for every wave and round, in the rows' order: what comes before it
+      static_assert(kScanThreads / 64 * kScanEach == 64, "one wave adds all counts up");
+      const int w = lane % (kScanThreads / 64), j = lane / (kScanThreads / 64), n = wave_n[w][j];
+      int upto = n;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(upto, d);
+        upto += lane >= d ? o : 0;
+      }
+      wave_n[w][j] = upto - n;
+      if (lane == 63) round = upto;
+    }
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kScanEach; ++j) {
-      int before = 0, all = 0;
-      for (int w = 0; w < kScanThreads / 64; ++w) {
-        const int n = wave_n[w][j];
-        before += w < wave ? n : 0;
-        all += n;
-      }
       const int64_t r = base + j * kScanThreads + tid;
-      const int mine = at + before + __popcll(mask[j] & ((uint64_t(1) << lane) - 1));  // active rows before r
+      const int mine = done + wave_n[wave][j] + __popcll(mask[j] & ((uint64_t(1) << lane) - 1));  // active rows before r
       if (r < T) {
         if (f[j] == F_ACTIVE) rows[mine] = int32_t(r);
         else rows[T - 1 - (r - mine)] = int32_t(r);  // r - mine others before it: from the end
       }
-      at += all;
     }
-    done = at;
+    done += round;
     __syncthreads();
   }
   if (mean) atomicAdd(&tally[0], mean);  // whole numbers in LDS: the order does not matter
   if (bad) atomicAdd(&tally[1], bad);
   __syncthreads();
-  if (tid == 0) *counts = Counts{done, tally[0], tally[1], 0};
+  if (tid == 0) *counts = Counts{done, tally[0], tally[1], 0u};
+  __syncthreads();
 }
 
 // The hidden rows that take part, gathered as bf16 terms of Hp elements each, zeros behind them; their ids as padded
@@ -259,17 +262,18 @@ template <int DT> __device__ __forceinline__ void pack_row(const void* src, int6
   }
 }
 
-template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack(PackArgs a, Targets t) {
+template <int DT> __device__ __forceinline__ void pack_rows(const PackArgs& a, const Targets& t, const Piece* pieces, int64_t first, int64_t step) {
   constexpr int PL = DT == D_FP32 ? 3 : 1;
   const int lane = threadIdx.x & 63;
-  const int active = a.counts->active, end = (active + kUnit - 1) / kUnit * kUnit;
+  // the products go 2 kBK rows deep at a time, and tiles look up the ids of up to kUnit rows
+  const int active = a.counts->active, zeros = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK, end = (active + kUnit - 1) / kUnit * kUnit;
   const int K = t.K ? t.K : 1;
-  for (int64_t i = int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64; i < a.Tpad; i += int64_t(gridDim.x) * kRowWaves) {
+  for (int64_t i = first; i < a.Tpad; i += step) {
     const int64_t r = i < a.T ? a.rows[i] : -1;
     __bf16* dst = reinterpret_cast<__bf16*>(a.hp) + i * PL * a.Hp;
     if (i < active) {
       pack_row<DT>(a.hidden, r * a.ld, a.H, a.Hp, dst, lane);
-    } else if (i < end) {
+    } else if (i < zeros) {
       for (int c = lane * 8; c < PL * a.Hp; c += 512) *reinterpret_cast<bf16x8*>(dst + c) = bf16x8{};
     }
     if (i < end)
@@ -278,7 +282,7 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
         if (i < active && k < K) {
           const int64_t id = t.K ? id_at(t.ids, t.wide, r * t.ids_ld + k) : id_at(t.ids, t.wide, r);
           if (id >= 0) {
-            const Piece& p = a.pieces[piece_of<false>(a.pieces, a.P, int32_t(id))];
+            const Piece& p = pieces[piece_of<false>(pieces, a.P, int32_t(id))];
             at = p.start + int32_t(id) - p.first;
           }
         }
@@ -293,6 +297,9 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
         }
     }
   }
+}
+template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack(PackArgs a, Targets t) {
+  pack_rows<DT>(a, t, a.pieces, int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64, int64_t(gridDim.x) * kRowWaves);
 }
 
 // More ids a row than kFewIds are sorted by the tile of logits that they lie in, so that a tile finds its own: one
@@ -339,22 +346,44 @@ __global__ __launch_bounds__(kSortThreads) void k_vocab_sort(const int32_t* idt,
   }
 }
 
-// Output matrix pieces as bf16 terms (fp32 pieces, and bf16 ones that 16-byte loads do not fit), row v of the
-// padded vocabulary at out + v * PL * Hp; `pieces` is then pointed there.
-template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack_pieces(const Piece* pieces, Piece* packed, int P, int64_t Vp, int H, int Hp, char* out) {
+// A call's first launch (one for every kPieceTab pieces). Workgroup 0 writes the products' table of pieces and finds
+// the rows that take part (and packs them: few elements, which another launch would cost more than). The others copy
+// the output matrix as bf16 terms where the products cannot read it (fp32, and bf16 that 16-byte loads do not fit):
+// row v of the padded vocabulary at wp + v * PL * Hp.
+struct PrepareArgs {
+  PieceTab tab;
+  Piece* pieces;
+  char* wp;  // null: read in place
+  int32_t scan, pack, H, Hp;
+  int64_t T;
+  int32_t* rows;
+  uint8_t* flags;
+  Counts* counts;
+};
+template <int DT> __global__ __launch_bounds__(kScanThreads) void k_vocab_prepare(PrepareArgs p, Targets t, PackArgs a) {
   constexpr int PL = DT == D_FP32 ? 3 : 1;
-  const int lane = threadIdx.x & 63;
-  if (blockIdx.x == 0)
-    for (int p = threadIdx.x; p < P; p += kRowWaves * 64) {
-      Piece q = pieces[p];
-      q.w = out + int64_t(q.start) * PL * Hp * 2;
-      q.ld = int64_t(PL) * Hp;
-      packed[p] = q;
+  const int wave = threadIdx.x / 64, lane = threadIdx.x & 63;
+  const int64_t row = int64_t(PL) * p.Hp;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < p.tab.count; i += kScanThreads) {
+      Piece q = p.tab.p[i];
+      if (p.wp) {
+        q.w = p.wp + q.start * row * 2;
+        q.ld = row;
+      }
+      p.pieces[p.tab.at + i] = q;
     }
-  for (int64_t v = int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64; v < Vp; v += int64_t(gridDim.x) * kRowWaves) {
-    const Piece& p = pieces[piece_of<true>(pieces, P, int32_t(v))];
-    const int64_t r = v - p.start;
-    if (r < p.rows) pack_row<DT>(p.w, r * p.ld, H, Hp, reinterpret_cast<__bf16*>(out) + v * PL * Hp, lane);
+    if (p.scan) scan_rows(t, p.T, p.rows, p.flags, p.counts);
+    if (p.pack) pack_rows<DT>(a, t, p.tab.p, wave, kScanThreads / 64);
+  }
+  if (!p.wp) return;
+  const int64_t helpers = gridDim.x > 1 ? gridDim.x - 1 : 1, me = gridDim.x > 1 ? int64_t(blockIdx.x) - 1 : 0;
+  if (me < 0) return;
+  const Piece& last = p.tab.p[p.tab.count - 1];
+  for (int64_t v = p.tab.p[0].start + me * (kScanThreads / 64) + wave; v < int64_t(last.start) + last.rows; v += helpers * (kScanThreads / 64)) {
+    const Piece& q = p.tab.p[piece_of<true>(p.tab.p, p.tab.count, int32_t(v))];
+    const int64_t r = v - q.start;
+    if (r < q.rows) pack_row<DT>(q.w, r * q.ld, p.H, p.Hp, reinterpret_cast<__bf16*>(p.wp) + v * row, lane);
   }
 }
 
@@ -698,8 +727,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64), wm = wave % C::WM, wn = wave / C::WM;
   const int active = chunk_active(a);
   const int nlen = DIR == S_WEIGHT ? a.Vp : active;
-  const int ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles;
-  const int64_t tiles = int64_t(ntiles) * mtiles;
+  const uint32_t ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles, tiles = ntiles * mtiles, places = tiles * a.splits;
   const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK;
   const int steps = depth / kBK, all = steps * (a.planes == 1 ? 1 : 6);
   St st{a, 0, 0, tid, steps};
@@ -709,20 +737,20 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   o.wn = wn;
   o.lane = lane;
 
-  const auto place = [&](int64_t t) {
+  const auto place = [&](uint32_t t) {
     Place p;
     p.split = int(t / tiles);
     // Workgroups go to the eight dies in turn: each die gets a run of tiles, and of a run eight tiles of n share
     // their m with the neighbours, so that both operands are found in the die's cache.
-    int64_t u = t - p.split * tiles;
-    const int64_t per = tiles / 8, more = tiles % 8, die = u % 8, i = u / 8;
+    uint32_t u = t - p.split * tiles;
+    const uint32_t per = tiles / 8, more = tiles % 8, die = u % 8, i = u / 8;
     u = die * per + min(die, more) + i;
-    const int64_t group = u / (8 * int64_t(mtiles));
-    const int in_group = int(u - group * 8 * mtiles), width = min(8, ntiles - int(group) * 8);
+    const uint32_t group = u / (8 * mtiles), in_group = u - group * 8 * mtiles, width = min(8u, ntiles - group * 8);
     p.m0 = in_group / width * C::BM;
-    p.n0 = (int(group) * 8 + in_group % width) * C::BN;
-    p.s0 = int(int64_t(all / 2) * p.split / a.splits) * 2;
-    p.s1 = int(int64_t(all / 2) * (p.split + 1) / a.splits) * 2;
+    p.n0 = (group * 8 + in_group % width) * C::BN;
+    const int pairs = all / 2, share = pairs / a.splits, over = pairs % a.splits;
+    p.s0 = (p.split * share + min(p.split, over)) * 2;
+    p.s1 = p.s0 + (share + (p.split < over)) * 2;
     return p;
   };
   // The first kStages - 1 slices of a tile, on their way into LDS.
@@ -737,8 +765,8 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     }
   };
 
-  int64_t t = blockIdx.x;
-  if (t >= tiles * a.splits) return;
+  uint32_t t = blockIdx.x;
+  if (t >= places) return;
   Place at = place(t);
   start(at);
   while (true) {
@@ -845,7 +873,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     // next tile's first barrier.
     const Place done = at;
     t += gridDim.x;
-    const bool more = t < tiles * a.splits;
+    const bool more = t < places;
     if (more) {
       at = place(t);
       start(at);
@@ -946,7 +974,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 // softmax statistics, D, losses
 // ----------------------------------------------------------------------------
 struct Soft {
-  const Counts* counts;
+  Counts* counts;
   const int32_t* rows;
   const float* weights;
   const float2* stats;
@@ -961,57 +989,166 @@ struct Soft {
   char* d;
 };
 
-// 16 rows a workgroup: a wave's lanes are 16 rows x 4 statistics, and its 16 waves share the statistics.
+// What the rows' own ids are for.
+struct Ends {
+  const float2* teacher;  // by original row
+  const int32_t* idt;
+  int32_t ld_idt;
+  const float* zt;
+  float* row_loss;  // [rows that take part], weighted
+  float* each;      // by original row, or null
+  float* total;     // or null
+  uint32_t joins;   // workgroups of all joins together
+};
+
+// The teacher's probability of a row's entry (1 for the one target), and x = its logit less the row's largest.
+struct Teacher {
+  const Targets& t;
+  int64_t row;
+  float2 stat;
+  __device__ __forceinline__ float q(int k, float* x) const {
+    *x = 0;
+    if (!t.K) return 1.f;
+    *x = logit_at(t.logits, t.logits_dtype, row * t.logits_ld + k) / t.temperature - stat.x;
+    return expf(*x) / stat.y;
+  }
+};
+__device__ __forceinline__ Teacher teacher_of(const Targets& t, const Ends& e, int64_t row) { return Teacher{t, row, t.K ? e.teacher[row] : float2{0, 1}}; }
+
+// The rows' softmax statistics, weights and losses, 16 rows a workgroup: first a wave's lanes are 16 rows x 4
+// statistics, and its 16 waves share the statistics; then each wave takes a row's ids. The workgroup that comes last
+// adds the call's loss up, in 64 bits and in the rows' order, whichever it is.
 constexpr int kJoinThreads = 1024, kJoinRows = 16;
-__global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a) {
-  __shared__ float2 part[kJoinThreads / 16][kJoinRows];
-  const int row = threadIdx.x % 16, slice = threadIdx.x / 16;
+__global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Targets t) {
+  __shared__ float2 part[kJoinThreads / 64][kJoinRows];
+  __shared__ float row_lse[kJoinRows];
+  __shared__ double wave_sum[kJoinThreads / 64];
+  __shared__ bool is_last;
+  const int row = threadIdx.x % 16, slice = threadIdx.x / 16, wave = threadIdx.x / 64, lane = threadIdx.x & 63;
   const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + kUnit - 1) / kUnit * kUnit;
   for (int r0 = blockIdx.x * kJoinRows; r0 < end; r0 += gridDim.x * kJoinRows) {
     const int r = r0 + row;
     float m = -INFINITY, s = 0;
+    const auto join = [](float& m, float& s, float om, float os) {
+      if (os == 0) return;
+      const float top = fmaxf(m, om);  // a NaN sum stays one
+      s = (m == top ? s : s * exp2f(m - top)) + (om == top ? os : os * exp2f(om - top));
+      m = top;
+    };
+    const auto join_lanes = [&](float& m, float& s) {
+#pragma unroll
+      for (int d = 16; d < 64; d <<= 1) {
+        const float om = __shfl_xor(m, d), os = __shfl_xor(s, d);
+        // in the lanes' order, so that both partners get the same
+        float lm = lane & d ? om : m, ls = lane & d ? os : s;
+        join(lm, ls, lane & d ? m : om, lane & d ? s : os);
+        m = lm;
+        s = ls;
+      }
+    };
     if (r < active)
       for (int b = slice; b < a.blocks; b += kJoinThreads / 16) {
         const float2 x = a.stats[int64_t(b) * a.ld_stats + r];
-        if (x.y == 0) continue;
-        const float top = fmaxf(m, x.x);  // a NaN sum stays one
-        s = (m == top ? s : s * exp2f(m - top)) + (x.x == top ? x.y : x.y * exp2f(x.x - top));
-        m = top;
+        join(m, s, x.x, x.y);
       }
-    part[slice][row] = float2{m, s};
+    join_lanes(m, s);
+    if (lane < 16) part[wave][row] = float2{m, s};
     __syncthreads();
-    if (threadIdx.x < kJoinRows) {
+    if (wave == 0) {
+      m = -INFINITY, s = 0;
+      for (int w = lane / 16; w < kJoinThreads / 64; w += 4) join(m, s, part[w][row].x, part[w][row].y);
+      join_lanes(m, s);
       float lse = 0, coef = 0;
       if (r < active) {
-        float top = -INFINITY;
-        for (int w = 0; w < kJoinThreads / 16; ++w) top = fmaxf(top, part[w][row].x);
-        float all = 0;
-        for (int w = 0; w < kJoinThreads / 16; ++w) {
-          const float2 x = part[w][row];
-          if (x.y != 0) all += x.y * exp2f(x.x - top);
-        }
-        lse = top + log2f(all);
+        lse = m + log2f(s);
         coef = 1.f / a.temperature;
         if (a.weights) coef *= a.weights[a.rows[a.chunk + r]];
         if (a.reduction == R_MEAN) coef /= float(a.counts->mean);
       }
-      a.lse[r] = lse;
-      a.coef[r] = coef;
+      if (lane < 16) {
+        a.lse[r] = row_lse[row] = lse;
+        a.coef[r] = coef;
+      }
     }
     __syncthreads();
+    const int i = r0 + wave;
+    if (i < active) {
+      const int64_t from = a.rows[a.chunk + i];
+      const Teacher teacher = teacher_of(t, e, from);
+      float loss = 0;
+      for (int k = lane; k < e.ld_idt; k += 64) {
+        if (e.idt[(a.chunk + i) * int64_t(e.ld_idt) + k] < 0) continue;
+        float x;
+        const float q = teacher.q(k, &x);
+        if (q != 0) loss += q * ((t.K ? x - logf(teacher.stat.y) : 0.f) + (row_lse[wave] - e.zt[int64_t(i) * e.ld_idt + k]) * kLn2);
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
+      if (lane == 0) {
+        if (a.weights) loss *= a.weights[from];
+        if (e.each) e.each[from] = loss;
+        else __hip_atomic_store(&e.row_loss[a.chunk + i], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    __syncthreads();
+  }
+  if (!e.total) return;
+  // Every wave's losses have reached memory (they are written past the caches, and waited for) before the workgroup
+  // counts itself. A fence would write all of the cache back: 40 us behind a product that has just filled it.
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(waits(0));
+  __syncthreads();
+  if (threadIdx.x == 0) is_last = __hip_atomic_fetch_add(&a.counts->joined, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == e.joins;
+  __syncthreads();
+  if (!is_last) return;
+  double sum = 0;
+  for (int i = threadIdx.x; i < a.counts->active; i += kJoinThreads) sum += double(__hip_atomic_load(&e.row_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+#pragma unroll
+  for (int d = 32; d; d >>= 1) sum += __shfl_down(sum, d);
+  if (lane == 0) wave_sum[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0;
+    for (int w = 0; w < kJoinThreads / 64; ++w) sum += wave_sum[w];
+    if (a.reduction == R_MEAN && a.counts->mean) sum /= a.counts->mean;
+    *e.total = a.counts->bad ? NAN : float(sum);
+  }
+}
+
+// D at an id of a row: c (p - q), q summed over the row's equal ids.
+template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const Ends& e, const Targets& t, int i, int k, int32_t id) {
+  const Teacher teacher = teacher_of(t, e, a.rows[a.chunk + i]);
+  const int32_t* ids = e.idt + (a.chunk + i) * int64_t(e.ld_idt);
+  float q = 0;
+  for (int l = 0; l < e.ld_idt; ++l) {
+    float x;
+    if (ids[l] == id) q += teacher.q(l, &x);
+  }
+  const float d = a.coef[i] * (exp2f(e.zt[int64_t(i) * e.ld_idt + k] - a.lse[i]) - q);
+  __bf16* row = reinterpret_cast<__bf16*>(a.d) + int64_t(i) * (DT == D_BF16 ? 1 : 3) * a.Vp;
+  if constexpr (DT == D_BF16) {
+    row[id] = __bf16(d);
+  } else {
+    __bf16 b[3];
+    split3(d, b);
+#pragma unroll
+    for (int j = 0; j < 3; ++j) row[j * a.Vp + id] = b[j];
   }
 }
 
 // exp(z - m) -> c p, 64 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
-constexpr int kNormThreads = 256, kNormRows = 64, kNormCols = 512;
-template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a) {
+constexpr int kNormThreads = 256, kNormRows = 64, kNormCols = 512, kBatch = 4;
+template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
   constexpr int kBlocks = kNormCols / 128;
   __shared__ float factor[kNormRows][kBlocks];
   const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + kNormRows - 1) / kNormRows;
   const int64_t cols = (a.Vp + kNormCols - 1) / kNormCols, tiles = cols * end;
-  for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int r0 = int(t / cols) * kNormRows;
-    const int64_t c0 = (t % cols) * kNormCols;
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int r0 = int(tile / cols) * kNormRows;
+    const int64_t c0 = (tile % cols) * kNormCols;
+    static_assert(kNormThreads == kNormRows * kFewIds, "a thread for each of a tile's few ids");
+    const int own_row = r0 + threadIdx.x / kFewIds, own_k = threadIdx.x % kFewIds;
+    const int32_t own = e.ld_idt == kFewIds && own_row < active ? e.idt[int64_t(a.chunk + own_row) * kFewIds + own_k] : -1;
     {
       const int r = threadIdx.x % kNormRows, b = threadIdx.x / kNormRows;
       const int64_t c = c0 + b * 128;
@@ -1024,115 +1161,54 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
     constexpr int kLanes = kNormCols / 8;
     const int c8 = threadIdx.x % kLanes * 8;
     if (c0 + c8 < a.Vp)
-      for (int r = threadIdx.x / kLanes; r < kNormRows; r += kNormThreads / kLanes) {
-        const float f = factor[r][c8 / 128];
-        const bool there = r0 + r < active;
-        if constexpr (DT == D_BF16) {
-          bf16x8* p = reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8);
-          bf16x8 v = {};
-          if (there) {
-            v = *p;
+      for (int r4 = threadIdx.x / kLanes; r4 < kNormRows; r4 += kBatch * kNormThreads / kLanes) {
+        using In = std::conditional_t<DT == D_BF16, bf16x8, f32x8>;
+        In v[kBatch];  // loaded together
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __bf16(float(v[j]) * f);
+        for (int q = 0; q < kBatch; ++q) {
+          const int r = r4 + q * kNormThreads / kLanes;
+          v[q] = In{};
+          if (r0 + r >= active) continue;
+          if constexpr (DT == D_BF16) v[q] = *reinterpret_cast<const In*>(reinterpret_cast<const __bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8);
+          else v[q] = *reinterpret_cast<const In*>(a.exps + int64_t(r0 + r) * a.Vp + c0 + c8);
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+          const int r = r4 + q * kNormThreads / kLanes;
+          const float f = factor[r][c8 / 128];
+          if constexpr (DT == D_BF16) {
+            bf16x8 o;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __bf16(float(v[q][j]) * f);
+            *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8) = o;
+          } else {
+            bf16x8 o[3];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              __bf16 b[3];
+              split3(v[q][j] * f, b);
+              o[0][j] = b[0];
+              o[1][j] = b[1];
+              o[2][j] = b[2];
+            }
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + (int64_t(r0 + r) * 3 + i) * a.Vp + c0 + c8) = o[i];
           }
-          *p = v;
-        } else {
-          const float* s = a.exps + int64_t(r0 + r) * a.Vp + c0 + c8;
-          bf16x8 o[3];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            __bf16 b[3];
-            split3(there ? s[j] * f : 0.f, b);
-            o[0][j] = b[0];
-            o[1][j] = b[1];
-            o[2][j] = b[2];
-          }
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + (int64_t(r0 + r) * 3 + i) * a.Vp + c0 + c8) = o[i];
         }
       }
     __syncthreads();
+    if (own >= c0 && own < c0 + kNormCols) put_own<DT>(a, e, t, own_row, own_k, own);
   }
 }
 
-// A wave per row: the row's loss, and D at the row's own ids: c (p - q), q summed over equal ids.
-struct Ends {
-  const float2* teacher;  // by original row
-  const int32_t* idt;
-  int32_t ld_idt;
-  const float* zt;
-  float* row_loss;  // [rows that take part], weighted
-  float* each;      // by original row, or null
-  bool grad;
-};
-template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_targets(Soft a, Ends e, Targets t) {
-  const int lane = threadIdx.x & 63, active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows);
-  const int K = t.K ? t.K : 1;
-  for (int i = blockIdx.x * kRowWaves + threadIdx.x / 64; i < active; i += gridDim.x * kRowWaves) {
-    const int64_t r = a.rows[a.chunk + i];
-    const float lse = a.lse[i], coef = a.coef[i];
-    const int32_t* ids = e.idt + (a.chunk + i) * int64_t(e.ld_idt);
-    float2 stat = {0, 1};
-    if (t.K) stat = e.teacher[r];
-    auto q_of = [&](int k, float* x) {
-      if (!t.K) return 1.f;
-      *x = logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) / t.temperature - stat.x;
-      return expf(*x) / stat.y;
-    };
-    float loss = 0;
-    for (int k = lane; k < K; k += 64) {
-      const int32_t id = ids[k];
-      if (id < 0) continue;
-      const float z = e.zt[int64_t(i) * e.ld_idt + k];
-      float x = 0;
-      const float q = q_of(k, &x);
-      if (q != 0) loss += q * ((t.K ? x - logf(stat.y) : 0.f) + (lse - z) * kLn2);
-      if (e.grad) {
-        float all = q;
-        if (t.K) {
-          all = 0;
-          for (int l = 0; l < K; ++l) {
-            float y;
-            if (ids[l] == id) all += q_of(l, &y);
-          }
-        }
-        const float d = coef * (exp2f(z - lse) - all);
-        __bf16* row = reinterpret_cast<__bf16*>(a.d) + (DT == D_BF16 ? int64_t(i) * a.Vp : int64_t(i) * 3 * a.Vp);
-        if constexpr (DT == D_BF16) {
-          row[id] = __bf16(d);
-        } else {
-          __bf16 b[3];
-          split3(d, b);
-#pragma unroll
-          for (int j = 0; j < 3; ++j) row[j * a.Vp + id] = b[j];
-        }
-      }
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
-    if (lane == 0) {
-      if (a.weights) loss *= a.weights[r];
-      if (e.each) e.each[r] = loss;
-      else e.row_loss[a.chunk + i] = loss;
-    }
-  }
-}
-
-// The call's loss: the rows' in 64 bits, in an order that their number fixes.
-__global__ __launch_bounds__(1024) void k_vocab_loss(const float* row_loss, const Counts* counts, int reduction, float* out) {
-  __shared__ double wave[16];
-  double s = 0;
-  for (int i = threadIdx.x; i < counts->active; i += 1024) s += double(row_loss[i]);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) s += __shfl_down(s, d);
-  if (threadIdx.x % 64 == 0) wave[threadIdx.x / 64] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    s = 0;
-    for (int w = 0; w < 16; ++w) s += wave[w];
-    if (reduction == R_MEAN && counts->mean) s /= counts->mean;
-    *out = counts->bad ? NAN : float(s);
+// More ids a row than kFewIds: a thread for each.
+template <int DT> __global__ __launch_bounds__(256) void k_vocab_own(Soft a, Ends e, Targets t) {
+  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows);
+  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < int64_t(active) * e.ld_idt; n += int64_t(gridDim.x) * 256) {
+    const int i = int(n / e.ld_idt), k = int(n % e.ld_idt);
+    const int32_t id = e.idt[int64_t(a.chunk) * e.ld_idt + n];
+    if (id >= 0) put_own<DT>(a, e, t, i, k, id);
   }
 }
 
@@ -1170,6 +1246,8 @@ enum Size { Z_S = 0, Z_M = 1, Z_L = 2 };
 // Scratch of D and the exponentials that one chunk of tokens may take.
 constexpr int64_t kChunkBytes = int64_t(4) << 30;
 constexpr int kUnits = 256;  // compute units
+// Hidden elements that the first launch's one workgroup packs itself rather than leaving them to another launch.
+constexpr int64_t kFewElements = 32768;
 
 struct Plan {
   int planes, Hp, Kp;  // Kp: ids of a row, whole vectors of them
@@ -1180,7 +1258,7 @@ struct Plan {
   int block;  // columns a statistic covers: a logits tile's
   int tile_rows;  // rows of a logits tile
   // offsets in the workspace
-  size_t counts, pieces, packed_pieces, rows, flags, teacher, idt, hp, wp, lse, coef, row_loss, zt, starts, entries, stats, exps, d, part, bytes;
+  size_t counts, pieces, rows, flags, teacher, idt, hp, wp, lse, coef, row_loss, zt, starts, entries, stats, exps, d, part, bytes;
 };
 
 int64_t tiles_of(Size z, int64_t m, int64_t n) {
@@ -1223,7 +1301,6 @@ Plan plan_of(const Vocab& v, bool grad) {
   auto take = [&](size_t bytes) { const size_t o = at; at += up(bytes); return o; };
   p.counts = take(sizeof(Counts));
   p.pieces = take(sizeof(Piece) * v.pieces.size());
-  p.packed_pieces = take(p.packed ? sizeof(Piece) * v.pieces.size() : 0);
   p.rows = take(size_t(p.Tpad) * 4);
   p.flags = take(size_t(p.Tpad));
   p.teacher = take(v.top ? size_t(p.Tpad) * 8 : 0);
@@ -1266,43 +1343,48 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   Sequence s{st, {static_cast<hipEvent_t>(v.start_event), static_cast<hipEvent_t>(v.stop_event)}, 0};
   const int64_t P = int64_t(v.pieces.size());
   const bool each = v.reduction == R_NONE;
-  const int64_t per_chunk = 3 + (grad ? 3 + (p.hidden_splits > 1) + (p.chunks == 1 && p.weight_splits > 1) : 0);
-  s.left = (P + kPieceTab - 1) / kPieceTab + (v.top ? 1 : 0) + 2 + (p.packed ? 1 : 0) + (p.Kp > kFewIds ? 1 : 0) + p.chunks * per_chunk +
-           (grad && p.chunks > 1 ? 1 : 0) + (each ? 0 : 1);
+  const int64_t batches = (P + kPieceTab - 1) / kPieceTab, row_blocks = (p.Tpad + kRowWaves - 1) / kRowWaves;
+  const bool sorted = p.Kp > kFewIds, pack_first = batches == 1 && v.T * p.Hp * p.planes <= kFewElements;
+  const int64_t per_chunk = 2 + (grad ? 3 + sorted + (p.hidden_splits > 1) + (p.chunks == 1 && p.weight_splits > 1) : 0);
+  s.left = batches + (v.top ? 1 : 0) + !pack_first + sorted + p.chunks * per_chunk + (grad && p.chunks > 1 ? 1 : 0);
   Piece* pieces = reinterpret_cast<Piece*>(ws + p.pieces);
   Counts* counts = reinterpret_cast<Counts*>(ws + p.counts);
   int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
   uint8_t* flags = reinterpret_cast<uint8_t*>(ws + p.flags);
   float2* teacher = reinterpret_cast<float2*>(ws + p.teacher);
+  const Targets t{v.ids, v.logits, v.token_weights, v.ids_ld, v.logits_ld, v.ignore, p.V, v.top, v.logits_dtype, v.wide_ids, v.temperature};
+  const PackArgs pa{v.hidden, v.ld, v.T, p.Tpad, int32_t(v.H), p.Hp, int32_t(P), pieces, rows, flags, counts, ws + p.hp,
+                    reinterpret_cast<int32_t*>(ws + p.idt), p.Kp, grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
+  if (v.top) s.launch(k_vocab_teacher, blocks_of(row_blocks), kRowWaves * 64, t, v.T, teacher, flags);
   int64_t first = 0, start = 0;
   for (int64_t i0 = 0; i0 < P; i0 += kPieceTab) {
-    PieceTab tab;
-    tab.at = int32_t(i0);
-    tab.count = int32_t(std::min<int64_t>(kPieceTab, P - i0));
-    for (int i = 0; i < tab.count; ++i) {
+    PrepareArgs pr{};
+    pr.tab.at = int32_t(i0);
+    pr.tab.count = int32_t(std::min<int64_t>(kPieceTab, P - i0));
+    const int64_t before = start;
+    for (int i = 0; i < pr.tab.count; ++i) {
       const VocabPiece& q = v.pieces[size_t(i0 + i)];
-      tab.p[i] = Piece{static_cast<const char*>(q.w), static_cast<char*>(q.dw), q.ld, q.dld, int32_t(q.rows), int32_t(start), int32_t(first), 0};
+      pr.tab.p[i] = Piece{static_cast<const char*>(q.w), static_cast<char*>(q.dw), q.ld, q.dld, int32_t(q.rows), int32_t(start), int32_t(first), 0};
       first += q.rows;
       start += int64_t(up(size_t(q.rows), kUnit));
     }
-    s.launch(k_vocab_pieces, 1, 64, tab, pieces);
+    pr.pieces = pieces;
+    pr.wp = p.packed ? ws + p.wp : nullptr;
+    pr.scan = i0 == 0;
+    pr.pack = pack_first;
+    pr.H = int32_t(v.H);
+    pr.Hp = p.Hp;
+    pr.T = v.T;
+    pr.rows = rows;
+    pr.flags = flags;
+    pr.counts = counts;
+    s.launch(k_vocab_prepare<DT>, p.packed ? blocks_of(1 + (start - before + kScanThreads / 64 - 1) / (kScanThreads / 64)) : 1, kScanThreads, pr, t, pa);
   }
-  const Targets t{v.ids, v.logits, v.token_weights, v.ids_ld, v.logits_ld, v.ignore, p.V, v.top, v.logits_dtype, v.wide_ids, v.temperature};
-  const int64_t row_blocks = (p.Tpad + kRowWaves - 1) / kRowWaves;
-  if (v.top) s.launch(k_vocab_teacher, blocks_of(row_blocks), kRowWaves * 64, t, v.T, teacher, flags);
-  s.launch(k_vocab_scan, 1, kScanThreads, t, v.T, rows, flags, counts);
-  const PackArgs pa{v.hidden, v.ld, v.T, p.Tpad, int32_t(v.H), p.Hp, int32_t(P), pieces, rows, flags, counts, ws + p.hp,
-                    reinterpret_cast<int32_t*>(ws + p.idt), p.Kp, grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
-  s.launch(k_vocab_pack<DT>, blocks_of(row_blocks), kRowWaves * 64, pa, t);
-  if (p.Kp > kFewIds) {
+  if (!pack_first) s.launch(k_vocab_pack<DT>, blocks_of(row_blocks), kRowWaves * 64, pa, t);
+  if (sorted) {
     const int64_t row_tiles = p.Tpad / p.tile_rows;
     s.launch_lds(k_vocab_sort, std::min<int64_t>(row_tiles, launch_blocks()), kSortThreads, size_t(p.Vp / p.block + 1) * 4, pa.idt, p.Kp, p.tile_rows, p.block,
                  int(p.Vp / p.block), row_tiles, counts, reinterpret_cast<int32_t*>(ws + p.starts), reinterpret_cast<uint32_t*>(ws + p.entries));
-  }
-  if (p.packed) {
-    Piece* packed = reinterpret_cast<Piece*>(ws + p.packed_pieces);
-    s.launch(k_vocab_pack_pieces<DT>, blocks_of(p.Vp / kRowWaves), kRowWaves * 64, pieces, packed, int(P), p.Vp, int(v.H), p.Hp, ws + p.wp);
-    pieces = packed;
   }
   Product a{};
   a.pieces = pieces;
@@ -1329,13 +1411,16 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.dh_ld = v.dh_ld;
   Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
          v.temperature, reinterpret_cast<float*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
-  const Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, grad};
+  const auto rows_of = [&](int64_t c) { return std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)); };
+  const auto join_blocks = [&](int64_t n) { return blocks_of(int64_t(up(size_t(n), kUnit)) / kJoinRows); };
+  Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, each ? nullptr : v.loss, 0};
+  for (int64_t c = 0; c < p.chunks; ++c) ends.joins += uint32_t(join_blocks(rows_of(c)));
   float* dh_part = reinterpret_cast<float*>(ws + p.part);
   float* dw_part = dh_part;
   if (p.chunks > 1 && p.hidden_splits > 1) dw_part += size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp);
   for (int64_t c = 0; c < p.chunks; ++c) {
     a.chunk = f.chunk = int32_t(c * p.Tc);
-    a.chunk_rows = f.chunk_rows = int32_t(std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)));
+    a.chunk_rows = f.chunk_rows = int32_t(rows_of(c));
     const int64_t n = a.chunk_rows, npad = int64_t(up(size_t(n), kUnit));
     a.mtiles = int32_t(p.Vp / p.block);
     a.splits = 1;
@@ -1343,10 +1428,10 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     const int64_t tiles = tiles_of(p.logits, p.Vp, n);
     if (grad) launch_product<S_LOGITS, DT>(s, p.logits, tiles, a);
     else launch_product<S_LOGITS, 0>(s, p.logits, tiles, a);
-    s.launch(k_vocab_join, blocks_of(npad / kJoinRows), kJoinThreads, f);
-    if (grad) s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f);
-    s.launch(k_vocab_targets<DT>, blocks_of((n + kRowWaves - 1) / kRowWaves), kRowWaves * 64, f, ends, t);
+    s.launch(k_vocab_join, join_blocks(n), kJoinThreads, f, ends, t);
     if (!grad) continue;
+    s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f, ends, t);
+    if (sorted) s.launch(k_vocab_own<DT>, blocks_of((n * p.Kp + 255) / 256), 256, f, ends, t);
     const auto mtiles = [&](Size z) { return int32_t(tiles_of(z, v.H, 1)); };
     a.mtiles = mtiles(p.hidden);
     a.splits = p.hidden_splits;
@@ -1363,7 +1448,6 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     launch_product<S_WEIGHT, DT>(s, p.weight, tiles_of(p.weight, v.H, p.Vp), a);
     if (a.part && c + 1 == p.chunks) s.launch(k_vocab_sum<S_WEIGHT, DT>, blocks_of((p.Vp * p.Hp / 4 + 255) / 256), 256, a);
   }
-  if (!each) s.launch(k_vocab_loss, 1, 1024, ends.row_loss, counts, v.reduction, v.loss);
   return s.done("launching the vocabulary kernels");
 }
 
