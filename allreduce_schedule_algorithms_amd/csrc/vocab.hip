@@ -1136,26 +1136,26 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
   }
 }
 
-// exp(z - m) -> c p, 64 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
-constexpr int kNormThreads = 256, kNormRows = 64, kNormCols = 512, kBatch = 4;
+// exp(z - m) -> c p, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
+constexpr int kNormThreads = 256, kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
   constexpr int kBlocks = kNormCols / 128;
   __shared__ float factor[kNormRows][kBlocks];
-  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + kNormRows - 1) / kNormRows;
+  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK / kNormRows;
   const int64_t cols = (a.Vp + kNormCols - 1) / kNormCols, tiles = cols * end;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int r0 = int(tile / cols) * kNormRows;
     const int64_t c0 = (tile % cols) * kNormCols;
-    static_assert(kNormThreads == kNormRows * kFewIds, "a thread for each of a tile's few ids");
+    static_assert(kNormThreads >= kNormRows * kFewIds, "a thread for each of a tile's few ids");
     const int own_row = r0 + threadIdx.x / kFewIds, own_k = threadIdx.x % kFewIds;
-    const int32_t own = e.ld_idt == kFewIds && own_row < active ? e.idt[int64_t(a.chunk + own_row) * kFewIds + own_k] : -1;
+    const int32_t own = e.ld_idt == kFewIds && threadIdx.x < kNormRows * kFewIds && own_row < active ? e.idt[int64_t(a.chunk + own_row) * kFewIds + own_k] : -1;
     {
       const int r = threadIdx.x % kNormRows, b = threadIdx.x / kNormRows;
       const int64_t c = c0 + b * 128;
       float f = 0;
-      const float w = a.coef[r0 + r];
+      const float w = b < kBlocks ? a.coef[r0 + r] : 0.f;
       if (w != 0 && c < a.Vp) f = exp2f(a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r]) * w;
-      factor[r][b] = f;
+      if (b < kBlocks) factor[r][b] = f;
     }
     __syncthreads();
     constexpr int kLanes = kNormCols / 8;
@@ -1229,7 +1229,16 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
       row = p.dw + int64_t(n - p.start) * p.dld * e;
     }
     f32x4 s = {0, 0, 0, 0};
-    for (int k = 0; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(a.part + k * a.part_stride + int64_t(n) * a.Hp + m);
+    const float* from = a.part + int64_t(n) * a.Hp + m;
+    int k = 0;
+    for (; k + 8 <= a.splits; k += 8) {  // eight on their way together, added in order
+      f32x4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const f32x4*>(from + (k + q) * a.part_stride);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s += v[q];
+    }
+    for (; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(from + k * a.part_stride);
     if constexpr (DT == D_BF16) put(reinterpret_cast<__bf16*>(row) + m, __builtin_convertvector(s, bf16x4), a.H - m);
     else put(reinterpret_cast<float*>(row) + m, s, a.H - m);
   }
