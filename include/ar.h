@@ -420,8 +420,9 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
  *  - Precision: logits, softmax and losses are fp32 (a call's loss is summed in 64 bits). bf16: products of the
  *    bf16 operands are exact and their sums fp32; d is rounded to bf16 twice (2^-8 of it together) before the
  *    gradients' products, whose fp32 sums are rounded to bf16 once. fp32: operands are split into three bf16 terms
- *    and six products of them summed, 2^-24 or so of a product. The order of every sum is fixed by the sizes, the
- *    alignment, the device and ar_set_launch_blocks(), so a call gives the same bits on every run.
+ *    (which hold all their bits down to 2^-133) and six products of them summed, 2^-24 or so of a product. Values
+ *    below 2^-126 on the way may be lost. The order of every sum is fixed by the sizes, the alignment and the number
+ *    of rows that take part, so a call gives the same bits on every run.
  *  - Stream, errors, capture: as for the gradient calls. The tables of pieces travel as kernel arguments.
  *  - Workspace: device scratch of ar_vocab_workspace_bytes() bytes, 16-byte aligned, contents unprepared. It is
  *    bounded in T but for the gathered hidden states (logits are worked on 4 GiB at a time), and the library keeps
