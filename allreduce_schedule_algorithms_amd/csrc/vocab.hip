@@ -716,6 +716,178 @@ struct Place {
   int m0, n0, split, s0, s1;
 };
 
+// A wave's place in its workgroup.
+struct Wave {
+  int m, n, lane;
+};
+
+// What a logits tile's pick asks for: a lane's row's ids where they are few (row n of the wave's part for lane n), or
+// the tile's entries and the first of them for the lane.
+struct Own {
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+  i32x4 ids = {-1, -1, -1, -1};
+  const uint32_t* entries = nullptr;
+  int first = 0, end = 0;
+};
+template <class C> __device__ __forceinline__ Own own_of(const Product& a, const Place& at, int active, Wave wave) {
+  Own own;
+  const int n = at.n0 + wave.n * C::NW + wave.lane;
+  if (a.ld_idt <= kFewIds) {
+    if (wave.lane < C::NW && n < active) own.ids = *reinterpret_cast<const Own::i32x4*>(a.idt + int64_t(a.chunk + n) * kFewIds);
+  } else {
+    const int tile = (a.chunk + at.n0) / C::BN;
+    const int32_t* at_m = a.starts + int64_t(tile) * (a.mtiles + 1) + at.m0 / C::BM;
+    own.first = __builtin_amdgcn_readfirstlane(at_m[0]);
+    own.end = __builtin_amdgcn_readfirstlane(at_m[1]);
+    own.entries = a.entries + int64_t(tile) * a.entries_ld;
+    if (own.first + wave.lane < own.end) own.ids[0] = int32_t(own.entries[own.first + wave.lane]);
+  }
+  return own;
+}
+
+// A logits tile: no logits where the piece has no rows (piece_left: those it has from the tile's first on), and the
+// logits at the rows' own ids put away.
+template <class C> __device__ __forceinline__ void pick_own(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, const Own& own, int piece_left, Wave wave) {
+  const int wm = wave.m, wn = wave.n, lane = wave.lane, wn0 = at.n0 + wn * C::NW;
+  // Everything is in units of log 2 from here on: x = z log2(e) is one product with the sum, and 2^(x - m) one
+  // more operation. (a.scale carries a rounding of 2^-24 of x, the same for all.)
+  if (piece_left < C::BM) {
+    const int left = piece_left - wm * C::MW - lane / 16 * 4;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = i * 16 + e < left ? acc[i][j][e] : -INFINITY;
+  }
+  // the logits of the rows' own ids: every lane has one that may lie in the wave's part of the tile, and the wave
+  // takes those that do one by one
+  const auto pick = [&](uint32_t m, uint32_t n, uint32_t k) {
+    const uint32_t r = m - wm * C::MW, c = n - wn * C::NW;
+    for (uint64_t hit = __ballot(r < uint32_t(C::MW) && c < uint32_t(C::NW)); hit; hit &= hit - 1) {
+      const int src = __builtin_ctzll(hit);
+      const int row = __builtin_amdgcn_readlane(int(r), src), col = __builtin_amdgcn_readlane(int(c), src), which = __builtin_amdgcn_readlane(int(k), src);
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+        if (col / 16 == j) {
+#pragma unroll
+          for (int i = 0; i < C::FM; ++i)
+            if (row / 16 == i) x = acc[i][j];
+        }
+      const float v = row % 4 == 0 ? x[0] : row % 4 == 1 ? x[1] : row % 4 == 2 ? x[2] : x[3];
+      if (lane == row % 16 / 4 * 16 + col % 16) a.zt[int64_t(wn0 + col) * a.ld_idt + which] = v * a.scale;
+    }
+  };
+  if (a.ld_idt <= kFewIds) {
+#pragma unroll 1
+    for (int e = 0; e < kFewIds; ++e) {
+      const int32_t id = e == 0 ? own.ids[0] : e == 1 ? own.ids[1] : e == 2 ? own.ids[2] : own.ids[3];
+      pick(uint32_t(id - at.m0), id >= 0 ? uint32_t(wn * C::NW + lane) : ~0u, uint32_t(e));
+    }
+  } else {
+#pragma unroll 1
+    for (int e = own.first; e < own.end; e += 64) {
+      const uint32_t x = e == own.first ? uint32_t(own.ids[0]) : e + lane < own.end ? own.entries[e + lane] : ~0u;
+      pick(x == ~0u ? ~0u : x & 255, x >> 8 & 255, x >> 16);
+    }
+  }
+}
+
+// A logits tile's exponentials, largest values and sums. scratch: [2][WM][BN] of LDS.
+template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, Wave wave, AR_LDS float* scratch) {
+  const int wm = wave.m, wn = wave.n, lane = wave.lane, wn0 = at.n0 + wn * C::NW, wm0 = at.m0 + wm * C::MW;
+  AR_LDS float* top = scratch;  // [WM][BN]
+  AR_LDS float* sum = top + C::WM * C::BN;  // [WM][BN]
+  float mx[C::FN];
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) m = fmaxf(fmaxf(m, acc[i][j][e]), acc[i][j][e + 1]);
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    if (lane < 16) top[wm * C::BN + wn * C::NW + j * 16 + lane] = m;
+  }
+  lds_barrier();
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < C::WM; ++w) m = fmaxf(m, top[w * C::BN + wn * C::NW + j * 16 + lane % 16]);
+    mx[j] = m == -INFINITY ? 0.f : m * a.scale;  // a tile without rows of the vocabulary: exponentials of 0
+    float s = 0;
+    const int64_t row = int64_t(wn0 + j * 16 + lane % 16) * a.Vp + wm0;
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.scale, -mx[j]));
+        s += acc[i][j][e];
+      }
+      if constexpr (KEEP == D_BF16)
+        if (i & 1) *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + row + (i - 1) * 16 + lane / 16 * 8) = eight_of(acc[i - 1][j], acc[i][j]);
+      if constexpr (KEEP == D_FP32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.part) + row + i * 16 + lane / 16 * 4) = acc[i][j];
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) sum[wm * C::BN + wn * C::NW + j * 16 + lane] = s;
+  }
+  lds_barrier();
+  if (wm == 0 && lane < 16)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) {
+      const int n = wn * C::NW + j * 16 + lane;
+      float s = 0;
+#pragma unroll
+      for (int w = 0; w < C::WM; ++w) s += sum[w * C::BN + n];
+      a.stats[int64_t(at.m0 / C::BM) * a.ld_stats + at.n0 + n] = float2{mx[j], s};
+    }
+}
+
+// A gradient's tile, n < nlen of it.
+template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradient(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, int nlen, Wave wave) {
+  const int lane = wave.lane, wn0 = at.n0 + wave.n * C::NW, wm0 = at.m0 + wave.m * C::MW;
+  constexpr int kBytes = KEEP == D_BF16 ? 2 : 4;
+  // a tile of the vocabulary lies in one piece
+  const Piece* p = nullptr;
+  if constexpr (DIR == S_WEIGHT) p = a.pieces + __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, at.n0));
+#pragma unroll
+  for (int j = 0; j < C::FN; ++j) {
+    const int n = wn0 + j * 16 + lane % 16;
+    char* row = nullptr;
+    bool there = n < nlen;
+    if (!a.part) {
+      if constexpr (DIR == S_HIDDEN) {
+        if (there) row = static_cast<char*>(a.dh) + int64_t(a.rows[a.chunk + n]) * a.dh_ld * kBytes;
+      } else {
+        there = n - p->start < p->rows;
+        row = p->dw + int64_t(n - p->start) * p->dld * kBytes;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      const int m = wm0 + i * 16 + lane / 16 * 4;
+      if (a.part) {
+        if (there && m < a.Hp) {
+          f32x4* q = reinterpret_cast<f32x4*>(a.part + at.split * a.part_stride + int64_t(n) * a.Hp + m);
+          *q = a.accumulate ? *q + acc[i][j] : acc[i][j];
+        }
+      } else if constexpr (KEEP == D_BF16) {
+        if (i & 1) {
+          const int m8 = wm0 + (i - 1) * 16 + lane / 16 * 8;
+          const bf16x8 v = eight_of(acc[i - 1][j], acc[i][j]);
+          if (there && m8 < a.H) put(reinterpret_cast<__bf16*>(row) + m8, v, a.H - m8);
+        }
+      } else {
+        if (there && m < a.H) put(reinterpret_cast<float*>(row) + m, acc[i][j], a.H - m);
+      }
+    }
+  }
+}
+
 // KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
 // the outputs' type.
 template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
@@ -732,6 +904,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   const int steps = depth / kBK, all = steps * (a.planes == 1 ? 1 : 6);
   St st{a, 0, 0, tid, steps};
   st.wave = wave;
+  const Wave w{wm, wn, lane};
   O o;
   o.wm = wm;
   o.wn = wn;
@@ -770,24 +943,8 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   Place at = place(t);
   start(at);
   while (true) {
-    const int wn0 = at.n0 + wn * C::NW, wm0 = at.m0 + wm * C::MW;
-    typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-    // What the tile's pick will ask for: row wn0 + lane's ids where they are few, or the first of the tile's entries.
-    i32x4 ids = {-1, -1, -1, -1};
-    const uint32_t* entries = nullptr;
-    int first = 0, last_entry = 0;
-    if constexpr (DIR == S_LOGITS) {
-      if (a.ld_idt <= kFewIds) {
-        if (lane < C::NW && wn0 + lane < active) ids = *reinterpret_cast<const i32x4*>(a.idt + int64_t(a.chunk + wn0 + lane) * kFewIds);
-      } else {
-        const int tile = (a.chunk + at.n0) / C::BN;
-        const int32_t* at_m = a.starts + int64_t(tile) * (mtiles + 1) + at.m0 / C::BM;
-        first = __builtin_amdgcn_readfirstlane(at_m[0]);
-        last_entry = __builtin_amdgcn_readfirstlane(at_m[1]);
-        entries = a.entries + int64_t(tile) * a.entries_ld;
-        if (first + lane < last_entry) ids[0] = int32_t(entries[first + lane]);
-      }
-    }
+    Own own;
+    if constexpr (DIR == S_LOGITS) own = own_of<C>(a, at, active, w);
     f32x4 acc[C::FM][C::FN];
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
@@ -824,51 +981,8 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     __syncthreads();
 
     const int piece_left = DIR == S_LOGITS ? st.rows - (at.m0 - st.start) : 0;  // rows of the piece from the tile's first on
-    if constexpr (DIR == S_LOGITS) {
-      // Everything is in units of log 2 from here on: x = z log2(e) is one product with the sum, and 2^(x - m) one
-      // more operation. (a.scale carries a rounding of 2^-24 of x, the same for all.)
-      if (piece_left < C::BM) {
-        const int left = piece_left - wm * C::MW - lane / 16 * 4;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = i * 16 + e < left ? acc[i][j][e] : -INFINITY;
-      }
-      // the logits of the rows' own ids: every lane has one that may lie in the wave's part of the tile, and the wave
-      // takes those that do one by one
-      const auto pick = [&](uint32_t m, uint32_t n, uint32_t k) {
-        const uint32_t r = m - wm * C::MW, c = n - wn * C::NW;
-        for (uint64_t hit = __ballot(r < uint32_t(C::MW) && c < uint32_t(C::NW)); hit; hit &= hit - 1) {
-          const int src = __builtin_ctzll(hit);
-          const int row = __builtin_amdgcn_readlane(int(r), src), col = __builtin_amdgcn_readlane(int(c), src), which = __builtin_amdgcn_readlane(int(k), src);
-          f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-          for (int j = 0; j < C::FN; ++j)
-            if (col / 16 == j) {
-#pragma unroll
-              for (int i = 0; i < C::FM; ++i)
-                if (row / 16 == i) x = acc[i][j];
-            }
-          const float v = row % 4 == 0 ? x[0] : row % 4 == 1 ? x[1] : row % 4 == 2 ? x[2] : x[3];
-          if (lane == row % 16 / 4 * 16 + col % 16) a.zt[int64_t(wn0 + col) * a.ld_idt + which] = v * a.scale;
-        }
-      };
-      if (a.ld_idt <= kFewIds) {
-#pragma unroll 1
-        for (int e = 0; e < kFewIds; ++e) {
-          const int32_t id = e == 0 ? ids[0] : e == 1 ? ids[1] : e == 2 ? ids[2] : ids[3];
-          pick(uint32_t(id - at.m0), id >= 0 ? uint32_t(wn * C::NW + lane) : ~0u, uint32_t(e));
-        }
-      } else {
-#pragma unroll 1
-        for (int e = first; e < last_entry; e += 64) {
-          const uint32_t x = e == first ? uint32_t(ids[0]) : e + lane < last_entry ? entries[e + lane] : ~0u;
-          pick(x == ~0u ? ~0u : x & 255, x >> 8 & 255, x >> 16);
-        }
-      }
-    }
+    if constexpr (DIR == S_LOGITS) pick_own<C>(a, acc, at, own, piece_left, w);
+
     // The next tile's first slices travel while this one's results are written; `last` is free of them until the
     // next tile's first barrier.
     const Place done = at;
@@ -879,94 +993,158 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
       start(at);
     }
 
-    if constexpr (DIR == S_LOGITS) {
-      AR_LDS float* top = (AR_LDS float*)last;  // [WM][BN]
-      AR_LDS float* sum = top + C::WM * C::BN;  // [WM][BN]
-      float mx[C::FN];
+    if constexpr (DIR == S_LOGITS) put_logits<C, KEEP>(a, acc, done, w, (AR_LDS float*)last);
+    else put_gradient<C, DIR, KEEP>(a, acc, done, nlen, w);
+    if (!more) return;
+  }
+}
+
+// Few rows against an output matrix that loads into LDS cannot bring as bf16 (fp32, or rows at odd addresses): the
+// products read it as it is, split it into terms on the way to LDS and multiply all terms of a slice at once, where
+// many rows are better served by a copy (which reads, writes and reads again what is read once here). S_LOGITS and
+// S_HIDDEN only: the output matrix is X. kDeep slices are on their way in registers.
+constexpr int kFewRows = 64, kDeep = 3;
+template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThreads, TileS::kWaves) void k_vocab_few(Product a) {
+  using C = TileS;
+  static_assert(C::WN == 1 && C::BM == 128 && C::BN == 64 && C::kThreads == 256, "the loads below");
+  constexpr bool kAlong = DIR == S_LOGITS;
+  constexpr int PL = DT == D_FP32 ? 3 : 1, kPer = DT == D_FP32 ? 4 : 8;  // kPer: elements of a 16-byte load
+  constexpr int kLoads = C::BM * kBK / kPer / C::kThreads, kRow = (kAlong ? kBK : C::BM) / kPer;
+  constexpr int kSlice = PL * C::kStage;
+  using E = std::conditional_t<DT == D_FP32, float, uint16_t>;
+  typedef E V __attribute__((ext_vector_type(kPer)));
+  typedef E Any __attribute__((ext_vector_type(kPer), aligned(sizeof(E))));
+  __shared__ __attribute__((aligned(512))) char shared[2 * kSlice];
+  AR_LDS char* lds = (AR_LDS char*)shared;
+  const int tid = threadIdx.x, lane = tid & 63, wm = __builtin_amdgcn_readfirstlane(tid / 64);
+  const Wave w{wm, 0, lane};
+  const int active = chunk_active(a), steps = (DIR == S_LOGITS ? a.Hp : a.Vp) / kBK;
+  const int ntiles = (active + C::BN - 1) / C::BN, tiles = ntiles * a.mtiles;
+  struct Slice {
+    V x[kLoads];
+    bf16x8 y[PL];
+  };
+  for (int t = blockIdx.x; t < tiles * a.splits; t += gridDim.x) {
+    const int split = t / tiles, u = t - split * tiles, share = steps / a.splits, over = steps % a.splits;
+    const int s0 = split * share + min(split, over);
+    const Place at{u / ntiles * C::BM, u % ntiles * C::BN, split, s0, s0 + share + (split < over)};
+    int rows = 0, start = 0, next = 0;
+    int64_t ld = 0;
+    const E* wp = nullptr;
+    const auto take_at = [&](int32_t row) {
+      const int p = __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, row));
+      wp = reinterpret_cast<const E*>(uniform(reinterpret_cast<int64_t>(a.pieces[p].w)));
+      ld = uniform(a.pieces[p].ld);
+      rows = __builtin_amdgcn_readfirstlane(a.pieces[p].rows);
+      start = __builtin_amdgcn_readfirstlane(a.pieces[p].start);
+      next = p + 1 < a.P ? __builtin_amdgcn_readfirstlane(a.pieces[p + 1].start) : 0x7fffffff;
+    };
+    if constexpr (kAlong) take_at(at.m0);
+    Own own;
+    if constexpr (kAlong) own = own_of<C>(a, at, active, w);
+
+    const auto load = [&](Slice& r, int s) {
+      const int k = s * kBK;
+      if (!kAlong && s < at.s1 && (k < start || k >= next)) take_at(k);
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        float m = -INFINITY;
+      for (int i = 0; i < kLoads; ++i) {
+        const int q = i * C::kThreads + tid, outer = q / kRow, inner = q % kRow * kPer;
+        // the row of the piece and the first column of it
+        const int64_t row = kAlong ? at.m0 - start + outer : k - start + outer;
+        const int col = kAlong ? k + inner : at.m0 + inner;
+        r.x[i] = V{};
+        if (s >= at.s1 || row >= rows || col >= a.H) continue;
+        const E* p = wp + row * ld + col;
+        if (col + kPer <= a.H) {
+          r.x[i] = *reinterpret_cast<const Any*>(p);
+        } else {
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) m = fmaxf(fmaxf(m, acc[i][j][e]), acc[i][j][e + 1]);
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
-        if (lane < 16) top[wm * C::BN + wn * C::NW + j * 16 + lane] = m;
+          for (int j = 0; j < kPer - 1; ++j)
+            if (col + j < a.H) r.x[i][j] = p[j];
+        }
       }
-      lds_barrier();
 #pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < C::WM; ++w) m = fmaxf(m, top[w * C::BN + wn * C::NW + j * 16 + lane % 16]);
-        mx[j] = m == -INFINITY ? 0.f : m * a.scale;  // a tile without rows of the vocabulary: exponentials of 0
-        float s = 0;
-        const int64_t row = int64_t(wn0 + j * 16 + lane % 16) * a.Vp + wm0;
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.scale, -mx[j]));
-            s += acc[i][j][e];
-          }
-          if constexpr (KEEP == D_BF16)
-            if (i & 1) *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + row + (i - 1) * 16 + lane / 16 * 8) = eight_of(acc[i - 1][j], acc[i][j]);
-          if constexpr (KEEP == D_FP32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.part) + row + i * 16 + lane / 16 * 4) = acc[i][j];
-        }
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
-        if (lane < 16) sum[wm * C::BN + wn * C::NW + j * 16 + lane] = s;
+      for (int i = 0; i < PL; ++i) {
+        r.y[i] = bf16x8{};
+        const int64_t n = at.n0 + tid / 4;
+        if (s >= at.s1) continue;
+        const char* p = DIR == S_LOGITS ? a.hp + (((a.chunk + n) * PL + i) * a.Hp + k + tid % 4 * 8) * 2 : a.d + ((n * PL + i) * a.Vp + k + tid % 4 * 8) * 2;
+        r.y[i] = *reinterpret_cast<const bf16x8*>(p);
       }
-      lds_barrier();
-      if (wm == 0 && lane < 16)
+    };
+    const auto store = [&](const Slice& r, AR_LDS char* to) {
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j) {
-          const int n = wn * C::NW + j * 16 + lane;
-          float s = 0;
+      for (int i = 0; i < kLoads; ++i) {
+        const uint32_t q = i * C::kThreads + tid, outer = q / kRow, byte = q % kRow * kPer * 2;  // byte of the row in a term's slice
+        AR_LDS char* p = to + (kAlong ? outer * 64 + ((byte / 16) ^ along_swizzle(outer)) * 16 + byte % 16
+                                      : outer * (C::BM * 2) + ((byte / 32) ^ across_swizzle<C::BM>(outer)) * 32 + byte % 32);
+        if constexpr (DT == D_BF16) {
+          *reinterpret_cast<AR_LDS V*>(p) = r.x[i];
+        } else {
+          bf16x4 o[3];
 #pragma unroll
-          for (int w = 0; w < C::WM; ++w) s += sum[w * C::BN + n];
-          a.stats[int64_t(done.m0 / C::BM) * a.ld_stats + done.n0 + n] = float2{mx[j], s};
-        }
-    } else {
-      constexpr int kBytes = KEEP == D_BF16 ? 2 : 4;
-      // a tile of the vocabulary lies in one piece
-      const Piece* p = nullptr;
-      if constexpr (DIR == S_WEIGHT) p = a.pieces + __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, done.n0));
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) {
-        const int n = wn0 + j * 16 + lane % 16;
-        char* row = nullptr;
-        bool there = n < nlen;
-        if (!a.part) {
-          if constexpr (DIR == S_HIDDEN) {
-            if (there) row = static_cast<char*>(a.dh) + int64_t(a.rows[a.chunk + n]) * a.dh_ld * kBytes;
-          } else {
-            there = n - p->start < p->rows;
-            row = p->dw + int64_t(n - p->start) * p->dld * kBytes;
+          for (int j = 0; j < 4; ++j) {
+            __bf16 b[3];
+            split3(r.x[i][j], b);
+            o[0][j] = b[0];
+            o[1][j] = b[1];
+            o[2][j] = b[2];
           }
-        }
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-          const int m = wm0 + i * 16 + lane / 16 * 4;
-          if (a.part) {
-            if (there && m < a.Hp) {
-              f32x4* q = reinterpret_cast<f32x4*>(a.part + done.split * a.part_stride + int64_t(n) * a.Hp + m);
-              *q = a.accumulate ? *q + acc[i][j] : acc[i][j];
-            }
-          } else if constexpr (KEEP == D_BF16) {
-            if (i & 1) {
-              const int m8 = wm0 + (i - 1) * 16 + lane / 16 * 8;
-              const bf16x8 v = eight_of(acc[i - 1][j], acc[i][j]);
-              if (there && m8 < a.H) put(reinterpret_cast<__bf16*>(row) + m8, v, a.H - m8);
-            }
-          } else {
-            if (there && m < a.H) put(reinterpret_cast<float*>(row) + m, acc[i][j], a.H - m);
+          for (int l = 0; l < 3; ++l) *reinterpret_cast<AR_LDS bf16x4*>(p + l * C::kX) = o[l];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PL; ++i) {
+        const uint32_t row = tid / 4;
+        *reinterpret_cast<AR_LDS bf16x8*>(to + PL * C::kX + i * C::kY + row * 64 + ((tid % 4) ^ along_swizzle(row)) * 16) = r.y[i];
+      }
+    };
+
+    f32x4 acc[C::FM][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    Slice r[kDeep];
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) load(r[i], at.s0 + i);
+    for (int s = at.s0; s < at.s1; s += kDeep) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {  // slices behind the last are zeros
+        AR_LDS char* here = lds + ((s - at.s0 + i) & 1) * kSlice;
+        store(r[i], here);
+        load(r[i], s + i + kDeep);
+        lds_barrier();  // the slice is there, and the one before the last has been multiplied
+        bf16x8 y[PL][C::FN];
+#pragma unroll
+        for (int l = 0; l < PL; ++l)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) y[l][j] = read_along(here + PL * C::kX + l * C::kY, j * 16, lane);
+#pragma unroll
+        for (int f = 0; f < C::FM; ++f) {
+          bf16x8 x[PL];
+#pragma unroll
+          for (int l = 0; l < PL; ++l) {
+            if constexpr (kAlong) x[l] = read_along(here + l * C::kX, wm * C::MW + f * 16, lane);
+            else x[l] = read_across<C::BM>(here + l * C::kX, wm * C::MW + f * 16, lane);
           }
+#pragma unroll
+          for (int pass = 0; pass < (PL == 3 ? 6 : 1); ++pass)
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j)
+              acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
         }
       }
     }
-    if (!more) return;
+    __syncthreads();
+    if constexpr (kAlong) {
+      pick_own<C>(a, acc, at, own, rows - (at.m0 - start), w);
+      put_logits<C, KEEP>(a, acc, at, w, (AR_LDS float*)lds);
+      __syncthreads();
+    } else {
+      put_gradient<C, DIR, KEEP>(a, acc, at, active, w);
+    }
   }
 }
 
@@ -1261,7 +1439,8 @@ constexpr int64_t kFewElements = 32768;
 struct Plan {
   int planes, Hp, Kp;  // Kp: ids of a row, whole vectors of them
   int64_t V = 0, Vp = 0, Tpad, Tc, chunks;
-  bool packed;
+  bool packed;  // the output matrix is copied as bf16 terms
+  bool few;     // or split on its way into few rows' products
   Size logits, hidden, weight;
   int hidden_splits = 1, weight_splits = 1;
   int block;  // columns a statistic covers: a logits tile's
@@ -1276,7 +1455,7 @@ int64_t tiles_of(Size z, int64_t m, int64_t n) {
 }
 
 Size size_for(int64_t m, int64_t n, int64_t splits) {
-  if (n <= 64) return Z_S;
+  if (n <= kFewRows) return Z_S;
   return tiles_of(Z_L, m, n) * splits >= kUnits * 3 / 4 ? Z_L : Z_M;
 }
 
@@ -1297,6 +1476,8 @@ Plan plan_of(const Vocab& v, bool grad) {
     p.Vp += int64_t(up(size_t(q.rows), kUnit));
     if (reinterpret_cast<uintptr_t>(q.w) % 16 || q.ld % 8 || q.ld >= (1 << 21)) p.packed = true;
   }
+  p.few = p.packed && v.T <= kFewRows;
+  if (p.few) p.packed = false;
   p.Tpad = int64_t(up(size_t(std::max<int64_t>(v.T, 1)), kUnit));
   // a chunk's scratch: statistics at their finest, and with gradients the exponentials and D
   const int64_t per = p.Vp / 128 * 8 + (grad ? (v.dtype == D_FP32 ? 10 : 2) * p.Vp : 0);
@@ -1327,8 +1508,9 @@ Plan plan_of(const Vocab& v, bool grad) {
   if (grad) {
     p.exps = take(v.dtype == D_FP32 ? size_t(p.Tc) * size_t(p.Vp) * 4 : 0);
     p.d = take(size_t(p.Tc) * size_t(p.Vp) * size_t(p.planes) * 2);
-    p.hidden = size_for(v.H, n, p.Vp / kBK * passes / 8);
-    p.hidden_splits = splits_for(tiles_of(p.hidden, v.H, n), p.Vp / kBK * passes, n * p.Hp * 4);
+    const int64_t hidden_steps = p.Vp / kBK * (p.few ? 1 : passes);
+    p.hidden = size_for(v.H, n, hidden_steps / 8);
+    p.hidden_splits = splits_for(tiles_of(p.hidden, v.H, n), hidden_steps, n * p.Hp * 4);
     p.weight = size_for(v.H, p.Vp, 1);
     if (p.chunks == 1) p.weight_splits = splits_for(tiles_of(p.weight, v.H, p.Vp), (n + kBK - 1) / kBK * passes, p.Vp * p.Hp * 4);
     const size_t dh = p.hidden_splits > 1 ? size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp) * 4 : 0;
@@ -1339,9 +1521,11 @@ Plan plan_of(const Vocab& v, bool grad) {
   return p;
 }
 
-template <int DIR, int KEEP> void launch_product(Sequence& s, Size z, int64_t tiles, Product a) {
+template <int DT, int DIR, int KEEP> void launch_product(Sequence& s, const Plan& p, Size z, int64_t tiles, Product a) {
   const int64_t most = std::min<int64_t>(launch_blocks(), kUnits * (z == Z_L ? 1 : 2));  // as many as stay resident
   const int64_t blocks = std::max<int64_t>(1, std::min(tiles * a.splits, most));
+  if constexpr (DIR != S_WEIGHT)
+    if (p.few) return s.launch(k_vocab_few<DT, DIR, KEEP>, blocks, TileS::kThreads, a);
   if (z == Z_L) s.launch(k_vocab_product<TileL, DIR, KEEP>, blocks, TileL::kThreads, a);
   else if (z == Z_M) s.launch(k_vocab_product<TileM, DIR, KEEP>, blocks, TileM::kThreads, a);
   else if constexpr (DIR != S_WEIGHT) s.launch(k_vocab_product<TileS, DIR, KEEP>, blocks, TileS::kThreads, a);
@@ -1403,7 +1587,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.Hp = p.Hp;
   a.Vp = int32_t(p.Vp);
   a.planes = p.planes;
-  a.kend = p.packed ? p.Hp : int32_t(v.H);
+  a.kend = p.packed ? p.Hp : int32_t(v.H);  // (few rows' products go by H)
   a.hp = ws + p.hp;
   a.d = ws + p.d;
   a.scale = float(1.4426950408889634 / double(v.temperature));
@@ -1435,8 +1619,8 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     a.splits = 1;
     a.part = f.exps;
     const int64_t tiles = tiles_of(p.logits, p.Vp, n);
-    if (grad) launch_product<S_LOGITS, DT>(s, p.logits, tiles, a);
-    else launch_product<S_LOGITS, 0>(s, p.logits, tiles, a);
+    if (grad) launch_product<DT, S_LOGITS, DT>(s, p, p.logits, tiles, a);
+    else launch_product<DT, S_LOGITS, 0>(s, p, p.logits, tiles, a);
     s.launch(k_vocab_join, join_blocks(n), kJoinThreads, f, ends, t);
     if (!grad) continue;
     s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f, ends, t);
@@ -1447,14 +1631,14 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     a.part = a.splits > 1 ? dh_part : nullptr;
     a.part_stride = p.Tc * p.Hp;
     a.accumulate = 0;
-    launch_product<S_HIDDEN, DT>(s, p.hidden, tiles_of(p.hidden, v.H, n), a);
+    launch_product<DT, S_HIDDEN, DT>(s, p, p.hidden, tiles_of(p.hidden, v.H, n), a);
     if (a.splits > 1) s.launch(k_vocab_sum<S_HIDDEN, DT>, blocks_of((n * p.Hp / 4 + 255) / 256), 256, a);
     a.mtiles = mtiles(p.weight);
     a.splits = p.weight_splits;
     a.part = a.splits > 1 || p.chunks > 1 ? dw_part : nullptr;
     a.part_stride = p.Vp * p.Hp;
     a.accumulate = c > 0;
-    launch_product<S_WEIGHT, DT>(s, p.weight, tiles_of(p.weight, v.H, p.Vp), a);
+    launch_product<DT, S_WEIGHT, DT>(s, p, p.weight, tiles_of(p.weight, v.H, p.Vp), a);
     if (a.part && c + 1 == p.chunks) s.launch(k_vocab_sum<S_WEIGHT, DT>, blocks_of((p.Vp * p.Hp / 4 + 255) / 256), 256, a);
   }
   return s.done("launching the vocabulary kernels");
