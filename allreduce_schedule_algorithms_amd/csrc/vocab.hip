@@ -1013,7 +1013,10 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
   constexpr int kSlice = PL * C::kStage;
   using E = std::conditional_t<DT == D_FP32, float, uint16_t>;
   typedef E V __attribute__((ext_vector_type(kPer)));
-  typedef E Any __attribute__((ext_vector_type(kPer), aligned(sizeof(E))));
+  // (in global memory: a load that may be of LDS would be waited for with it)
+  typedef E Any __attribute__((ext_vector_type(kPer), aligned(sizeof(E)), address_space(1)));
+  typedef E Global __attribute__((address_space(1)));
+  constexpr int kCols = kAlong ? kBK : C::BM;
   __shared__ __attribute__((aligned(512))) char shared[2 * kSlice];
   AR_LDS char* lds = (AR_LDS char*)shared;
   const int tid = threadIdx.x, lane = tid & 63, wm = __builtin_amdgcn_readfirstlane(tid / 64);
@@ -1030,10 +1033,10 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
     const Place at{u / ntiles * C::BM, u % ntiles * C::BN, split, s0, s0 + share + (split < over)};
     int rows = 0, start = 0, next = 0;
     int64_t ld = 0;
-    const E* wp = nullptr;
+    uintptr_t wp = 0;
     const auto take_at = [&](int32_t row) {
       const int p = __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, row));
-      wp = reinterpret_cast<const E*>(uniform(reinterpret_cast<int64_t>(a.pieces[p].w)));
+      wp = uintptr_t(uniform(reinterpret_cast<int64_t>(a.pieces[p].w)));
       ld = uniform(a.pieces[p].ld);
       rows = __builtin_amdgcn_readfirstlane(a.pieces[p].rows);
       start = __builtin_amdgcn_readfirstlane(a.pieces[p].start);
@@ -1043,36 +1046,38 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
     Own own;
     if constexpr (kAlong) own = own_of<C>(a, at, active, w);
 
+    // Every load is of memory that is there, so that none depends on another's branch: behind the piece's rows its last
+    // one is read (logits without a row, and rows that meet zeros of D), behind a row's end its last elements, which
+    // store() moves to their places, and behind the last slice that one again.
     const auto load = [&](Slice& r, int s) {
-      const int k = s * kBK;
-      if (!kAlong && s < at.s1 && (k < start || k >= next)) take_at(k);
+      const int k = min(s, at.s1 - 1) * kBK;
+      if (!kAlong && (k < start || k >= next)) take_at(k);
+      const int row0 = kAlong ? at.m0 - start : k - start, col0 = kAlong ? k : at.m0;
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
-        const int q = i * C::kThreads + tid, outer = q / kRow, inner = q % kRow * kPer;
-        // the row of the piece and the first column of it
-        const int64_t row = kAlong ? at.m0 - start + outer : k - start + outer;
-        const int col = kAlong ? k + inner : at.m0 + inner;
-        r.x[i] = V{};
-        if (s >= at.s1 || row >= rows || col >= a.H) continue;
-        const E* p = wp + row * ld + col;
-        if (col + kPer <= a.H) {
-          r.x[i] = *reinterpret_cast<const Any*>(p);
-        } else {
+        const int q = i * C::kThreads + tid;
+        r.x[i] = *reinterpret_cast<const Any*>(reinterpret_cast<const Global*>(wp) + int64_t(min(row0 + q / kRow, rows - 1)) * ld + min(col0 + q % kRow * kPer, a.H - kPer));
+      }
+      const int64_t n = at.n0 + tid / 4;
+      const char* p = (DIR == S_LOGITS ? a.hp + (a.chunk + n) * PL * a.Hp * 2 : a.d + n * PL * a.Vp * 2) + (k + tid % 4 * 8) * 2;
 #pragma unroll
-          for (int j = 0; j < kPer - 1; ++j)
-            if (col + j < a.H) r.x[i][j] = p[j];
+      for (int i = 0; i < PL; ++i)
+        r.y[i] = *reinterpret_cast<const __attribute__((address_space(1))) bf16x8*>(reinterpret_cast<uintptr_t>(p) + int64_t(i) * (DIR == S_LOGITS ? a.Hp : a.Vp) * 2);
+    };
+    const auto store = [&](Slice& r, int s, AR_LDS char* to) {
+      const int col0 = kAlong ? s * kBK : at.m0;
+      if (col0 + kCols > a.H) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int over = max(col0 + (i * C::kThreads + tid) % kRow * kPer - (a.H - kPer), 0);  // how far the load lies before its place
+          V v = {};
+#pragma unroll
+          for (int d = 0; d < kPer; ++d)
+#pragma unroll
+            for (int j = 0; j + d < kPer; ++j) v[j] = over == d ? r.x[i][j + d] : v[j];
+          r.x[i] = v;
         }
       }
-#pragma unroll
-      for (int i = 0; i < PL; ++i) {
-        r.y[i] = bf16x8{};
-        const int64_t n = at.n0 + tid / 4;
-        if (s >= at.s1) continue;
-        const char* p = DIR == S_LOGITS ? a.hp + (((a.chunk + n) * PL + i) * a.Hp + k + tid % 4 * 8) * 2 : a.d + ((n * PL + i) * a.Vp + k + tid % 4 * 8) * 2;
-        r.y[i] = *reinterpret_cast<const bf16x8*>(p);
-      }
-    };
-    const auto store = [&](const Slice& r, AR_LDS char* to) {
 #pragma unroll
       for (int i = 0; i < kLoads; ++i) {
         const uint32_t q = i * C::kThreads + tid, outer = q / kRow, byte = q % kRow * kPer * 2;  // byte of the row in a term's slice
@@ -1107,13 +1112,16 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
 #pragma unroll
       for (int j = 0; j < C::FN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     Slice r[kDeep];
+    if (at.s0 < at.s1) {
 #pragma unroll
-    for (int i = 0; i < kDeep; ++i) load(r[i], at.s0 + i);
+      for (int i = 0; i < kDeep; ++i) load(r[i], at.s0 + i);
+    }
     for (int s = at.s0; s < at.s1; s += kDeep) {
 #pragma unroll
-      for (int i = 0; i < kDeep; ++i) {  // slices behind the last are zeros
+      for (int i = 0; i < kDeep; ++i) {
+        if (s + i >= at.s1) break;
         AR_LDS char* here = lds + ((s - at.s0 + i) & 1) * kSlice;
-        store(r[i], here);
+        store(r[i], s + i, here);
         load(r[i], s + i + kDeep);
         lds_barrier();  // the slice is there, and the one before the last has been multiplied
         bf16x8 y[PL][C::FN];
@@ -1476,7 +1484,7 @@ Plan plan_of(const Vocab& v, bool grad) {
     p.Vp += int64_t(up(size_t(q.rows), kUnit));
     if (reinterpret_cast<uintptr_t>(q.w) % 16 || q.ld % 8 || q.ld >= (1 << 21)) p.packed = true;
   }
-  p.few = p.packed && v.T <= kFewRows;
+  p.few = p.packed && v.T <= kFewRows && v.H >= 8;  // (a whole vector in every row)
   if (p.few) p.packed = false;
   p.Tpad = int64_t(up(size_t(std::max<int64_t>(v.T, 1)), kUnit));
   // a chunk's scratch: statistics at their finest, and with gradients the exponentials and D
