@@ -98,6 +98,30 @@ __device__ __forceinline__ void split3(float x, __bf16 (&t)[3]) {
   }
 }
 
+// The same of N values, two at a time: the rare magnitudes that round to an infinity, infinities and NaN take the
+// way above.
+template <int N, class V, class B> __device__ __forceinline__ void split3_of(const V& x, B (&t)[3]) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) most = max(most, as_u(x[j]) & 0x7fffffffu);
+  if (most < 0x7f7f8000u) {
+    V r = x;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      t[i] = __builtin_convertvector(r, B);
+      r -= __builtin_convertvector(t[i], V);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      __bf16 b[3];
+      split3(x[j], b);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) t[i][j] = b[i];
+    }
+  }
+}
+
 // ----------------------------------------------------------------------------
 // rows
 // ----------------------------------------------------------------------------
@@ -247,15 +271,16 @@ template <int DT> __device__ __forceinline__ void pack_row(const void* src, int6
       *reinterpret_cast<A*>(dst + c) = v;
     } else {
       const float* s = static_cast<const float*>(src) + at + c;
-      bf16x8 o[3];
+      typedef float V __attribute__((ext_vector_type(8), aligned(4)));
+      f32x8 v;
+      if (c + 8 <= H) {
+        v = *reinterpret_cast<const V*>(s);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        __bf16 b[3];
-        split3(c + j < H ? s[j] : 0.f, b);
-        o[0][j] = b[0];
-        o[1][j] = b[1];
-        o[2][j] = b[2];
+        for (int j = 0; j < 8; ++j) v[j] = c + j < H ? s[j] : 0.f;
       }
+      bf16x8 o[3];
+      split3_of<8>(v, o);
 #pragma unroll
       for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(dst + int64_t(i) * Hp + c) = o[i];
     }
@@ -412,6 +437,8 @@ template <int BM_, int BN_, int WM_, int WN_, int WAVES_, int STAGES_> struct Ti
 using TileL = Tile<256, 256, 2, 4, 2, 5>;
 using TileM = Tile<128, 128, 2, 2, 2, 5>;
 using TileS = Tile<128, 64, 4, 1, 2, 5>;
+// Few rows of an output matrix that is split on the way: fp32 takes three times the LDS, and half the tile.
+template <int DT> using TileF = std::conditional_t<DT == D_FP32, Tile<64, 64, 4, 1, 2, 5>, TileS>;
 
 struct Product {
   const Piece* pieces;
@@ -796,6 +823,7 @@ template <class C> __device__ __forceinline__ void pick_own(const Product& a, f3
 
 // A logits tile's exponentials, largest values and sums. scratch: [2][WM][BN] of LDS.
 template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, Wave wave, AR_LDS float* scratch) {
+  static_assert(KEEP != D_BF16 || C::FM % 2 == 0, "bf16 is written by pairs of products");
   const int wm = wave.m, wn = wave.n, lane = wave.lane, wn0 = at.n0 + wn * C::NW, wm0 = at.m0 + wm * C::MW;
   AR_LDS float* top = scratch;  // [WM][BN]
   AR_LDS float* sum = top + C::WM * C::BN;  // [WM][BN]
@@ -849,6 +877,7 @@ template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Pr
 
 // A gradient's tile, n < nlen of it.
 template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradient(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, int nlen, Wave wave) {
+  static_assert(KEEP != D_BF16 || C::FM % 2 == 0, "bf16 is written by pairs of products");
   const int lane = wave.lane, wn0 = at.n0 + wave.n * C::NW, wm0 = at.m0 + wave.m * C::MW;
   constexpr int kBytes = KEEP == D_BF16 ? 2 : 4;
   // a tile of the vocabulary lies in one piece
@@ -1004,9 +1033,9 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 // many rows are better served by a copy (which reads, writes and reads again what is read once here). S_LOGITS and
 // S_HIDDEN only: the output matrix is X. kDeep slices are on their way in registers.
 constexpr int kFewRows = 64, kDeep = 3;
-template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThreads, TileS::kWaves) void k_vocab_few(Product a) {
-  using C = TileS;
-  static_assert(C::WN == 1 && C::BM == 128 && C::BN == 64 && C::kThreads == 256, "the loads below");
+template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileF<DT>::kThreads, TileF<DT>::kWaves) void k_vocab_few(Product a) {
+  using C = TileF<DT>;
+  static_assert(C::WN == 1 && C::BN == 64 && C::kThreads == 256, "the loads below");
   constexpr bool kAlong = DIR == S_LOGITS;
   constexpr int PL = DT == D_FP32 ? 3 : 1, kPer = DT == D_FP32 ? 4 : 8;  // kPer: elements of a 16-byte load
   constexpr int kLoads = C::BM * kBK / kPer / C::kThreads, kRow = (kAlong ? kBK : C::BM) / kPer;
@@ -1023,6 +1052,7 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
   const Wave w{wm, 0, lane};
   const int active = chunk_active(a), steps = (DIR == S_LOGITS ? a.Hp : a.Vp) / kBK;
   const int ntiles = (active + C::BN - 1) / C::BN, tiles = ntiles * a.mtiles;
+  const int parts = __builtin_amdgcn_readfirstlane((active + 15) / 16);  // sixteen rows each
   struct Slice {
     V x[kLoads];
     bf16x8 y[PL];
@@ -1087,14 +1117,7 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
           *reinterpret_cast<AR_LDS V*>(p) = r.x[i];
         } else {
           bf16x4 o[3];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            __bf16 b[3];
-            split3(r.x[i][j], b);
-            o[0][j] = b[0];
-            o[1][j] = b[1];
-            o[2][j] = b[2];
-          }
+          split3_of<4>(r.x[i], o);
 #pragma unroll
           for (int l = 0; l < 3; ++l) *reinterpret_cast<AR_LDS bf16x4*>(p + l * C::kX) = o[l];
         }
@@ -1128,7 +1151,8 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
 #pragma unroll
         for (int l = 0; l < PL; ++l)
 #pragma unroll
-          for (int j = 0; j < C::FN; ++j) y[l][j] = read_along(here + PL * C::kX + l * C::kY, j * 16, lane);
+          for (int j = 0; j < C::FN; ++j)
+            if (j < parts) y[l][j] = read_along(here + PL * C::kX + l * C::kY, j * 16, lane);
 #pragma unroll
         for (int f = 0; f < C::FM; ++f) {
           bf16x8 x[PL];
@@ -1141,7 +1165,7 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileS::kThread
           for (int pass = 0; pass < (PL == 3 ? 6 : 1); ++pass)
 #pragma unroll
             for (int j = 0; j < C::FN; ++j)
-              acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
+              if (j < parts) acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
         }
       }
     }
@@ -1169,7 +1193,8 @@ struct Soft {
   int32_t planes, block;  // block: columns a statistic covers
   int64_t Vp;
   float temperature;
-  float* lse;    // [chunk rows], times log2(e), as the statistics
+  float2* lse;   // [chunk rows] in two parts: the largest logit, the log of the sum around it (their sum would round
+                 // p by 2^-24 of the logit)
   float* coef;   // [chunk rows]: the row's weight in the loss over the temperature; 0 behind the rows
   float* exps;   // fp32: exp(z - m)
   char* d;
@@ -1207,7 +1232,7 @@ __device__ __forceinline__ Teacher teacher_of(const Targets& t, const Ends& e, i
 constexpr int kJoinThreads = 1024, kJoinRows = 16;
 __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Targets t) {
   __shared__ float2 part[kJoinThreads / 64][kJoinRows];
-  __shared__ float row_lse[kJoinRows];
+  __shared__ float2 row_lse[kJoinRows];
   __shared__ double wave_sum[kJoinThreads / 64];
   __shared__ bool is_last;
   const int row = threadIdx.x % 16, slice = threadIdx.x / 16, wave = threadIdx.x / 64, lane = threadIdx.x & 63;
@@ -1244,9 +1269,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
       m = -INFINITY, s = 0;
       for (int w = lane / 16; w < kJoinThreads / 64; w += 4) join(m, s, part[w][row].x, part[w][row].y);
       join_lanes(m, s);
-      float lse = 0, coef = 0;
+      float2 lse = {0, 0};
+      float coef = 0;
       if (r < active) {
-        lse = m + log2f(s);
+        lse = float2{m, log2f(s)};
         coef = 1.f / a.temperature;
         if (a.weights) coef *= a.weights[a.rows[a.chunk + r]];
         if (a.reduction == R_MEAN) coef /= float(a.counts->mean);
@@ -1266,7 +1292,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
         if (e.idt[(a.chunk + i) * int64_t(e.ld_idt) + k] < 0) continue;
         float x;
         const float q = teacher.q(k, &x);
-        if (q != 0) loss += q * ((t.K ? x - logf(teacher.stat.y) : 0.f) + (row_lse[wave] - e.zt[int64_t(i) * e.ld_idt + k]) * kLn2);
+        if (q != 0) loss += q * ((t.K ? x - logf(teacher.stat.y) : 0.f) + ((row_lse[wave].x - e.zt[int64_t(i) * e.ld_idt + k]) + row_lse[wave].y) * kLn2);
       }
 #pragma unroll
       for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
@@ -1310,7 +1336,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
     float x;
     if (ids[l] == id) q += teacher.q(l, &x);
   }
-  const float d = a.coef[i] * (exp2f(e.zt[int64_t(i) * e.ld_idt + k] - a.lse[i]) - q);
+  const float d = a.coef[i] * (exp2f((e.zt[int64_t(i) * e.ld_idt + k] - a.lse[i].x) - a.lse[i].y) - q);
   __bf16* row = reinterpret_cast<__bf16*>(a.d) + int64_t(i) * (DT == D_BF16 ? 1 : 3) * a.Vp;
   if constexpr (DT == D_BF16) {
     row[id] = __bf16(d);
@@ -1325,7 +1351,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
 // exp(z - m) -> c p, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
 constexpr int kNormThreads = 256, kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
-  constexpr int kBlocks = kNormCols / 128;
+  constexpr int kBlocks = kNormCols / 64;  // no statistic covers fewer columns
   __shared__ float factor[kNormRows][kBlocks];
   const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK / kNormRows;
   const int64_t cols = (a.Vp + kNormCols - 1) / kNormCols, tiles = cols * end;
@@ -1337,10 +1363,10 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
     const int32_t own = e.ld_idt == kFewIds && threadIdx.x < kNormRows * kFewIds && own_row < active ? e.idt[int64_t(a.chunk + own_row) * kFewIds + own_k] : -1;
     {
       const int r = threadIdx.x % kNormRows, b = threadIdx.x / kNormRows;
-      const int64_t c = c0 + b * 128;
+      const int64_t c = c0 + b * 64;
       float f = 0;
       const float w = b < kBlocks ? a.coef[r0 + r] : 0.f;
-      if (w != 0 && c < a.Vp) f = exp2f(a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r]) * w;
+      if (w != 0 && c < a.Vp) f = exp2f((a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r].x) - a.lse[r0 + r].y) * w;
       if (b < kBlocks) factor[r][b] = f;
     }
     __syncthreads();
@@ -1361,7 +1387,7 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
           const int r = r4 + q * kNormThreads / kLanes;
-          const float f = factor[r][c8 / 128];
+          const float f = factor[r][c8 / 64];
           if constexpr (DT == D_BF16) {
             bf16x8 o;
 #pragma unroll
@@ -1369,14 +1395,7 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
             *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8) = o;
           } else {
             bf16x8 o[3];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              __bf16 b[3];
-              split3(v[q][j] * f, b);
-              o[0][j] = b[0];
-              o[1][j] = b[1];
-              o[2][j] = b[2];
-            }
+            split3_of<8>(v[q] * f, o);
 #pragma unroll
             for (int i = 0; i < 3; ++i)
               *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + (int64_t(r0 + r) * 3 + i) * a.Vp + c0 + c8) = o[i];
@@ -1436,7 +1455,7 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
 size_t up(size_t n, size_t unit = 256) { return (n + unit - 1) / unit * unit; }
 int64_t blocks_of(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(n, std::min<int64_t>(launch_blocks(), int64_t(1) << 22))); }
 
-enum Size { Z_S = 0, Z_M = 1, Z_L = 2 };
+enum Size { Z_S = 0, Z_M = 1, Z_L = 2, Z_F = 3 };
 
 // Scratch of D and the exponentials that one chunk of tokens may take.
 constexpr int64_t kChunkBytes = int64_t(4) << 30;
@@ -1458,7 +1477,7 @@ struct Plan {
 };
 
 int64_t tiles_of(Size z, int64_t m, int64_t n) {
-  const int64_t bm = z == Z_L ? 256 : 128, bn = z == Z_L ? 256 : z == Z_M ? 128 : 64;
+  const int64_t bm = z == Z_L ? 256 : z == Z_F ? 64 : 128, bn = z == Z_L ? 256 : z == Z_M ? 128 : 64;
   return ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
 }
 
@@ -1488,12 +1507,14 @@ Plan plan_of(const Vocab& v, bool grad) {
   if (p.few) p.packed = false;
   p.Tpad = int64_t(up(size_t(std::max<int64_t>(v.T, 1)), kUnit));
   // a chunk's scratch: statistics at their finest, and with gradients the exponentials and D
-  const int64_t per = p.Vp / 128 * 8 + (grad ? (v.dtype == D_FP32 ? 10 : 2) * p.Vp : 0);
+  const int64_t per = p.Vp / 64 * 8 + (grad ? (v.dtype == D_FP32 ? 10 : 2) * p.Vp : 0);
   p.Tc = std::min(p.Tpad, std::max<int64_t>(kUnit, kChunkBytes / per / kUnit * kUnit));
   p.chunks = (p.Tpad + p.Tc - 1) / p.Tc;
   const int64_t n = std::min(p.Tc, v.T), passes = p.planes == 1 ? 1 : 6;
   p.logits = size_for(p.Vp, n, 1);
-  p.block = p.logits == Z_L ? 256 : 128;
+  const Size few = v.dtype == D_FP32 ? Z_F : Z_S;
+  if (p.few) p.logits = few;
+  p.block = p.logits == Z_L ? 256 : p.logits == Z_F ? 64 : 128;
   p.tile_rows = p.logits == Z_L ? 256 : p.logits == Z_M ? 128 : 64;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += up(bytes); return o; };
@@ -1505,7 +1526,7 @@ Plan plan_of(const Vocab& v, bool grad) {
   p.idt = take(size_t(p.Kp) * size_t(p.Tpad) * 4);
   p.hp = take(size_t(p.Tpad) * size_t(p.planes) * size_t(p.Hp) * 2);
   p.wp = take(p.packed ? size_t(p.Vp) * size_t(p.planes) * size_t(p.Hp) * 2 : 0);
-  p.lse = take(size_t(p.Tc) * 4);
+  p.lse = take(size_t(p.Tc) * 8);
   p.coef = take(size_t(p.Tc) * 4);
   p.row_loss = take(size_t(p.Tpad) * 4);
   p.zt = take(size_t(p.Tc) * size_t(p.Kp) * 4);
@@ -1517,7 +1538,7 @@ Plan plan_of(const Vocab& v, bool grad) {
     p.exps = take(v.dtype == D_FP32 ? size_t(p.Tc) * size_t(p.Vp) * 4 : 0);
     p.d = take(size_t(p.Tc) * size_t(p.Vp) * size_t(p.planes) * 2);
     const int64_t hidden_steps = p.Vp / kBK * (p.few ? 1 : passes);
-    p.hidden = size_for(v.H, n, hidden_steps / 8);
+    p.hidden = p.few ? few : size_for(v.H, n, hidden_steps / 8);
     p.hidden_splits = splits_for(tiles_of(p.hidden, v.H, n), hidden_steps, n * p.Hp * 4);
     p.weight = size_for(v.H, p.Vp, 1);
     if (p.chunks == 1) p.weight_splits = splits_for(tiles_of(p.weight, v.H, p.Vp), (n + kBK - 1) / kBK * passes, p.Vp * p.Hp * 4);
@@ -1533,7 +1554,7 @@ template <int DT, int DIR, int KEEP> void launch_product(Sequence& s, const Plan
   const int64_t most = std::min<int64_t>(launch_blocks(), kUnits * (z == Z_L ? 1 : 2));  // as many as stay resident
   const int64_t blocks = std::max<int64_t>(1, std::min(tiles * a.splits, most));
   if constexpr (DIR != S_WEIGHT)
-    if (p.few) return s.launch(k_vocab_few<DT, DIR, KEEP>, blocks, TileS::kThreads, a);
+    if (p.few) return s.launch(k_vocab_few<DT, DIR, KEEP>, blocks, TileF<DT>::kThreads, a);
   if (z == Z_L) s.launch(k_vocab_product<TileL, DIR, KEEP>, blocks, TileL::kThreads, a);
   else if (z == Z_M) s.launch(k_vocab_product<TileM, DIR, KEEP>, blocks, TileM::kThreads, a);
   else if constexpr (DIR != S_WEIGHT) s.launch(k_vocab_product<TileS, DIR, KEEP>, blocks, TileS::kThreads, a);
@@ -1611,7 +1632,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.dh = v.dh;
   a.dh_ld = v.dh_ld;
   Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
-         v.temperature, reinterpret_cast<float*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
+         v.temperature, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
   const auto rows_of = [&](int64_t c) { return std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)); };
   const auto join_blocks = [&](int64_t n) { return blocks_of(int64_t(up(size_t(n), kUnit)) / kJoinRows); };
   Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, each ? nullptr : v.loss, 0};
