@@ -1031,9 +1031,10 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 // Few rows against an output matrix that loads into LDS cannot bring as bf16 (fp32, or rows at odd addresses): the
 // products read it as it is, split it into terms on the way to LDS and multiply all terms of a slice at once, where
 // many rows are better served by a copy (which reads, writes and reads again what is read once here). S_LOGITS and
-// S_HIDDEN only: the output matrix is X. kDeep slices are on their way in registers.
+// S_HIDDEN only: the output matrix is X. kDeep slices are on their way in registers. PARTS: sixteen rows each, of which
+// products are formed.
 constexpr int kFewRows = 64, kDeep = 3;
-template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileF<DT>::kThreads, TileF<DT>::kWaves) void k_vocab_few(Product a) {
+template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(TileF<DT>::kThreads, TileF<DT>::kWaves) void k_vocab_few(Product a) {
   using C = TileF<DT>;
   static_assert(C::WN == 1 && C::BN == 64 && C::kThreads == 256, "the loads below");
   constexpr bool kAlong = DIR == S_LOGITS;
@@ -1052,7 +1053,6 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileF<DT>::kTh
   const Wave w{wm, 0, lane};
   const int active = chunk_active(a), steps = (DIR == S_LOGITS ? a.Hp : a.Vp) / kBK;
   const int ntiles = (active + C::BN - 1) / C::BN, tiles = ntiles * a.mtiles;
-  const int parts = __builtin_amdgcn_readfirstlane((active + 15) / 16);  // sixteen rows each
   struct Slice {
     V x[kLoads];
     bf16x8 y[PL];
@@ -1088,7 +1088,7 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileF<DT>::kTh
         const int q = i * C::kThreads + tid;
         r.x[i] = *reinterpret_cast<const Any*>(reinterpret_cast<const Global*>(wp) + int64_t(min(row0 + q / kRow, rows - 1)) * ld + min(col0 + q % kRow * kPer, a.H - kPer));
       }
-      const int64_t n = at.n0 + tid / 4;
+      const int64_t n = min(at.n0 + tid / 4, active - 1);
       const char* p = (DIR == S_LOGITS ? a.hp + (a.chunk + n) * PL * a.Hp * 2 : a.d + n * PL * a.Vp * 2) + (k + tid % 4 * 8) * 2;
 #pragma unroll
       for (int i = 0; i < PL; ++i)
@@ -1147,12 +1147,11 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileF<DT>::kTh
         store(r[i], s + i, here);
         load(r[i], s + i + kDeep);
         lds_barrier();  // the slice is there, and the one before the last has been multiplied
-        bf16x8 y[PL][C::FN];
+        bf16x8 y[PL][PARTS];
 #pragma unroll
         for (int l = 0; l < PL; ++l)
 #pragma unroll
-          for (int j = 0; j < C::FN; ++j)
-            if (j < parts) y[l][j] = read_along(here + PL * C::kX + l * C::kY, j * 16, lane);
+          for (int j = 0; j < PARTS; ++j) y[l][j] = read_along(here + PL * C::kX + l * C::kY, j * 16, lane);
 #pragma unroll
         for (int f = 0; f < C::FM; ++f) {
           bf16x8 x[PL];
@@ -1164,8 +1163,8 @@ template <int DT, int DIR, int KEEP> __global__ __launch_bounds__(TileF<DT>::kTh
 #pragma unroll
           for (int pass = 0; pass < (PL == 3 ? 6 : 1); ++pass)
 #pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-              if (j < parts) acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
+            for (int j = 0; j < PARTS; ++j)
+              acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
         }
       }
     }
@@ -1554,7 +1553,10 @@ template <int DT, int DIR, int KEEP> void launch_product(Sequence& s, const Plan
   const int64_t most = std::min<int64_t>(launch_blocks(), kUnits * (z == Z_L ? 1 : 2));  // as many as stay resident
   const int64_t blocks = std::max<int64_t>(1, std::min(tiles * a.splits, most));
   if constexpr (DIR != S_WEIGHT)
-    if (p.few) return s.launch(k_vocab_few<DT, DIR, KEEP>, blocks, TileF<DT>::kThreads, a);
+    if (p.few) {
+      if (a.chunk_rows <= 16) return s.launch(k_vocab_few<DT, DIR, KEEP, 1>, blocks, TileF<DT>::kThreads, a);
+      return s.launch(k_vocab_few<DT, DIR, KEEP, 4>, blocks, TileF<DT>::kThreads, a);
+    }
   if (z == Z_L) s.launch(k_vocab_product<TileL, DIR, KEEP>, blocks, TileL::kThreads, a);
   else if (z == Z_M) s.launch(k_vocab_product<TileM, DIR, KEEP>, blocks, TileM::kThreads, a);
   else if constexpr (DIR != S_WEIGHT) s.launch(k_vocab_product<TileS, DIR, KEEP>, blocks, TileS::kThreads, a);
