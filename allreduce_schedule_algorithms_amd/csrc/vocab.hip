@@ -170,9 +170,9 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int
   }
 }
 
-// Rows that take part, in order, at rows[0..active); the others behind them. One workgroup.
+// Rows that take part, in order, at rows[0..active); the others behind them. One workgroup; returns active.
 constexpr int kScanThreads = 1024, kScanEach = 4;
-__device__ __forceinline__ void scan_rows(const Targets& t, int64_t T, int32_t* rows, uint8_t* flags, Counts* counts) {
+__device__ __forceinline__ int scan_rows(const Targets& t, int64_t T, int32_t* rows, uint8_t* flags, Counts* counts) {
   __shared__ int wave_n[kScanThreads / 64][kScanEach], tally[2], round;
   const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
   if (tid < 2) tally[tid] = 0;
@@ -229,6 +229,7 @@ __device__ __forceinline__ void scan_rows(const Targets& t, int64_t T, int32_t* 
   __syncthreads();
   if (tid == 0) *counts = Counts{done, tally[0], tally[1], 0u};
   __syncthreads();
+  return done;
 }
 
 // The hidden rows that take part, gathered as bf16 terms of Hp elements each, zeros behind them; their ids as padded
@@ -249,49 +250,48 @@ struct PackArgs {
   float* each;   // every row's loss, or null
 };
 
-template <int DT> __device__ __forceinline__ float elem(const void* p, int64_t i) {
-  if constexpr (DT == D_BF16) return as_f(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
-  else return static_cast<const float*>(p)[i];
-}
-
-// A row of H elements into terms of Hp elements, zero behind H. Called by a whole wave.
+// A row of H elements into terms of Hp elements, zero behind H. Called by a whole wave; four vectors a lane are on
+// their way together.
 template <int DT> __device__ __forceinline__ void pack_row(const void* src, int64_t at, int H, int Hp, __bf16* dst, int lane) {
-  for (int c = lane * 8; c < Hp; c += 512) {
-    if constexpr (DT == D_BF16) {
-      const uint16_t* s = static_cast<const uint16_t*>(src) + at + c;
-      typedef uint16_t V __attribute__((ext_vector_type(8), aligned(2)));
-      V v;
+  using E = std::conditional_t<DT == D_BF16, uint16_t, float>;
+  typedef E V __attribute__((ext_vector_type(8)));
+  typedef E Any __attribute__((ext_vector_type(8), aligned(sizeof(E))));
+  const E* s = static_cast<const E*>(src) + at;
+  for (int c0 = lane * 8; c0 < Hp; c0 += 4 * 512) {
+    V v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = c0 + q * 512;
+      v[q] = V{};
       if (c + 8 <= H) {
-        v = *reinterpret_cast<const V*>(s);
+        v[q] = *reinterpret_cast<const Any*>(s + c);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < H ? s[j] : uint16_t(0);
+        for (int j = 0; j < 7; ++j)
+          if (c + j < H) v[q][j] = s[c + j];
       }
-      typedef uint16_t A __attribute__((ext_vector_type(8)));
-      *reinterpret_cast<A*>(dst + c) = v;
-    } else {
-      const float* s = static_cast<const float*>(src) + at + c;
-      typedef float V __attribute__((ext_vector_type(8), aligned(4)));
-      f32x8 v;
-      if (c + 8 <= H) {
-        v = *reinterpret_cast<const V*>(s);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int c = c0 + q * 512;
+      if (c >= Hp) break;
+      if constexpr (DT == D_BF16) {
+        *reinterpret_cast<V*>(dst + c) = v[q];
       } else {
+        bf16x8 o[3];
+        split3_of<8>(v[q], o);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = c + j < H ? s[j] : 0.f;
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(dst + int64_t(i) * Hp + c) = o[i];
       }
-      bf16x8 o[3];
-      split3_of<8>(v, o);
-#pragma unroll
-      for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(dst + int64_t(i) * Hp + c) = o[i];
     }
   }
 }
 
-template <int DT> __device__ __forceinline__ void pack_rows(const PackArgs& a, const Targets& t, const Piece* pieces, int64_t first, int64_t step) {
+template <int DT> __device__ __forceinline__ void pack_rows(const PackArgs& a, const Targets& t, const Piece* pieces, int active, int64_t first, int64_t step) {
   constexpr int PL = DT == D_FP32 ? 3 : 1;
   const int lane = threadIdx.x & 63;
   // the products go 2 kBK rows deep at a time, and tiles look up the ids of up to kUnit rows
-  const int active = a.counts->active, zeros = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK, end = (active + kUnit - 1) / kUnit * kUnit;
+  const int zeros = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK, end = (active + kUnit - 1) / kUnit * kUnit;
   const int K = t.K ? t.K : 1;
   for (int64_t i = first; i < a.Tpad; i += step) {
     const int64_t r = i < a.T ? a.rows[i] : -1;
@@ -324,7 +324,7 @@ template <int DT> __device__ __forceinline__ void pack_rows(const PackArgs& a, c
   }
 }
 template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack(PackArgs a, Targets t) {
-  pack_rows<DT>(a, t, a.pieces, int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64, int64_t(gridDim.x) * kRowWaves);
+  pack_rows<DT>(a, t, a.pieces, a.counts->active, int64_t(blockIdx.x) * kRowWaves + threadIdx.x / 64, int64_t(gridDim.x) * kRowWaves);
 }
 
 // More ids a row than kFewIds are sorted by the tile of logits that they lie in, so that a tile finds its own: one
@@ -398,8 +398,10 @@ template <int DT> __global__ __launch_bounds__(kScanThreads) void k_vocab_prepar
       }
       p.pieces[p.tab.at + i] = q;
     }
-    if (p.scan) scan_rows(t, p.T, p.rows, p.flags, p.counts);
-    if (p.pack) pack_rows<DT>(a, t, p.tab.p, wave, kScanThreads / 64);
+    if (p.scan) {
+      const int active = scan_rows(t, p.T, p.rows, p.flags, p.counts);
+      if (p.pack) pack_rows<DT>(a, t, p.tab.p, active, wave, kScanThreads / 64);
+    }
   }
   if (!p.wp) return;
   const int64_t helpers = gridDim.x > 1 ? gridDim.x - 1 : 1, me = gridDim.x > 1 ? int64_t(blockIdx.x) - 1 : 0;
@@ -1326,15 +1328,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
   }
 }
 
-// D at an id of a row: c (p - q), q summed over the row's equal ids.
-template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const Ends& e, const Targets& t, int i, int k, int32_t id) {
-  const Teacher teacher = teacher_of(t, e, a.rows[a.chunk + i]);
-  const int32_t* ids = e.idt + (a.chunk + i) * int64_t(e.ld_idt);
-  float q = 0;
-  for (int l = 0; l < e.ld_idt; ++l) {
-    float x;
-    if (ids[l] == id) q += teacher.q(l, &x);
-  }
+// D at an id of a row: c (p - q), q the sum over the row's equal ids.
+template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const Ends& e, int i, int k, int32_t id, float q) {
   const float d = a.coef[i] * (exp2f((e.zt[int64_t(i) * e.ld_idt + k] - a.lse[i].x) - a.lse[i].y) - q);
   __bf16* row = reinterpret_cast<__bf16*>(a.d) + int64_t(i) * (DT == D_BF16 ? 1 : 3) * a.Vp;
   if constexpr (DT == D_BF16) {
@@ -1402,17 +1397,35 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
         }
       }
     __syncthreads();
-    if (own >= c0 && own < c0 + kNormCols) put_own<DT>(a, e, t, own_row, own_k, own);
+    if (own >= c0 && own < c0 + kNormCols) {
+      const Teacher teacher = teacher_of(t, e, a.rows[a.chunk + own_row]);
+      float q = 0, x;
+      for (int l = 0; l < kFewIds; ++l)
+        if (e.idt[int64_t(a.chunk + own_row) * kFewIds + l] == own) q += teacher.q(l, &x);
+      put_own<DT>(a, e, own_row, own_k, own, q);
+    }
   }
 }
 
-// More ids a row than kFewIds: a thread for each.
+// More ids a row than kFewIds: a wave for 64 of a row's, which it compares with all of the row's, 64 in registers.
 template <int DT> __global__ __launch_bounds__(256) void k_vocab_own(Soft a, Ends e, Targets t) {
-  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows);
-  for (int64_t n = int64_t(blockIdx.x) * 256 + threadIdx.x; n < int64_t(active) * e.ld_idt; n += int64_t(gridDim.x) * 256) {
-    const int i = int(n / e.ld_idt), k = int(n % e.ld_idt);
-    const int32_t id = e.idt[int64_t(a.chunk) * e.ld_idt + n];
-    if (id >= 0) put_own<DT>(a, e, t, i, k, id);
+  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), lane = threadIdx.x & 63, parts = (e.ld_idt + 63) / 64;
+  for (int64_t n = int64_t(blockIdx.x) * 4 + threadIdx.x / 64; n < int64_t(active) * parts; n += int64_t(gridDim.x) * 4) {
+    const int i = int(n / parts), k = int(n % parts) * 64 + lane;
+    const int32_t* ids = e.idt + (a.chunk + i) * int64_t(e.ld_idt);
+    const Teacher teacher = teacher_of(t, e, a.rows[a.chunk + i]);
+    const int32_t id = k < e.ld_idt ? ids[k] : -1;
+    float sum = 0;
+    for (int l0 = 0; l0 < e.ld_idt; l0 += 64) {
+      const int32_t other = l0 + lane < e.ld_idt ? ids[l0 + lane] : -1;
+      float x, q = 0;
+      if (other >= 0) q = teacher.q(l0 + lane, &x);
+      for (int l = 0; l < min(64, e.ld_idt - l0); ++l) {
+        const float ql = as_f(__builtin_amdgcn_readlane(as_u(q), l));
+        sum += __builtin_amdgcn_readlane(other, l) == id ? ql : 0.f;
+      }
+    }
+    if (id >= 0) put_own<DT>(a, e, i, k, id, sum);
   }
 }
 
@@ -1655,7 +1668,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     s.launch(k_vocab_join, join_blocks(n), kJoinThreads, f, ends, t);
     if (!grad) continue;
     s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f, ends, t);
-    if (sorted) s.launch(k_vocab_own<DT>, blocks_of((n * p.Kp + 255) / 256), 256, f, ends, t);
+    if (sorted) s.launch(k_vocab_own<DT>, blocks_of((n * ((p.Kp + 63) / 64) + 3) / 4), 256, f, ends, t);
     const auto mtiles = [&](Size z) { return int32_t(tiles_of(z, v.H, 1)); };
     a.mtiles = mtiles(p.hidden);
     a.splits = p.hidden_splits;
