@@ -35,6 +35,8 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x8 __attribute__((ext_vector_type(8)));
@@ -449,7 +451,7 @@ struct Product {
   int32_t chunk, chunk_rows;  // this call's rows: [chunk, chunk + chunk_rows) of those that take part
   int32_t kend;               // elements of a row along H that exist
   const char* hp;             // gathered hidden rows
-  char* d;                    // [rows][planes * Vp]: exp(z - m), then D
+  char* d;                    // [rows][planes * Vp]: (bf16) exp(z - m) in fp16, then D
   // logits
   float scale;  // log2(e) / temperature
   float2* stats;  // [Vp / BM][ld_stats]
@@ -715,10 +717,10 @@ template <class E, class V> __device__ __forceinline__ void put(E* p, V v, int l
 
 // Two products' registers, m 4 (lane / 16) on of 16 each, rounded and exchanged between the quarters of the wave: m
 // 8 (lane / 16) on of the 32.
-__device__ __forceinline__ bf16x8 eight_of(f32x4 a, f32x4 b) {
+template <class V8, class V4> __device__ __forceinline__ V8 eight_of(f32x4 a, f32x4 b) {
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  const u32x2 x = __builtin_bit_cast(u32x2, __builtin_convertvector(a, bf16x4)), y = __builtin_bit_cast(u32x2, __builtin_convertvector(b, bf16x4));
+  const u32x2 x = __builtin_bit_cast(u32x2, __builtin_convertvector(a, V4)), y = __builtin_bit_cast(u32x2, __builtin_convertvector(b, V4));
   u32x4 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -727,7 +729,7 @@ __device__ __forceinline__ bf16x8 eight_of(f32x4 a, f32x4 b) {
     r[i] = q[0];
     r[2 + i] = q[1];
   }
-  return __builtin_bit_cast(bf16x8, r);
+  return __builtin_bit_cast(V8, r);
 }
 
 // A barrier for what the workgroup leaves in LDS, which waits for no load or store of global memory.
@@ -823,6 +825,11 @@ template <class C> __device__ __forceinline__ void pick_own(const Product& a, f3
   }
 }
 
+// A bf16 call keeps its exponentials in fp16, as many bytes with eight times the precision: times kKept they are
+// normal down to 2^-28 of the tile's largest, off by 2^-11 of their value or 2^-39 of the largest. (In bf16 D was
+// rounded twice, and its products' results off by half as much again.)
+constexpr float kKept = 16384;
+
 // A logits tile's exponentials, largest values and sums. scratch: [2][WM][BN] of LDS.
 template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, Wave wave, AR_LDS float* scratch) {
   static_assert(KEEP != D_BF16 || C::FM % 2 == 0, "bf16 is written by pairs of products");
@@ -858,7 +865,7 @@ template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Pr
         s += acc[i][j][e];
       }
       if constexpr (KEEP == D_BF16)
-        if (i & 1) *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + row + (i - 1) * 16 + lane / 16 * 8) = eight_of(acc[i - 1][j], acc[i][j]);
+        if (i & 1) *reinterpret_cast<f16x8*>(reinterpret_cast<_Float16*>(a.d) + row + (i - 1) * 16 + lane / 16 * 8) = eight_of<f16x8, f16x4>(acc[i - 1][j] * kKept, acc[i][j] * kKept);
       if constexpr (KEEP == D_FP32) *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.part) + row + i * 16 + lane / 16 * 4) = acc[i][j];
     }
     s += __shfl_xor(s, 16);
@@ -909,7 +916,7 @@ template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradie
       } else if constexpr (KEEP == D_BF16) {
         if (i & 1) {
           const int m8 = wm0 + (i - 1) * 16 + lane / 16 * 8;
-          const bf16x8 v = eight_of(acc[i - 1][j], acc[i][j]);
+          const bf16x8 v = eight_of<bf16x8, bf16x4>(acc[i - 1][j], acc[i][j]);
           if (there && m8 < a.H) put(reinterpret_cast<__bf16*>(row) + m8, v, a.H - m8);
         }
       } else {
@@ -1342,7 +1349,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
   }
 }
 
-// exp(z - m) -> c p, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
+// exp(z - m) -> c p, in place for bf16, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
 constexpr int kNormThreads = 256, kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
   constexpr int kBlocks = kNormCols / 64;  // no statistic covers fewer columns
@@ -1361,21 +1368,21 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
       float f = 0;
       const float w = b < kBlocks ? a.coef[r0 + r] : 0.f;
       if (w != 0 && c < a.Vp) f = exp2f((a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r].x) - a.lse[r0 + r].y) * w;
-      if (b < kBlocks) factor[r][b] = f;
+      if (b < kBlocks) factor[r][b] = DT == D_BF16 ? f / kKept : f;
     }
     __syncthreads();
     constexpr int kLanes = kNormCols / 8;
     const int c8 = threadIdx.x % kLanes * 8;
     if (c0 + c8 < a.Vp)
       for (int r4 = threadIdx.x / kLanes; r4 < kNormRows; r4 += kBatch * kNormThreads / kLanes) {
-        using In = std::conditional_t<DT == D_BF16, bf16x8, f32x8>;
+        using In = std::conditional_t<DT == D_BF16, f16x8, f32x8>;
         In v[kBatch];  // loaded together
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
           const int r = r4 + q * kNormThreads / kLanes;
           v[q] = In{};
           if (r0 + r >= active) continue;
-          if constexpr (DT == D_BF16) v[q] = *reinterpret_cast<const In*>(reinterpret_cast<const __bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8);
+          if constexpr (DT == D_BF16) v[q] = *reinterpret_cast<const In*>(reinterpret_cast<const _Float16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8);
           else v[q] = *reinterpret_cast<const In*>(a.exps + int64_t(r0 + r) * a.Vp + c0 + c8);
         }
 #pragma unroll

@@ -37,8 +37,9 @@ def loss_and_gradients(hidden, weight, ids, logits=None, reduction="mean", tempe
     * statistics: a shift of all logits by at most dz changes log-sum-exp by at most that; exponentials are off by 4 U
       and what rounds their argument, U (|z| + |lse|) log2(e), sums by U for each of at most 192 levels;
     * losses: both, the target's own logit, and a rounding of every operation (16 U of every term);
-    * D = c (p - q): p's relative error is that of its exponent; in bf16 exp(z - m) and D are rounded, 2 U_BF16;
-      in fp32 a few U;
+    * D = c (p - q): p's relative error is that of its exponent; in bf16 D is rounded, U_BF16, and exp(z - m) to fp16
+      times 2^14, 2^-11 of it or, below the smallest normal value, 2^-25, which is 2^-39 of the largest; in fp32 a
+      few U;
     * products of D: its error times the other operand, a sum of fp32 terms in any order (n U of the terms'
       magnitudes), the rounding of the result;
     * values below the smallest normal one, 2^-126, may be lost: the exponential (then times c), D itself, the terms
@@ -102,7 +103,8 @@ def loss_and_gradients(hidden, weight, ids, logits=None, reduction="mean", tempe
     dp = p * (dz + dlse + 4 * U * (2 + z.abs() + lse.abs()))
     dD = c.abs() * dp + 8 * U * (c.abs() * p)
     if dtype == "bf16":
-        dD = dD + 2.02 * U_BF16 * (c.abs() * p)
+        most_p = p.max(1, keepdim=True)[0] if len(take) else p.new_zeros(0, 1)
+        dD = dD + 1.01 * (U_BF16 + 2.0 ** -11) * (c.abs() * p) + 2.0 ** -39 * (c.abs() * most_p)
     own_q = torch.zeros_like(p).scatter_add_(1, at, q)
     dq = own_q * (K + 64) * U * (1 + (float(log_q.abs().max()) if log_q.numel() else 0.0))
     dD = dD + c.abs() * (dq + 4 * U * own_q) + (U_BF16 if dtype == "bf16" else U) * 1.01 * torch.where(own_q > 0, D.abs(), torch.zeros_like(D))

@@ -107,9 +107,10 @@ def test_workspace_is_bounded_in_the_tokens():
 
 
 def test_pointers_do_not_count_for_the_workspace_but_by_their_alignment():
-    def at(w):
-        return A.ar_vocab_workspace_bytes(call(pieces=[(w, None, 100, 64, 64)], hidden=None, ids=None, loss=None, dh=None))
+    def at(w, T=100):
+        return A.ar_vocab_workspace_bytes(call(T=T, pieces=[(w, None, 100, 64, 64)], hidden=None, ids=None, loss=None, dh=None))
     assert at(None) == at(BASE) < at(BASE + 2)
+    assert at(BASE, 64) == at(BASE + 2, 64)  # few rows: read in place at any address
 
 
 def test_null_arguments():
