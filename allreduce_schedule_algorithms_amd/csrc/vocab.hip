@@ -447,7 +447,8 @@ template <int DT> using TileF = std::conditional_t<DT == D_FP32, Tile<64, 64, 4,
 struct Product {
   const Piece* pieces;
   const Counts* counts;
-  int32_t P, H, Hp, Vp, mtiles, planes, splits;
+  int32_t P, H, Hp, Vp, mtiles, planes;
+  int32_t splits, bn, resident;  // at most so many shares of the depth; columns of a tile; workgroups that stay resident
   int32_t chunk, chunk_rows;  // this call's rows: [chunk, chunk + chunk_rows) of those that take part
   int32_t kend;               // elements of a row along H that exist
   const char* hp;             // gathered hidden rows
@@ -740,6 +741,13 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Shares of a product's depth: as many as give every compute unit a tile, by the rows that there are (12 tiles in 21
+// shares run in one round where 32 took two; more shares are more partial sums to write and read).
+__device__ __forceinline__ int splits_of(const Product& a, int nlen) {
+  const int tiles = (nlen + a.bn - 1) / a.bn * a.mtiles;
+  return tiles ? min(max(a.resident / tiles, 1), a.splits) : 1;
+}
+
 __device__ __forceinline__ int chunk_active(const Product& a) { return min(max(a.counts->active - a.chunk, 0), a.chunk_rows); }
 
 // Where a workgroup's tile t lies, and which slices of the depth it takes.
@@ -937,7 +945,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64), wm = wave % C::WM, wn = wave / C::WM;
   const int active = chunk_active(a);
   const int nlen = DIR == S_WEIGHT ? a.Vp : active;
-  const uint32_t ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles, tiles = ntiles * mtiles, places = tiles * a.splits;
+  const uint32_t ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles, tiles = ntiles * mtiles, splits = splits_of(a, nlen), places = tiles * splits;
   const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK;
   const int steps = depth / kBK, all = steps * (a.planes == 1 ? 1 : 6);
   St st{a, 0, 0, tid, steps};
@@ -959,7 +967,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
     const uint32_t group = u / (8 * mtiles), in_group = u - group * 8 * mtiles, width = min(8u, ntiles - group * 8);
     p.m0 = in_group / width * C::BM;
     p.n0 = (group * 8 + in_group % width) * C::BN;
-    const int pairs = all / 2, share = pairs / a.splits, over = pairs % a.splits;
+    const int pairs = all / 2, share = pairs / splits, over = pairs % splits;
     p.s0 = (p.split * share + min(p.split, over)) * 2;
     p.s1 = p.s0 + (share + (p.split < over)) * 2;
     return p;
@@ -1066,8 +1074,9 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
     V x[kLoads];
     bf16x8 y[PL];
   };
-  for (int t = blockIdx.x; t < tiles * a.splits; t += gridDim.x) {
-    const int split = t / tiles, u = t - split * tiles, share = steps / a.splits, over = steps % a.splits;
+  const int splits = splits_of(a, active);
+  for (int t = blockIdx.x; t < tiles * splits; t += gridDim.x) {
+    const int split = t / tiles, u = t - split * tiles, share = steps / splits, over = steps % splits;
     const int s0 = split * share + min(split, over);
     const Place at{u / ntiles * C::BM, u % ntiles * C::BN, split, s0, s0 + share + (split < over)};
     int rows = 0, start = 0, next = 0;
@@ -1440,6 +1449,7 @@ template <int DT> __global__ __launch_bounds__(256) void k_vocab_own(Soft a, End
 template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Product a) {
   const int n_end = DIR == S_WEIGHT ? a.Vp : chunk_active(a), per = a.Hp / 4;
   const int64_t all = int64_t(n_end) * per;
+  const int splits = splits_of(a, n_end);
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
     const int n = int(i / per), m = int(i % per) * 4;
     if (m >= a.H) continue;
@@ -1455,14 +1465,14 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
     f32x4 s = {0, 0, 0, 0};
     const float* from = a.part + int64_t(n) * a.Hp + m;
     int k = 0;
-    for (; k + 8 <= a.splits; k += 8) {  // eight on their way together, added in order
+    for (; k + 8 <= splits; k += 8) {  // eight on their way together, added in order
       f32x4 v[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const f32x4*>(from + (k + q) * a.part_stride);
 #pragma unroll
       for (int q = 0; q < 8; ++q) s += v[q];
     }
-    for (; k < a.splits; ++k) s += *reinterpret_cast<const f32x4*>(from + k * a.part_stride);
+    for (; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(from + k * a.part_stride);
     if constexpr (DT == D_BF16) put(reinterpret_cast<__bf16*>(row) + m, __builtin_convertvector(s, bf16x4), a.H - m);
     else put(reinterpret_cast<float*>(row) + m, s, a.H - m);
   }
@@ -1570,8 +1580,7 @@ Plan plan_of(const Vocab& v, bool grad) {
 }
 
 template <int DT, int DIR, int KEEP> void launch_product(Sequence& s, const Plan& p, Size z, int64_t tiles, Product a) {
-  const int64_t most = std::min<int64_t>(launch_blocks(), kUnits * (z == Z_L ? 1 : 2));  // as many as stay resident
-  const int64_t blocks = std::max<int64_t>(1, std::min(tiles * a.splits, most));
+  const int64_t blocks = std::max<int64_t>(1, std::min({tiles * a.splits, launch_blocks(), int64_t(a.resident)}));
   if constexpr (DIR != S_WEIGHT)
     if (p.few) {
       if (a.chunk_rows <= 16) return s.launch(k_vocab_few<DT, DIR, KEEP, 1>, blocks, TileF<DT>::kThreads, a);
@@ -1666,6 +1675,11 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     a.chunk = f.chunk = int32_t(c * p.Tc);
     a.chunk_rows = f.chunk_rows = int32_t(rows_of(c));
     const int64_t n = a.chunk_rows, npad = int64_t(up(size_t(n), kUnit));
+    const auto tile = [&](Size z) {
+      a.bn = int32_t(z == Z_L ? 256 : z == Z_M ? 128 : 64);
+      a.resident = z == Z_L ? kUnits : 2 * kUnits;
+    };
+    tile(p.logits);
     a.mtiles = int32_t(p.Vp / p.block);
     a.splits = 1;
     a.part = f.exps;
@@ -1677,6 +1691,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f, ends, t);
     if (sorted) s.launch(k_vocab_own<DT>, blocks_of((n * ((p.Kp + 63) / 64) + 3) / 4), 256, f, ends, t);
     const auto mtiles = [&](Size z) { return int32_t(tiles_of(z, v.H, 1)); };
+    tile(p.hidden);
     a.mtiles = mtiles(p.hidden);
     a.splits = p.hidden_splits;
     a.part = a.splits > 1 ? dh_part : nullptr;
@@ -1684,6 +1699,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     a.accumulate = 0;
     launch_product<DT, S_HIDDEN, DT>(s, p, p.hidden, tiles_of(p.hidden, v.H, n), a);
     if (a.splits > 1) s.launch(k_vocab_sum<S_HIDDEN, DT>, blocks_of((n * p.Hp / 4 + 255) / 256), 256, a);
+    tile(p.weight);
     a.mtiles = mtiles(p.weight);
     a.splits = p.weight_splits;
     a.part = a.splits > 1 || p.chunks > 1 ? dw_part : nullptr;
