@@ -12,7 +12,7 @@
 //   dh = D W,  dW = D^T h
 //
 // Rows that the targets leave out take no part: the rows that count are gathered in order
-// (k_scan, k_pack), and every product runs over as many as there are. The products are
+// (k_vocab_prepare, k_vocab_pack), and every product runs over as many as there are. The products are
 // matrix products of bf16 operands with fp32 sums; fp32 operands are split exactly into
 // three bf16 terms each, and the six products of the larger terms are summed (what is
 // left out is 2^-26 of a product).
@@ -21,6 +21,9 @@
 // leaves the product as exp(z - m), m the row's largest of the tile, beside m and the tile's sum; once
 // a row's lse is known, one pass turns them into D. Nothing is added atomically: the
 // same sizes give the same bits on every run.
+//
+// 8192 tokens x 4096 x 128000 in bf16, 8 pieces, with gradients: 21.9 ms, of which products 7.06 + 6.71 + 7.15
+// (1216, 1281 and 1201 TFLOP/s), D 0.77, the rest 0.08.
 #include "vocab.h"
 
 #include <hip/hip_ext.h>
@@ -331,7 +334,8 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
 
 // More ids a row than kFewIds are sorted by the tile of logits that they lie in, so that a tile finds its own: one
 // workgroup for the rows of a tile counts them, adds the counts up and deals the entries out. (Where an entry lies
-// among its tile's does not show in any result.)
+// among its tile's does not show in any result.) 3687 rows x 64 ids: 22 us, after which the logits of 50000 take 888;
+// with tiles that compare all of their rows' ids, 1176.
 constexpr int kFewIds = 4, kSortThreads = 1024;
 __global__ __launch_bounds__(kSortThreads) void k_vocab_sort(const int32_t* idt, int ld_idt, int bn, int bm, int mtiles, int64_t row_tiles, const Counts* counts, int32_t* starts, uint32_t* entries) {
   extern __shared__ int32_t place[];  // [mtiles + 1]
@@ -376,7 +380,7 @@ __global__ __launch_bounds__(kSortThreads) void k_vocab_sort(const int32_t* idt,
 // A call's first launch (one for every kPieceTab pieces). Workgroup 0 writes the products' table of pieces and finds
 // the rows that take part (and packs them: few elements, which another launch would cost more than). The others copy
 // the output matrix as bf16 terms where the products cannot read it (fp32, and bf16 that 16-byte loads do not fit):
-// row v of the padded vocabulary at wp + v * PL * Hp.
+// row v of the padded vocabulary at wp + v * PL * Hp. Bound by memory: 131 MB of fp32 into 197 MB take 58 us, 5.6 TB/s.
 struct PrepareArgs {
   PieceTab tab;
   Piece* pieces;
@@ -426,7 +430,7 @@ template <int DT> __global__ __launch_bounds__(kScanThreads) void k_vocab_prepar
 // A slice lies in LDS either as rows of 32 k (64 bytes; "along k") or as k rows of the tile's columns ("across").
 // The loads write LDS in lane order, so the swizzle that spreads the reads over the banks is in which 16
 // bytes a lane loads: along k, chunk c of row r lies at c ^ {0, 2, 3, 1}[r / 4 % 4]; across, the 32 bytes c of k row r lie at
-// c ^ (r % 4 + 4 (r / 8 % 4)), and the reads transpose.
+// c ^ (r % 4 + 4 (r / 8 % 4)), and the reads transpose. The counters find no bank conflicts.
 enum Dir { S_LOGITS = 0, S_HIDDEN = 1, S_WEIGHT = 2 };
 
 template <int BM_, int BN_, int WM_, int WN_, int WAVES_, int STAGES_> struct Tile {
@@ -936,6 +940,11 @@ template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradie
 
 // KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
 // the outputs' type.
+// Bound by power where tiles are many: at 8192 x 4096 x 128000 the matrix pipes are busy for 65-72% of the time, the
+// clock at 1.7-1.8 GHz, 1200-1280 TFLOP/s (on zeros, 2.3 GHz at the same share). 256 x 256 outputs for 8 waves are
+// what the accumulators hold: each slice's 32 KB are read into LDS for 4.2 MFLOP. With 64 deep double buffers the three
+// took 7.8, 9.2 and 9.3 ms in place of 7.1, 6.7 and 7.2; in 32 x 32 x 16 products 2-8% more than in 16 x 16 x 32.
+// Of up to 64 rows the reading of the output matrix bounds it: 8 x 2048 x 32000 in 25 us, 5.4 TB/s.
 template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
   __shared__ __attribute__((aligned(512))) char shared[C::kStages * C::kStage];
   using St = Stager<C, DIR>;
@@ -1048,8 +1057,9 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 // Few rows against an output matrix that loads into LDS cannot bring as bf16 (fp32, or rows at odd addresses): the
 // products read it as it is, split it into terms on the way to LDS and multiply all terms of a slice at once, where
 // many rows are better served by a copy (which reads, writes and reads again what is read once here). S_LOGITS and
-// S_HIDDEN only: the output matrix is X. kDeep slices are on their way in registers. PARTS: sixteen rows each, of which
-// products are formed.
+// S_HIDDEN only: the output matrix is X. (us a loss of 2048 x 32000, so and with a copy: fp32 of 8 rows 74 and 297, of 64
+// 98 and 297; bf16 of 64 rows of odd width 52 and 86.) kDeep slices are on their way in registers. PARTS: sixteen rows
+// each, of which products are formed.
 constexpr int kFewRows = 64, kDeep = 3;
 template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(TileF<DT>::kThreads, TileF<DT>::kWaves) void k_vocab_few(Product a) {
   using C = TileF<DT>;
@@ -1245,7 +1255,8 @@ __device__ __forceinline__ Teacher teacher_of(const Targets& t, const Ends& e, i
 
 // The rows' softmax statistics, weights and losses, 16 rows a workgroup: first a wave's lanes are 16 rows x 4
 // statistics, and its 16 waves share the statistics; then each wave takes a row's ids. The workgroup that comes last
-// adds the call's loss up, in 64 bits and in the rows' order, whichever it is.
+// adds the call's loss up, in 64 bits and in the rows' order, whichever it is. 8192 rows x 500 statistics: 34 us; few rows
+// take 6, a chain of waits for memory.
 constexpr int kJoinThreads = 1024, kJoinRows = 16;
 __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Targets t) {
   __shared__ float2 part[kJoinThreads / 64][kJoinRows];
@@ -1359,6 +1370,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
 }
 
 // exp(z - m) -> c p, in place for bf16, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
+// Bound by memory: 8192 x 128000 in bf16, 2.1 GB each way, take 767 us, 5.6 TB/s.
 constexpr int kNormThreads = 256, kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
   constexpr int kBlocks = kNormCols / 64;  // no statistic covers fewer columns
@@ -1445,7 +1457,7 @@ template <int DT> __global__ __launch_bounds__(256) void k_vocab_own(Soft a, End
   }
 }
 
-// Partial gradients [splits][n][Hp] joined in order, into the outputs.
+// Partial gradients [splits][n][Hp] joined in order, into the outputs. Bound by memory: 67 MB into 8 in 14 us, 5.3 TB/s.
 template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Product a) {
   const int n_end = DIR == S_WEIGHT ? a.Vp : chunk_active(a), per = a.Hp / 4;
   const int64_t all = int64_t(n_end) * per;
@@ -1490,7 +1502,8 @@ enum Size { Z_S = 0, Z_M = 1, Z_L = 2, Z_F = 3 };
 constexpr int64_t kChunkBytes = int64_t(4) << 30;
 constexpr int kUnits = 256;  // compute units
 // Hidden elements that the first launch's one workgroup packs itself rather than leaving them to another launch.
-constexpr int64_t kFewElements = 32768;
+// (us a loss, so and with the launch: 16 x 64 fp32 27.2 and 28.2, 8 x 2048 bf16 46.6 and 42.6, 48 x 256 31.6 and 27.0.)
+constexpr int64_t kFewElements = 4096;
 
 struct Plan {
   int planes, Hp, Kp;  // Kp: ids of a row, whole vectors of them
@@ -1510,12 +1523,17 @@ int64_t tiles_of(Size z, int64_t m, int64_t n) {
   return ((m + bm - 1) / bm) * ((n + bn - 1) / bn);
 }
 
+// Large tiles read each operand half as often as middle ones, but where they are half empty, or fewer than the compute
+// units, the middle ones win (us a bf16 loss of width 2048 in large and in middle tiles: 100 rows x 98304 168 and 125;
+// 256 rows x 16384, 64 large tiles, 67 and 47, x 32768 70 and 66, x 49152, 192 of them, 73 and 83, x 98304 154 and 174).
 Size size_for(int64_t m, int64_t n, int64_t splits) {
   if (n <= kFewRows) return Z_S;
+  if (n <= 128) return Z_M;
   return tiles_of(Z_L, m, n) * splits >= kUnits * 3 / 4 ? Z_L : Z_M;
 }
 
-// How often a product's depth is split so that its tiles fill the device.
+// How often a product's depth is split so that its tiles fill the device (us a call with gradients, so and unsplit:
+// 8 x 2048 x 32000 122 and 276, 1024 x 1024 x 32000 288 and 804, 48 x 256 x 1000 50 and 53).
 int splits_for(int64_t tiles, int64_t steps, int64_t part_bytes) {
   const int64_t want = (2 * kUnits) / std::max<int64_t>(tiles, 1), most = std::min<int64_t>(steps / 4, (int64_t(256) << 20) / std::max<int64_t>(part_bytes, 1));
   return int(std::max<int64_t>(1, std::min(want, most)));
