@@ -307,8 +307,9 @@ def _vocab(hidden, weight, ids, logits, reduction, ignore_index, temperature, to
             raise _invalid("teacher logits must be a float32 or bfloat16 matrix of at least one column")
         at, lld = _rows(torch, logits, "teacher logits", logits.dtype, index)
         kw = dict(top=shape[1], logits=at, logits_ld=lld, logits_dtype=_TYPES[logits.dtype], ids_ld=ids.stride(0))
-    if token_weights is not None and (token_weights.dtype != torch.float32 or token_weights.get_device() != index
-                                      or tuple(token_weights.shape) != (T,) or not token_weights.is_contiguous()):
+    w = token_weights
+    if w is not None and (not isinstance(w, torch.Tensor) or w.dtype != torch.float32 or w.get_device() != index
+                          or tuple(w.shape) != (T,) or not w.is_contiguous()):
         raise _invalid("token_weights must be contiguous float32, one a token, on hidden's device")
     if reduction not in REDUCTIONS:
         raise _invalid(f"reduction must be one of {', '.join(REDUCTIONS)}")

@@ -425,6 +425,7 @@ def test_refused_in_python():
         lambda: A.vocab_loss(h, w.t().contiguous().t(), y), lambda: A.vocab_loss(h, w, y, reduction="average"),
         lambda: A.vocab_loss(h, w, y, temperature=0.0), lambda: A.vocab_loss(h, w, y, token_weights=torch.ones(9, device="cuda")),
         lambda: A.vocab_loss(h, w, y, token_weights=torch.ones(10, device="cuda").double()), lambda: A.vocab_loss(h, [], y),
+        lambda: A.vocab_loss(h, w, y, token_weights=[1.0] * 10),
         lambda: A.vocab_loss(h[:, :0], w[:, :0], y), lambda: A.vocab_loss(h[:1].expand(10, 16), w, y),
         lambda: A.vocab_loss(h[0], w, y), lambda: A.vocab_loss(h, w[:0], y),
         lambda: A.vocab_loss_grad(h, w, y, out_hidden=h), lambda: A.vocab_loss_grad(h, w, y, out_weight=w),
@@ -558,3 +559,17 @@ def test_an_output_matrix_of_more_than_2_31_elements():
         want_h += q @ part.double()
         size += (q.abs() * (2.02 * ov.U_BF16 + 0.02)) @ part.double().abs()
     within(dh, want_h, size + ov.U_BF16 * want_h.abs(), "d_hidden")
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_the_largest_vocabulary_with_lists_of_ids(dtype):
+    """As many tiles of logits as there can be, whose ids are sorted."""
+    Case(3, 16, [1 << 19, 1 << 18, 1 << 18], dtype, top=6, seed=33).check()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("T", [8, 9, 33, 64, 127, 128])
+def test_rows_around_the_changes_of_kernel(dtype, T):
+    """Rows packed by the first launch or their own, and up to 64 and 128 rows' tiles."""
+    Case(T, 512, [700, 900], dtype, seed=34, left_out=0.2).check()
+    Case(T, 511, [700, 900], dtype, top=5, seed=35, left_out=0.2).check()
