@@ -22,8 +22,8 @@
 // a row's lse is known, one pass turns them into D. Nothing is added atomically: the
 // same sizes give the same bits on every run.
 //
-// 8192 tokens x 4096 x 128000 in bf16, 8 pieces, with gradients: 21.9 ms, of which products 7.06 + 6.71 + 7.15
-// (1216, 1281 and 1201 TFLOP/s), D 0.77, the rest 0.08.
+// 8192 tokens x 4096 x 128000 in bf16, 8 pieces, with gradients: 21.1 ms, of which products 6.85 + 6.38 + 6.95
+// (1254, 1346 and 1235 TFLOP/s), D 0.77, the rest 0.08.
 #include "vocab.h"
 
 #include <hip/hip_ext.h>
@@ -334,7 +334,7 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
 
 // More ids a row than kFewIds are sorted by the tile of logits that they lie in, so that a tile finds its own: one
 // workgroup for the rows of a tile counts them, adds the counts up and deals the entries out. (Where an entry lies
-// among its tile's does not show in any result.) 3687 rows x 64 ids: 22 us, after which the logits of 50000 take 888;
+// among its tile's does not show in any result.) 3687 rows x 64 ids: 22 us, after which the logits of 50000 took 887;
 // with tiles that compare all of their rows' ids, 1176.
 constexpr int kFewIds = 4, kSortThreads = 1024;
 __global__ __launch_bounds__(kSortThreads) void k_vocab_sort(const int32_t* idt, int ld_idt, int bn, int bm, int mtiles, int64_t row_tiles, const Counts* counts, int32_t* starts, uint32_t* entries) {
@@ -940,11 +940,11 @@ template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradie
 
 // KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
 // the outputs' type.
-// Bound by power where tiles are many: at 8192 x 4096 x 128000 the matrix pipes are busy for 65-72% of the time, the
-// clock at 1.7-1.8 GHz, 1200-1280 TFLOP/s (on zeros, 2.3 GHz at the same share). 256 x 256 outputs for 8 waves are
+// Bound by power where tiles are many: at 8192 x 4096 x 128000 the matrix pipes are busy for 64-72% of the time, the
+// clock at 1.8-1.9 GHz, 1235-1346 TFLOP/s (on zeros, 2.3 GHz at the same share). 256 x 256 outputs for 8 waves are
 // what the accumulators hold: each slice's 32 KB are read into LDS for 4.2 MFLOP. With 64 deep double buffers the three
-// took 7.8, 9.2 and 9.3 ms in place of 7.1, 6.7 and 7.2; in 32 x 32 x 16 products 2-8% more than in 16 x 16 x 32.
-// Of up to 64 rows the reading of the output matrix bounds it: 8 x 2048 x 32000 in 25 us, 5.4 TB/s.
+// took 7.8, 9.2 and 9.3 ms in place of 6.8, 6.4 and 7.0; in 32 x 32 x 16 products 2-8% more than in 16 x 16 x 32.
+// Of up to 64 rows the reading of the output matrix bounds it: 8 x 2048 x 32000 in 25 us, 5.3 TB/s.
 template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
   __shared__ __attribute__((aligned(512))) char shared[C::kStages * C::kStage];
   using St = Stager<C, DIR>;

@@ -418,19 +418,19 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
  *    (>= V; for cross entropy also a negative one that is not `ignore`) makes its row's loss, and so the
  *    call's, NaN, and gives no gradient.
  *  - Precision: logits, softmax and losses are fp32 (a call's loss is summed in 64 bits). bf16: products of the
- *    bf16 operands are exact and their sums fp32; d is rounded to bf16 once before the gradients'
- *    products (p before that to 2^-11 of it, or 2^-39 of the row's largest p), whose fp32 sums are rounded to bf16. fp32: operands are split into three bf16 terms
- *    (which hold all their bits down to 2^-133) and six products of them summed, 2^-24 or so of a product. Values
- *    below 2^-126 on the way may be lost. The order of every sum is fixed by the sizes, the alignment and the number
- *    of rows that take part, so a call gives the same bits on every run.
+ *    bf16 operands are exact and their sums fp32; d is rounded to bf16 once before the gradients' products (p before
+ *    that to 2^-11 of it, or 2^-39 of the row's largest p), whose fp32 sums are rounded to bf16. fp32: operands are
+ *    split into three bf16 terms (which hold all their bits down to 2^-133) and six products of them summed, 2^-24
+ *    or so of a product. Values below 2^-126 on the way may be lost. The order of every sum is fixed by the sizes,
+ *    the alignment and the number of rows that take part, so a call gives the same bits on every run.
  *  - Stream, errors, capture: as for the gradient calls. The tables of pieces travel as kernel arguments.
  *  - Workspace: device scratch of ar_vocab_workspace_bytes() bytes, 16-byte aligned, contents unprepared. It is
  *    bounded in T but for the gathered hidden states (logits are worked on 4 GiB at a time), and the library keeps
  *    none of its own for these calls: NULL is too small.
  *  - Memory: rows are contiguous, ld apart (>= their length), at any address that is a multiple of the element
- *    size; 16-byte aligned rows of bf16 with H and ld multiples of 8 are read in place, others are first copied into
- *    the workspace. What a call writes (loss, dh, dw, workspace) must not overlap, first to last element, anything
- *    else of it.
+ *    size. 16-byte aligned pieces of bf16 with H and ld multiples of 8 are read in place, and so is every piece where
+ *    T <= 64 and H >= 8; others are first copied into the workspace as bf16 terms. What a call writes (loss, dh, dw,
+ *    workspace) must not overlap, first to last element, anything else of it.
  *  - Limits: T < 2^30, H <= 65536, top <= 1024, P <= AR_MAX_RANKS, and V with every piece rounded up to a
  *    multiple of 256 rows at most 2^20. */
 typedef enum { AR_MEAN = 0, AR_TOTAL = 1, AR_NONE = 2 } ar_reduction;
