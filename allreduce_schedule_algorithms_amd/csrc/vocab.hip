@@ -892,7 +892,8 @@ template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Pr
       float s = 0;
 #pragma unroll
       for (int w = 0; w < C::WM; ++w) s += sum[w * C::BN + n];
-      a.stats[int64_t(at.m0 / C::BM) * a.ld_stats + at.n0 + n] = float2{mx[j], s};
+      // a sum of 0 is a tile without a logit: its largest is no value that may pass the row's
+      a.stats[int64_t(at.m0 / C::BM) * a.ld_stats + at.n0 + n] = float2{s == 0 ? -INFINITY : mx[j], s};
     }
 }
 

@@ -573,3 +573,43 @@ def test_rows_around_the_changes_of_kernel(dtype, T):
     """Rows packed by the first launch or their own, and up to 64 and 128 rows' tiles."""
     Case(T, 512, [700, 900], dtype, seed=34, left_out=0.2).check()
     Case(T, 511, [700, 900], dtype, top=5, seed=35, left_out=0.2).check()
+
+
+def shifted(c, by):
+    """The same case with all of its logits moved by `by` (over the temperature), through the last column."""
+    c.hidden[:, -1] = 1
+    for w in c.weight:
+        w[:, -1] = by
+    return c
+
+
+@pytest.mark.parametrize("by", [-200.0, 200.0])
+@pytest.mark.parametrize("top", [0, 3, 6])
+@pytest.mark.parametrize("T", [16, 50, 100, 300])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_logits_far_from_zero(dtype, T, top, by):
+    """A softmax does not know of a shift: neither may the tiles that lie behind a piece's rows, of 64, 128 or 256 rows."""
+    for pieces in ([100], [300], [41, 300], [65, 0, 1]):
+        shifted(Case(T, 40, pieces, dtype, top, seed=36, left_out=0.1), by).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_logits_far_from_zero_over_many_tiles(dtype):
+    shifted(Case(100, 64, [50257], dtype, top=3, seed=37, temperature=0.5), -60.0).check()
+
+
+def test_a_tile_whose_logits_are_all_minus_infinity():
+    """Rows of W that hold -infinity (the next smallest logits are below -89): no share of the distribution."""
+    torch = torch_mod()
+    for T in (20, 200):
+        c = shifted(Case(T, 40, [400], seed=38, reduction="none"), -200.0)
+        c.hidden[:, 0] = 1
+        c.ids.fill_(7)
+        want = lib().vocab_loss_grad(c.hidden, c.weight[0][:128], c.ids, "none")
+        c.weight[0][128:, 0] = -math.inf
+        loss, _, dw = c.run()
+        torch.cuda.synchronize()
+        # the same logits in other tiles, or in other sums: within twice the bound of the one
+        bound = ov.loss_and_gradients(c.hidden, c.weight[0][:128], c.ids, reduction="none", dtype="bf16")
+        assert bool(((loss - want[0]).abs() <= 2 * bound[3]).all())
+        assert bool(((dw[0][:128] - want[2]).abs() <= 2 * bound[5]).all()) and not bool(dw[0][128:].any())
