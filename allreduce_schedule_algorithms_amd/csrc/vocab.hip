@@ -48,7 +48,7 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 constexpr int kBK = 32;         // depth of a slice: one product's, 64 bytes of a row
 constexpr int kPieceTab = 64;   // pieces that one launch's arguments carry
 constexpr int kUnit = 256;      // pieces and token chunks are padded to this many rows
-constexpr float kLn2 = 0.69314718055994530942f;  // softmax statistics are in units of it
+constexpr float kLn2 = 0.69314718055994530942f;  // logs are in units of it
 
 // One piece as the kernels see it, in the workspace. `first`: its first row in the vocabulary; `start`: the same
 // with every piece padded to kUnit rows, the coordinate that tiles, D and the ids' table use.
@@ -459,11 +459,11 @@ struct Product {
   char* d;                    // [rows][planes * Vp]: (bf16) exp(z - m) in fp16, then D
   // logits
   float scale;  // log2(e) / temperature
-  float2* stats;  // [Vp / BM][ld_stats]
+  float2* stats;  // [Vp / BM][ld_stats]: a tile's largest product, the sum of 2^((product - largest) scale)
   int64_t ld_stats;
   const int32_t* idt;  // [rows][ld_idt], as zt
   int32_t ld_idt;
-  float* zt;  // the logits at those ids, times log2(e)
+  float* zt;  // the products at those ids
   const int32_t* starts;    // more than kFewIds: where each tile's entries begin, [row tiles][mtiles + 1]
   const uint32_t* entries;  // [row tiles][BN ids], m | n << 8 | k << 16 within the tile
   int32_t entries_ld;
@@ -792,8 +792,10 @@ template <class C> __device__ __forceinline__ Own own_of(const Product& a, const
 // logits at the rows' own ids put away.
 template <class C> __device__ __forceinline__ void pick_own(const Product& a, f32x4 (&acc)[C::FM][C::FN], const Place& at, const Own& own, int piece_left, Wave wave) {
   const int wm = wave.m, wn = wave.n, lane = wave.lane, wn0 = at.n0 + wn * C::NW;
-  // Everything is in units of log 2 from here on: x = z log2(e) is one product with the sum, and 2^(x - m) one
-  // more operation. (a.scale carries a rounding of 2^-24 of x, the same for all.)
+  // Products stay as they are, without the temperature, until two of them have been subtracted: the difference to the
+  // largest is exact next to it (its own is 0), where a rounding of 2^-24 of each logit would be one of the exponent
+  // (one target's probability of 1 off by 1e-4 at logits of 1500; infinite exponentials from 2^26 on). Times a.scale,
+  // whose rounding then is one of 2^-24 of the difference, it is the exponent of 2.
   if (piece_left < C::BM) {
     const int left = piece_left - wm * C::MW - lane / 16 * 4;
 #pragma unroll
@@ -819,7 +821,7 @@ template <class C> __device__ __forceinline__ void pick_own(const Product& a, f3
             if (row / 16 == i) x = acc[i][j];
         }
       const float v = row % 4 == 0 ? x[0] : row % 4 == 1 ? x[1] : row % 4 == 2 ? x[2] : x[3];
-      if (lane == row % 16 / 4 * 16 + col % 16) a.zt[int64_t(wn0 + col) * a.ld_idt + which] = v * a.scale;
+      if (lane == row % 16 / 4 * 16 + col % 16) a.zt[int64_t(wn0 + col) * a.ld_idt + which] = v;
     }
   };
   if (a.ld_idt <= kFewIds) {
@@ -866,14 +868,14 @@ template <class C, int KEEP> __device__ __forceinline__ void put_logits(const Pr
     float m = -INFINITY;
 #pragma unroll
     for (int w = 0; w < C::WM; ++w) m = fmaxf(m, top[w * C::BN + wn * C::NW + j * 16 + lane % 16]);
-    mx[j] = m == -INFINITY ? 0.f : m * a.scale;  // a tile without rows of the vocabulary: exponentials of 0
+    mx[j] = m == -INFINITY ? 0.f : m;  // a tile without rows of the vocabulary: exponentials of 0
     float s = 0;
     const int64_t row = int64_t(wn0 + j * 16 + lane % 16) * a.Vp + wm0;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], a.scale, -mx[j]));
+        acc[i][j][e] = __builtin_amdgcn_exp2f((acc[i][j][e] - mx[j]) * a.scale);
         s += acc[i][j][e];
       }
       if constexpr (KEEP == D_BF16)
@@ -1220,8 +1222,8 @@ struct Soft {
   int32_t blocks, chunk, chunk_rows, reduction;
   int32_t planes, block;  // block: columns a statistic covers
   int64_t Vp;
-  float temperature;
-  float2* lse;   // [chunk rows] in two parts: the largest logit, the log of the sum around it (their sum would round
+  float temperature, scale;  // scale: log2(e) / temperature
+  float2* lse;   // [chunk rows] in two parts: the largest product, the log of the sum around it (their sum would round
                  // p by 2^-24 of the logit)
   float* coef;   // [chunk rows]: the row's weight in the loss over the temperature; 0 behind the rows
   float* exps;   // fp32: exp(z - m)
@@ -1269,10 +1271,10 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
   for (int r0 = blockIdx.x * kJoinRows; r0 < end; r0 += gridDim.x * kJoinRows) {
     const int r = r0 + row;
     float m = -INFINITY, s = 0;
-    const auto join = [](float& m, float& s, float om, float os) {
+    const auto join = [&](float& m, float& s, float om, float os) {
       if (os == 0) return;
       const float top = fmaxf(m, om);  // a NaN sum stays one
-      s = (m == top ? s : s * exp2f(m - top)) + (om == top ? os : os * exp2f(om - top));
+      s = (m == top ? s : s * exp2f((m - top) * a.scale)) + (om == top ? os : os * exp2f((om - top) * a.scale));
       m = top;
     };
     const auto join_lanes = [&](float& m, float& s) {
@@ -1321,7 +1323,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
         if (e.idt[(a.chunk + i) * int64_t(e.ld_idt) + k] < 0) continue;
         float x;
         const float q = teacher.q(k, &x);
-        if (q != 0) loss += q * ((t.K ? x - logf(teacher.stat.y) : 0.f) + ((row_lse[wave].x - e.zt[int64_t(i) * e.ld_idt + k]) + row_lse[wave].y) * kLn2);
+        if (q != 0) loss += q * ((t.K ? x - logf(teacher.stat.y) : 0.f) + ((row_lse[wave].x - e.zt[int64_t(i) * e.ld_idt + k]) * a.scale + row_lse[wave].y) * kLn2);
       }
 #pragma unroll
       for (int d = 32; d; d >>= 1) loss += __shfl_xor(loss, d);
@@ -1358,7 +1360,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
 
 // D at an id of a row: c (p - q), q the sum over the row's equal ids.
 template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const Ends& e, int i, int k, int32_t id, float q) {
-  const float d = a.coef[i] * (exp2f((e.zt[int64_t(i) * e.ld_idt + k] - a.lse[i].x) - a.lse[i].y) - q);
+  const float d = a.coef[i] * (exp2f((e.zt[int64_t(i) * e.ld_idt + k] - a.lse[i].x) * a.scale - a.lse[i].y) - q);
   __bf16* row = reinterpret_cast<__bf16*>(a.d) + int64_t(i) * (DT == D_BF16 ? 1 : 3) * a.Vp;
   if constexpr (DT == D_BF16) {
     row[id] = __bf16(d);
@@ -1389,7 +1391,7 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
       const int64_t c = c0 + b * 64;
       float f = 0;
       const float w = b < kBlocks ? a.coef[r0 + r] : 0.f;
-      if (w != 0 && c < a.Vp) f = exp2f((a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r].x) - a.lse[r0 + r].y) * w;
+      if (w != 0 && c < a.Vp) f = exp2f((a.stats[c / a.block * a.ld_stats + r0 + r].x - a.lse[r0 + r].x) * a.scale - a.lse[r0 + r].y) * w;
       if (b < kBlocks) factor[r][b] = DT == D_BF16 ? f / kKept : f;
     }
     __syncthreads();
@@ -1682,7 +1684,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.dh = v.dh;
   a.dh_ld = v.dh_ld;
   Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
-         v.temperature, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
+         v.temperature, a.scale, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
   const auto rows_of = [&](int64_t c) { return std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)); };
   const auto join_blocks = [&](int64_t n) { return blocks_of(int64_t(up(size_t(n), kUnit)) / kJoinRows); };
   Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, each ? nullptr : v.loss, 0};

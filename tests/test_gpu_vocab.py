@@ -613,3 +613,61 @@ def test_a_tile_whose_logits_are_all_minus_infinity():
         bound = ov.loss_and_gradients(c.hidden, c.weight[0][:128], c.ids, reduction="none", dtype="bf16")
         assert bool(((loss - want[0]).abs() <= 2 * bound[3]).all())
         assert bool(((dw[0][:128] - want[2]).abs() <= 2 * bound[5]).all()) and not bool(dw[0][128:].any())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("scale,temperature", [(1e8, 1.0), (1e10, 1.0), (3e12, 1.0), (1.0, 1e-7), (60.0, 1e-9)])
+@pytest.mark.parametrize("T,top", [(60, 0), (60, 6), (200, 3)])
+def test_logits_of_any_size(dtype, scale, temperature, T, top):
+    """The exponent of a row's largest is 0, whatever rounding its logit takes on."""
+    Case(T, 40, [500], dtype, top, seed=39, scale=scale, temperature=temperature).check()
+
+
+@pytest.mark.parametrize("top", [0, 1, 6])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_target_far_ahead(dtype, top):
+    """Logits near 1500 whose largest, the target's, leads by more than 200: the others' exponentials, below 2^-288,
+    are 0 in fp32, the sum around the largest 1, and loss and gradients 0 to the last bit."""
+    torch = torch_mod()
+    for T in (50, 200):
+        c = Case(T, 40, [700], dtype, top, seed=40, reduction="sum")
+        c.weight[0].mul_(1e-3)
+        c.weight[0][:, 0] = 120 + torch.rand(700, generator=torch.Generator(device="cuda").manual_seed(41), device="cuda")
+        c.hidden[:, 0] = 9 + torch.rand(T, generator=torch.Generator(device="cuda").manual_seed(42), device="cuda")
+        c.weight[0][321, 0] = 151.3
+        c.ids.fill_(-1 if top else 321)
+        if top:
+            c.ids[:, 0] = 321
+        loss, dh, dw = c.run()
+        assert float(c.run(False)) == 0 and float(loss) == 0 and not bool(dh.any()) and not bool(dw[0].any())
+
+
+@pytest.mark.parametrize("T", [5, 50, 200])
+@pytest.mark.parametrize("top", [0, 6])
+def test_close_logits_far_from_zero(T, top):
+    """Logits 1472 + v % 8, 1487 at v = 77, that every sum holds exactly (64 times 23 + v % 8 / 64, all other products
+    0): the roundings that are left are the softmax's own, of differences of at most 15. An exponential's argument (two
+    roundings of at most 22 in units of log 2), itself, and its place in a sum (a lane's 32, its neighbours', 3 tiles:
+    under 48 levels) are off by (2 * 22 + 4 + 48) U of p, a teacher's probability by as much, D by 8 U more; dW = 64
+    sum D adds 6 T + 64 roundings (six products, five of them zeros), dh of 300 terms 6 * 300 + 64."""
+    torch = torch_mod()
+    c = Case(T, 40, [300], "fp32", top, seed=43, reduction="sum", temperature=1.0)
+    c.hidden.zero_()
+    c.hidden[:, 5] = 64
+    c.weight[0].zero_()
+    c.weight[0][:, 5] = 23 + torch.arange(300, device="cuda") % 8 / 64
+    c.weight[0][77, 5] = 23 + 15 / 64
+    if top:
+        c.ids[:, 0] = 77
+    else:
+        c.ids[:] = 77
+    loss, dh, dw = c.run()
+    want = c.want(False)
+    W, h = c.weight[0].double(), c.hidden.double()
+    p = torch.softmax(h @ W.t(), 1)
+    ids = c.ids.reshape(T, -1)
+    q = torch.zeros_like(p).scatter_add_(1, ids.clamp(min=0), (ids >= 0).double())  # at least the target's or teacher's
+    dD = 104 * ov.U * (p + q)
+    assert abs(float(loss) - float(want[0])) <= T * 15 * 2 * 104 * ov.U
+    within(dw[0], want[2], dD.t() @ h + (6 * T + 64) * ov.U * ((p + q).t() @ h) + 2.0 ** -120, "d_weight")
+    within(dh, want[1], dD @ W + (6 * 300 + 64) * ov.U * ((p + q) @ W) + 2.0 ** -120, "d_hidden")
