@@ -141,7 +141,8 @@ struct Targets {
   float temperature;
 };
 
-// Distillation: a wave per row finds the teacher's largest logit and the sum of exp around it.
+// Distillation: a wave per row finds the teacher's largest logit and the sum of exp around it. Logits are divided by the
+// temperature as differences to the largest: their own quotients may pass the largest fp32 value.
 constexpr int kRowWaves = 4;
 __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int64_t T, float2* stat, uint8_t* flags) {
   const int lane = threadIdx.x & 63;
@@ -152,7 +153,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int
       const int64_t id = id_at(t.ids, t.wide, r * t.ids_ld + k);
       if (id < 0) continue;
       bad |= id >= t.V;
-      const float x = logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) / t.temperature;
+      const float x = logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k);
       nan |= x != x;
       top = fmaxf(top, x);
     }
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int
     float sum = 0;
     for (int k = lane; k < t.K; k += 64)
       if (id_at(t.ids, t.wide, r * t.ids_ld + k) >= 0)
-        sum += expf(logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) / t.temperature - top);
+        sum += expf((logit_at(t.logits, t.logits_dtype, r * t.logits_ld + k) - top) / t.temperature);
 #pragma unroll
     for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
     if (lane == 0) {
@@ -1242,7 +1243,8 @@ struct Ends {
   uint32_t joins;   // workgroups of all joins together
 };
 
-// The teacher's probability of a row's entry (1 for the one target), and x = its logit less the row's largest.
+// The teacher's probability of a row's entry (1 for the one target), and x = its logit less the row's largest, over
+// the temperature.
 struct Teacher {
   const Targets& t;
   int64_t row;
@@ -1250,7 +1252,7 @@ struct Teacher {
   __device__ __forceinline__ float q(int k, float* x) const {
     *x = 0;
     if (!t.K) return 1.f;
-    *x = logit_at(t.logits, t.logits_dtype, row * t.logits_ld + k) / t.temperature - stat.x;
+    *x = (logit_at(t.logits, t.logits_dtype, row * t.logits_ld + k) - stat.x) / t.temperature;
     return expf(*x) / stat.y;
   }
 };

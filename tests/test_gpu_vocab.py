@@ -671,3 +671,17 @@ def test_close_logits_far_from_zero(T, top):
     assert abs(float(loss) - float(want[0])) <= T * 15 * 2 * 104 * ov.U
     within(dw[0], want[2], dD.t() @ h + (6 * T + 64) * ov.U * ((p + q).t() @ h) + 2.0 ** -120, "d_weight")
     within(dh, want[1], dD @ W + (6 * 300 + 64) * ov.U * ((p + q) @ W) + 2.0 ** -120, "d_hidden")
+
+
+@pytest.mark.parametrize("top", [3, 6])
+@pytest.mark.parametrize("T", [4, 200])
+def test_a_teachers_logits_over_a_small_temperature(T, top):
+    """Their quotients lie past the largest fp32 value, their differences' exponentials do not."""
+    torch = torch_mod()
+    c = Case(T, 40, [200], "fp32", top, seed=44, temperature=1e-37)
+    c.hidden.zero_()
+    c.ids = (torch.arange(T, device="cuda")[:, None] * 7 + torch.arange(top, device="cuda")) % 200
+    c.logits[:] = 300 - 90.0 * torch.arange(top, device="cuda")
+    c.logits[1, 0] = c.logits[1, 1]
+    loss, dh, _ = c.check()
+    assert math.isfinite(float(loss)) and bool(dh.any())
