@@ -1306,9 +1306,9 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
       float coef = 0;
       if (r < active) {
         lse = float2{m, log2f(s)};
-        coef = 1.f / a.temperature;
-        if (a.weights) coef *= a.weights[a.rows[a.chunk + r]];
-        if (a.reduction == R_MEAN) coef /= float(a.counts->mean);
+        // in 64 bits: a weight over a small temperature may pass the largest fp32 value where its share of the mean does not
+        const double w = a.weights ? a.weights[a.rows[a.chunk + r]] : 1.f, n = a.reduction == R_MEAN ? a.counts->mean : 1;
+        coef = float(w / (double(a.temperature) * n));
       }
       if (lane < 16) {
         a.lse[r] = row_lse[row] = lse;

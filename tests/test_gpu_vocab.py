@@ -685,3 +685,17 @@ def test_a_teachers_logits_over_a_small_temperature(T, top):
     c.logits[1, 0] = c.logits[1, 1]
     loss, dh, _ = c.check()
     assert math.isfinite(float(loss)) and bool(dh.any())
+
+
+@pytest.mark.parametrize("T", [2, 200])
+def test_a_weight_over_a_small_temperature(T):
+    """A row's weight over the temperature may pass the largest fp32 value before it is divided by the rows."""
+    torch = torch_mod()
+    c = Case(T, 40, [200], "fp32", seed=45, temperature=1e-38, token_weights=torch.full((T,), 8.0, device="cuda"))
+    c.hidden.zero_()
+    for w in c.weight:
+        w.mul_(1e-3)
+    if T == 2:
+        c.kw["token_weights"].fill_(4.0)
+    loss, dh, dw = c.check()
+    assert math.isfinite(float(loss)) and bool(dh.any()) and bool(torch.isfinite(dh).all())
