@@ -281,8 +281,8 @@ ar_status check_vocab(const ar_vocab* c, bool grad, bool run, ar::Vocab* out) {
   if (!is_float(c->dtype)) return bad("dtype must be AR_FP32 or AR_BF16");
   if (c->P < 1 || c->P > AR_MAX_RANKS) return bad("P must be in [1, " + std::to_string(AR_MAX_RANKS) + "]");
   if (!c->pieces) return bad("pieces is NULL");
-  if (!(c->temperature > 0) || !std::isfinite(c->temperature) || !std::isfinite(1.f / c->temperature))
-    return bad("temperature must be positive and finite, and its reciprocal too");
+  if (!(c->temperature > 0) || !std::isfinite(c->temperature) || !std::isfinite(float(ar::kLog2e / double(c->temperature))))
+    return bad("temperature must be positive and finite, and log2(e) over it too");
   if (c->reduction < AR_MEAN || c->reduction > AR_NONE) return bad("unknown reduction");
   if (c->top < 0 || c->top > 1024) return bad("top must be in [0, 1024]");
   if (c->ids_bytes != 4 && c->ids_bytes != 8) return bad("ids_bytes must be 4 or 8");

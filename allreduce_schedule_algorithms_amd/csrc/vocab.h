@@ -7,6 +7,8 @@
 
 namespace ar {
 
+constexpr double kLog2e = 1.4426950408889634;  // exponentials are powers of 2: of logits times this
+
 enum Reduction : int32_t { R_MEAN = 0, R_SUM = 1, R_NONE = 2 };
 
 // One rank's rows of the output matrix, and where their gradient goes.

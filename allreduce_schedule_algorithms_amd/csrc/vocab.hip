@@ -1673,7 +1673,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.kend = p.packed ? p.Hp : int32_t(v.H);  // (few rows' products go by H)
   a.hp = ws + p.hp;
   a.d = ws + p.d;
-  a.scale = float(1.4426950408889634 / double(v.temperature));
+  a.scale = float(kLog2e / double(v.temperature));
   a.stats = reinterpret_cast<float2*>(ws + p.stats);
   a.ld_stats = p.Tc;
   a.idt = pa.idt;

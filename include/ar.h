@@ -452,7 +452,7 @@ typedef struct ar_vocab {
   const void* hidden;
   int64_t ld;
   const ar_vocab_piece* pieces; /* host array of P */
-  float temperature;            /* > 0, finite */
+  float temperature;            /* > 0, finite, and log2(e) / temperature too: from 4.24e-39 on */
   int32_t reduction;            /* ar_reduction */
   const float* token_weights;   /* device, T of them, or NULL: 1 */
   int32_t top;                  /* 0: cross entropy with targets ids[T]; K: distillation with ids [T, K] */

@@ -211,3 +211,16 @@ def test_a_mistake_in_the_oracle_shows(top):
     assert float((wrong[0] - loss).abs()) > float(bl)
     assert bool(((wrong[1] - dh).abs() > bh)[kept].any(1).all())
     assert bool(((wrong[2] - dw).abs() > bw).any())
+
+
+def test_a_temperature_whose_scale_is_infinite():
+    """Logits are scaled by log2(e) / temperature: past the largest fp32 value it would make the difference of equal
+    logits, 0, a NaN. 4.24e-39 is the smallest temperature that it does not."""
+    largest = torch.finfo(torch.float32).max
+    for t, fine in ((3e-39, False), (4.23e-39, False), (4.25e-39, True), (1e-38, True)):
+        assert (float(torch.tensor(math.log2(math.e) / t, dtype=torch.float64)) <= largest) == fine
+        if fine:
+            assert A.ar_vocab_workspace_bytes(call(temperature=t), True) > 0
+        else:
+            assert all("log2(e)" in message for message in both(call(temperature=t)))
+            refused(lambda: A.ar_vocab_workspace_bytes(call(temperature=t), False))
