@@ -1499,7 +1499,8 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
 // host
 // ----------------------------------------------------------------------------
 size_t up(size_t n, size_t unit = 256) { return (n + unit - 1) / unit * unit; }
-int64_t blocks_of(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(n, std::min<int64_t>(launch_blocks(), int64_t(1) << 22))); }
+// Workgroups of a launch: a dispatch's work-items are a 32-bit number, and some workgroups have 1024.
+int64_t blocks_of(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(n, std::min<int64_t>(launch_blocks(), int64_t(1) << 21))); }
 
 enum Size { Z_S = 0, Z_M = 1, Z_L = 2, Z_F = 3 };
 
@@ -1659,7 +1660,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   if (!pack_first) s.launch(k_vocab_pack<DT>, blocks_of(row_blocks), kRowWaves * 64, pa, t);
   if (sorted) {
     const int64_t row_tiles = p.Tpad / p.tile_rows;
-    s.launch_lds(k_vocab_sort, std::min<int64_t>(row_tiles, launch_blocks()), kSortThreads, size_t(p.Vp / p.block + 1) * 4, pa.idt, p.Kp, p.tile_rows, p.block,
+    s.launch_lds(k_vocab_sort, blocks_of(row_tiles), kSortThreads, size_t(p.Vp / p.block + 1) * 4, pa.idt, p.Kp, p.tile_rows, p.block,
                  int(p.Vp / p.block), row_tiles, counts, reinterpret_cast<int32_t*>(ws + p.starts), reinterpret_cast<uint32_t*>(ws + p.entries));
   }
   Product a{};

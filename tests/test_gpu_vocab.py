@@ -699,3 +699,28 @@ def test_a_weight_over_a_small_temperature(T):
         c.kw["token_weights"].fill_(4.0)
     loss, dh, dw = c.check()
     assert math.isfinite(float(loss)) and bool(dh.any()) and bool(torch.isfinite(dh).all())
+
+
+def test_more_tokens_than_a_launch_has_workgroups_for():
+    """2^26 rows and a few, 16 to a workgroup of 1024 that joins: 2^32 work-items, one more than a launch may have.
+    Products of small whole numbers are exact, so a loss is off by its softmax and its own operations only."""
+    torch = torch_mod()
+    T, H = (1 << 26) + 3, 8
+    g = torch.Generator(device="cuda").manual_seed(48)
+    h = torch.randint(-2, 3, (T, H), generator=g, device="cuda", dtype=torch.int8).bfloat16()
+    w = torch.randint(-2, 3, (2, H), generator=g, device="cuda").bfloat16()
+    y = torch.randint(0, 2, (T,), generator=g, device="cuda", dtype=torch.int32)
+    y[::5] = -100
+    each, total = lib().vocab_loss(h, w, y, "none"), lib().vocab_loss(h, w, y, "sum")
+    sums = [0.0, 0.0]
+    for r in torch.arange(T, device="cuda").split(1 << 24):
+        z = h[r].double() @ w.double().t()
+        lse = torch.logsumexp(z, 1)
+        kept = y[r] >= 0
+        zt = z.gather(1, y[r].long().clamp(min=0)[:, None])[:, 0]
+        want = torch.where(kept, lse - zt, torch.zeros_like(lse))
+        bound = torch.where(kept, (280 + 24 * (lse.abs() + zt.abs())) * ov.U, torch.zeros_like(lse))
+        within(each[r], want, bound, "loss")
+        sums[0] += float(want.sum())
+        sums[1] += float(bound.sum())
+    assert abs(float(total) - sums[0]) <= sums[1] + ov.U * abs(sums[0])
