@@ -68,7 +68,6 @@ struct Counts {
   int32_t active;  // rows that take part
   int32_t mean;    // rows that are not left out (those of weight 0 among them)
   int32_t bad;     // rows with an id outside the vocabulary
-  uint32_t joined; // workgroups that have left their rows' losses
 };
 
 enum Flag : uint8_t { F_OUT = 0, F_ACTIVE = 1, F_BAD = 2, F_ZERO = 3 };
@@ -233,7 +232,7 @@ __device__ __forceinline__ int scan_rows(const Targets& t, int64_t T, int32_t* r
   if (mean) atomicAdd(&tally[0], mean);  // whole numbers in LDS: the order does not matter
   if (bad) atomicAdd(&tally[1], bad);
   __syncthreads();
-  if (tid == 0) *counts = Counts{done, tally[0], tally[1], 0u};
+  if (tid == 0) *counts = Counts{done, tally[0], tally[1]};
   __syncthreads();
   return done;
 }
@@ -1240,7 +1239,6 @@ struct Ends {
   float* row_loss;  // [rows that take part], weighted
   float* each;      // by original row, or null
   float* total;     // or null
-  uint32_t joins;   // workgroups of all joins together
 };
 
 // The teacher's probability of a row's entry (1 for the one target), and x = its logit less the row's largest, over
@@ -1259,15 +1257,12 @@ struct Teacher {
 __device__ __forceinline__ Teacher teacher_of(const Targets& t, const Ends& e, int64_t row) { return Teacher{t, row, t.K ? e.teacher[row] : float2{0, 1}}; }
 
 // The rows' softmax statistics, weights and losses, 16 rows a workgroup: first a wave's lanes are 16 rows x 4
-// statistics, and its 16 waves share the statistics; then each wave takes a row's ids. The workgroup that comes last
-// adds the call's loss up, in 64 bits and in the rows' order, whichever it is. 8192 rows x 500 statistics: 34 us; few rows
-// take 6, a chain of waits for memory.
+// statistics, and its 16 waves share the statistics; then each wave takes a row's ids. 8192 rows x 500 statistics: 34
+// us; few rows take 6, a chain of waits for memory.
 constexpr int kJoinThreads = 1024, kJoinRows = 16;
 __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Targets t) {
   __shared__ float2 part[kJoinThreads / 64][kJoinRows];
   __shared__ float2 row_lse[kJoinRows];
-  __shared__ double wave_sum[kJoinThreads / 64];
-  __shared__ bool is_last;
   const int row = threadIdx.x % 16, slice = threadIdx.x / 16, wave = threadIdx.x / 64, lane = threadIdx.x & 63;
   const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + kUnit - 1) / kUnit * kUnit;
   for (int r0 = blockIdx.x * kJoinRows; r0 < end; r0 += gridDim.x * kJoinRows) {
@@ -1332,33 +1327,39 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
       if (lane == 0) {
         if (a.weights) loss *= a.weights[from];
         if (e.each) e.each[from] = loss;
-        else __hip_atomic_store(&e.row_loss[a.chunk + i], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else e.row_loss[a.chunk + i] = loss;
       }
     }
     __syncthreads();
   }
-  if (!e.total) return;
-  // Every wave's losses have reached memory (they are written past the caches, and waited for) before the workgroup
-  // counts itself. A fence would write all of the cache back: 40 us behind a product that has just filled it.
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(waits(0));
-  __syncthreads();
-  if (threadIdx.x == 0) is_last = __hip_atomic_fetch_add(&a.counts->joined, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1 == e.joins;
-  __syncthreads();
-  if (!is_last) return;
+}
+
+// The call's loss from its rows' (of launches before): one workgroup adds them up, in 64 bits and in an order that their
+// number fixes.
+constexpr int kNormThreads = 256;
+__device__ __forceinline__ void put_total(const Soft& a, const Ends& e) {
+  __shared__ double wave_sum[kNormThreads / 64];
+  const int active = a.counts->active, lane = threadIdx.x & 63;
   double sum = 0;
-  for (int i = threadIdx.x; i < a.counts->active; i += kJoinThreads) sum += double(__hip_atomic_load(&e.row_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  constexpr int kTogether = 16;  // on their way at once: behind the last row that one again, for nothing
+  for (int64_t i0 = threadIdx.x; i0 < active; i0 += kTogether * kNormThreads) {
+    float x[kTogether];
+#pragma unroll
+    for (int q = 0; q < kTogether; ++q) x[q] = e.row_loss[min(i0 + q * kNormThreads, int64_t(active) - 1)];
+#pragma unroll
+    for (int q = 0; q < kTogether; ++q) sum += i0 + q * kNormThreads < active ? x[q] : 0.f;
+  }
 #pragma unroll
   for (int d = 32; d; d >>= 1) sum += __shfl_down(sum, d);
-  if (lane == 0) wave_sum[wave] = sum;
+  if (lane == 0) wave_sum[threadIdx.x / 64] = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0;
-    for (int w = 0; w < kJoinThreads / 64; ++w) sum += wave_sum[w];
-    if (a.reduction == R_MEAN && a.counts->mean) sum /= a.counts->mean;
-    *e.total = a.counts->bad ? NAN : float(sum);
-  }
+  if (threadIdx.x) return;
+  sum = 0;
+  for (int w = 0; w < kNormThreads / 64; ++w) sum += wave_sum[w];
+  if (a.reduction == R_MEAN && a.counts->mean) sum /= a.counts->mean;
+  *e.total = a.counts->bad ? NAN : float(sum);
 }
+__global__ __launch_bounds__(kNormThreads) void k_vocab_total(Soft a, Ends e) { put_total(a, e); }
 
 // D at an id of a row: c (p - q), q the sum over the row's equal ids.
 template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const Ends& e, int i, int k, int32_t id, float q) {
@@ -1376,8 +1377,9 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
 
 // exp(z - m) -> c p, in place for bf16, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
 // Bound by memory: 8192 x 128000 in bf16, 2.1 GB each way, take 767 us, 5.6 TB/s.
-constexpr int kNormThreads = 256, kNormRows = 16, kNormCols = 512, kBatch = 4;
+constexpr int kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
+  if (e.total && blockIdx.x + 1 == gridDim.x) put_total(a, e);
   constexpr int kBlocks = kNormCols / 64;  // no statistic covers fewer columns
   __shared__ float factor[kNormRows][kBlocks];
   const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK / kNormRows;
@@ -1623,7 +1625,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   const int64_t batches = (P + kPieceTab - 1) / kPieceTab, row_blocks = (p.Tpad + kRowWaves - 1) / kRowWaves;
   const bool sorted = p.Kp > kFewIds, pack_first = batches == 1 && v.T * p.Hp * p.planes <= kFewElements;
   const int64_t per_chunk = 2 + (grad ? 3 + sorted + (p.hidden_splits > 1) + (p.chunks == 1 && p.weight_splits > 1) : 0);
-  s.left = batches + (v.top ? 1 : 0) + !pack_first + sorted + p.chunks * per_chunk + (grad && p.chunks > 1 ? 1 : 0);
+  s.left = batches + (v.top ? 1 : 0) + !pack_first + sorted + p.chunks * per_chunk + (grad ? p.chunks > 1 : !each);
   Piece* pieces = reinterpret_cast<Piece*>(ws + p.pieces);
   Counts* counts = reinterpret_cast<Counts*>(ws + p.counts);
   int32_t* rows = reinterpret_cast<int32_t*>(ws + p.rows);
@@ -1690,8 +1692,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
          v.temperature, a.scale, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
   const auto rows_of = [&](int64_t c) { return std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)); };
   const auto join_blocks = [&](int64_t n) { return blocks_of(int64_t(up(size_t(n), kUnit)) / kJoinRows); };
-  Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, each ? nullptr : v.loss, 0};
-  for (int64_t c = 0; c < p.chunks; ++c) ends.joins += uint32_t(join_blocks(rows_of(c)));
+  Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, nullptr};
   float* dh_part = reinterpret_cast<float*>(ws + p.part);
   float* dw_part = dh_part;
   if (p.chunks > 1 && p.hidden_splits > 1) dw_part += size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp);
@@ -1711,8 +1712,13 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     if (grad) launch_product<DT, S_LOGITS, DT>(s, p, p.logits, tiles, a);
     else launch_product<DT, S_LOGITS, 0>(s, p, p.logits, tiles, a);
     s.launch(k_vocab_join, join_blocks(n), kJoinThreads, f, ends, t);
-    if (!grad) continue;
-    s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols)), kNormThreads, f, ends, t);
+    const bool total = !each && c + 1 == p.chunks;
+    ends.total = total ? v.loss : nullptr;
+    if (!grad) {
+      if (total) s.launch(k_vocab_total, 1, kNormThreads, f, ends);
+      continue;
+    }
+    s.launch(k_vocab_normalize<DT>, blocks_of(npad / kNormRows * ((p.Vp + kNormCols - 1) / kNormCols) + total), kNormThreads, f, ends, t);
     if (sorted) s.launch(k_vocab_own<DT>, blocks_of((n * ((p.Kp + 63) / 64) + 3) / 4), 256, f, ends, t);
     const auto mtiles = [&](Size z) { return int32_t(tiles_of(z, v.H, 1)); };
     tile(p.hidden);

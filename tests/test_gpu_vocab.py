@@ -724,3 +724,24 @@ def test_more_tokens_than_a_launch_has_workgroups_for():
         sums[0] += float(want.sum())
         sums[1] += float(bound.sum())
     assert abs(float(total) - sums[0]) <= sums[1] + ov.U * abs(sums[0])
+
+
+@pytest.mark.parametrize("limit", [1, 3, None])
+@pytest.mark.parametrize("T,V,dtype,top", [(40, [300], "fp32", 0), (1000, [3000, 500], "bf16", 6), (5000, [700], "bf16", 0), (3300, [1 << 17], "fp32", 3)])
+def test_the_loss_is_the_sum_of_its_rows(T, V, dtype, top, limit):
+    """Whatever workgroups a call has, one chunk or two: the rows' own losses summed in 64 bits, and rounded."""
+    torch = torch_mod()
+    A = lib()
+    c = Case(T, 24, V, dtype, top, seed=49, left_out=0.05, weights=True)
+    prev = A.ar_set_launch_blocks(limit) if limit and T * sum(V) < 1 << 23 else None
+    try:
+        for turn in range(3):
+            c.hidden.neg_()
+            each, total, mean, with_grad = c.run(False, reduction="none"), c.run(False, reduction="sum"), c.run(False), c.run()[0]
+            count = int((c.ids.reshape(T, -1) >= 0).any(1).sum())
+            for got, want in ((total, each.double().sum()), (mean, each.double().sum() / count)):
+                assert abs(float(got) - float(want)) <= ov.U * abs(float(want)) + T * 2.0 ** -52 * float(each.double().abs().sum())
+            assert torch.equal(mean, with_grad)
+    finally:
+        if prev is not None:
+            A.ar_set_launch_blocks(prev)
