@@ -358,7 +358,8 @@ def vocab_loss_grad(hidden, weight, targets, reduction="mean", ignore_index=-100
     """vocab_loss and its gradients: (loss, d_hidden, d_weight), d_weight as weight (a tensor, or a list of pieces).
 
     The gradients are of the loss ("none": of the rows' sum), in the inputs' type; d_hidden is the sum over all
-    pieces, as an Allreduce of the ranks' parts leaves it. out_hidden, out_weight: tensors that receive them.
+    pieces, as an Allreduce of the ranks' parts leaves it. out_hidden, out_weight: tensors that receive them. The
+    workspace holds up to 4 GiB of logits at a time (2 bytes each in bf16, 10 in fp32).
     """
     return _vocab(hidden, weight, targets, None, reduction, ignore_index, temperature, token_weights, True, out_hidden,
                   out_weight, stream, workspace)

@@ -2,7 +2,7 @@
 // to a teacher's top logits, of hidden states h [T, H] against an output matrix W [V, H]
 // whose rows lie in P pieces, and their gradients.
 //
-//   z = h W^T / temperature                       (never kept as a whole)
+//   z = h W^T / temperature                       (not kept; with gradients its exponentials are, a chunk of tokens' at a time)
 //   lse_t = log(sum_v exp z_tv),  p = exp(z - lse)
 //   cross entropy:  loss_t = lse_t - z_ty
 //   distillation:   q_t = softmax(teacher / temperature),
@@ -1506,7 +1506,7 @@ int64_t blocks_of(int64_t n) { return std::max<int64_t>(1, std::min<int64_t>(n, 
 
 enum Size { Z_S = 0, Z_M = 1, Z_L = 2, Z_F = 3 };
 
-// Scratch of D and the exponentials that one chunk of tokens may take.
+// Scratch that one chunk of tokens may take (plan_of).
 constexpr int64_t kChunkBytes = int64_t(4) << 30;
 constexpr int kUnits = 256;  // compute units
 // Hidden elements that the first launch's one workgroup packs itself rather than leaving them to another launch.
@@ -1561,8 +1561,9 @@ Plan plan_of(const Vocab& v, bool grad) {
   p.few = p.packed && v.T <= kFewRows && v.H >= 8;  // (a whole vector in every row)
   if (p.few) p.packed = false;
   p.Tpad = int64_t(up(size_t(std::max<int64_t>(v.T, 1)), kUnit));
-  // a chunk's scratch: statistics at their finest, and with gradients the exponentials and D
-  const int64_t per = p.Vp / 64 * 8 + (grad ? (v.dtype == D_FP32 ? 10 : 2) * p.Vp : 0);
+  // a chunk's scratch: statistics at their finest, the own ids' logits, log-sum-exp and weight, and with gradients the
+  // exponentials and D
+  const int64_t per = p.Vp / 64 * 8 + p.Kp * 4 + 12 + (grad ? (v.dtype == D_FP32 ? 10 : 2) * p.Vp : 0);
   p.Tc = std::min(p.Tpad, std::max<int64_t>(kUnit, kChunkBytes / per / kUnit * kUnit));
   p.chunks = (p.Tpad + p.Tc - 1) / p.Tc;
   const int64_t n = std::min(p.Tc, v.T), passes = p.planes == 1 ? 1 : 6;

@@ -403,7 +403,7 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
 /* ---- losses over a vocabulary in pieces ----
  * The output layer of a model whose vocabulary is spread over P ranks, with its loss and gradients: hidden
  * states h [T, H] against an output matrix W [V, H] whose rows (the vocabulary) lie in P pieces in rank order.
- *   z_t  = h_t W^T / temperature        (V logits a token; never kept as a whole)
+ *   z_t  = h_t W^T / temperature        (V logits a token; see Workspace)
  *   l_t  = log(sum_v exp(z_tv)),  p_t = exp(z_t - l_t)
  *   cross entropy (top = 0), target y_t:       loss_t = w_t (l_t - z_ty)
  *   distillation (top = K >= 1), a teacher's K logits and their ids a token: q_t = softmax of its logits /
@@ -426,9 +426,13 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
  *    lost. The order of every sum is fixed by the sizes, the alignment and the number of rows that take part, so a
  *    call gives the same bits on every run.
  *  - Stream, errors, capture: as for the gradient calls. The tables of pieces travel as kernel arguments.
- *  - Workspace: device scratch of ar_vocab_workspace_bytes() bytes, 16-byte aligned, contents unprepared. It is
- *    bounded in T but for the gathered hidden states (logits are worked on 4 GiB at a time), and the library keeps
- *    none of its own for these calls: NULL is too small.
+ *  - Workspace: device scratch of ar_vocab_workspace_bytes() bytes, 16-byte aligned, contents unprepared; the library
+ *    keeps none of its own for these calls: NULL is too small. The loss alone keeps no logits. With gradients a call
+ *    keeps 2 bytes a logit in bf16 and 10 in fp32 (exponentials, then d), of as many tokens at a time as take 4 GiB
+ *    with their statistics, at least 256. The rest grows with T: the gathered hidden states (2 bytes an element, 6 in
+ *    fp32, rows rounded up to 64 elements), 4 bytes an id (8 where top > 4, ids rounded up to 4) and some 20 bytes a token
+ *    (top > 4: 64 more at 2^20 ids). Copies of pieces that are not read in place take as many bytes an element, and
+ *    partial gradients at most 512 MiB, or, where there are more tokens than are worked on at a time, 4 V H bytes more.
  *  - Memory: rows are contiguous, ld apart (>= their length), at any address that is a multiple of the element
  *    size. 16-byte aligned pieces of bf16 with H and ld multiples of 8 are read in place, and so is every piece where
  *    T <= 64 and H >= 8; others are first copied into the workspace as bf16 terms. What a call writes (loss, dh, dw,

@@ -224,3 +224,20 @@ def test_a_temperature_whose_scale_is_infinite():
         else:
             assert all("log2(e)" in message for message in both(call(temperature=t)))
             refused(lambda: A.ar_vocab_workspace_bytes(call(temperature=t), False))
+
+
+@pytest.mark.parametrize("top,dtype", [(0, "bf16"), (3, "fp32"), (64, "bf16"), (1024, "bf16"), (1024, "fp32")])
+@pytest.mark.parametrize("rows", [100, 131072])
+@pytest.mark.parametrize("grad", [False, True])
+def test_what_of_the_workspace_grows_with_the_tokens(top, dtype, rows, grad):
+    """4 GiB of logits, ids' logits and statistics; a token's hidden states, ids and some words, as ar.h lists them; and
+    partial gradients of at most 512 MiB beside 4 bytes an element of W."""
+    kw = dict(TEACHER, top=top, ids_ld=top, logits_ld=top) if top else {}
+    ids = max(4, (top + 3) // 4 * 4)
+
+    def need(T):
+        return A.ar_vocab_workspace_bytes(call(T=T, dtype=dtype, pieces=[(BASE + 4 * GAP, BASE + 5 * GAP, rows, 64, 64)], **kw), grad)
+    per = 64 * (6 if dtype == "fp32" else 2) + ids * (8 if top > 4 else 4) + 90
+    terms = rows * 64 * 6 if dtype == "fp32" else 0
+    for T in (1 << 16, 1 << 21, 1 << 24):
+        assert need(T) <= (4 << 30) + T * per + terms + (512 << 20) + (rows + 255) * 64 * 4 + (1 << 20)
