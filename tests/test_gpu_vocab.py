@@ -745,3 +745,90 @@ def test_the_loss_is_the_sum_of_its_rows(T, V, dtype, top, limit):
     finally:
         if prev is not None:
             A.ar_set_launch_blocks(prev)
+
+
+def exact_products(T, V, H, gain=1024.0):
+    """fp32 inputs whose every sum has one product that is not 0: hidden row t is x_t at column t and 0 elsewhere, the
+    logit at id a_t leads by hundreds, so that D is w_t at a_t and -w_t at y_t and 0 elsewhere, all of full 24 bits."""
+    torch = torch_mod()
+    g = torch.Generator(device="cuda").manual_seed(46)
+    x, w = 1 + torch.rand(T, generator=g, device="cuda"), 1 + torch.rand(T, generator=g, device="cuda")
+    hidden = torch.zeros(T, H, device="cuda")
+    t = torch.arange(T, device="cuda")
+    hidden[t, t] = x
+    weight = torch.rand(V, H, generator=g, device="cuda") + 0.5
+    order = torch.randperm(V, generator=g, device="cuda")
+    a, y = order[:T], order[T: 2 * T]
+    weight[a, t] = gain * (1 + torch.rand(T, generator=g, device="cuda"))
+    return hidden, weight, a, y, w
+
+
+# rows, vocabulary: few rows' products, middle and large tiles
+@pytest.mark.parametrize("T,V", [(12, 600), (60, 600), (200, 1000), (200, 50000)])
+def test_fp32_products_keep_their_bits(T, V):
+    """A product of two 24-bit values from three bf16 terms each: the parts left out are below 2^-25 of it (x1 y2, x2 y1
+    and smaller: a second term is at most 2^-9 of the first's value, a third 2^-17), the six that are kept are exact in
+    fp32 and their sum is rounded five times: (6 + 2) U of the product. Losing any of the six shows (the CPU tests
+    say so). A loss is the difference of two, scaled twice: 3 U more of each, and of itself."""
+    torch = torch_mod()
+    H = 264
+    hidden, weight, a, y, w = exact_products(T, V, H)
+    loss, dh, dw = lib().vocab_loss_grad(hidden, weight, y, "none", token_weights=w)
+    t = torch.arange(T, device="cuda")
+    W, x, c = weight.double(), hidden.double()[t, t], w.double()
+    za, zy = x * W[a, t], x * W[y, t]
+    within(loss, c * (za - zy), 12 * ov.U * c * (za + zy), "loss")
+    # two products a sum, and the sum's rounding
+    within(dh, c[:, None] * (W[a] - W[y]), 10 * ov.U * c[:, None] * (W[a] + W[y]), "d_hidden")
+    want = torch.zeros(V, H, dtype=torch.float64, device="cuda")
+    want[a, t] = c * x
+    want[y, t] = -c * x
+    within(dw, want, 9 * ov.U * want.abs(), "d_weight")
+
+
+def by_rows(c, rows, count):
+    """The oracle's losses, gradients and bounds from `rows` rows at a time; c.kw's reduction is "none" or "sum", or "mean"
+    of `count` rows."""
+    torch = torch_mod()
+    T = len(c.ids)
+    kw = dict(c.kw)
+    share = 1.0 / count if kw.get("reduction", "mean") == "mean" else 1.0
+    weights = kw.pop("token_weights", torch.ones(T, device="cuda")).double() * share
+    kw["reduction"] = "none"
+    W = torch.cat(c.weight)
+    each, dh, dw = [], [], 0
+    beach, bh, bw = [], [], 0
+    for r in torch.arange(T, device="cuda").split(rows):
+        out = ov.loss_and_gradients(c.hidden[r], W, c.ids[r], None if c.logits is None else c.logits[r], dtype=c.dtype,
+                                    **dict(kw, token_weights=weights[r]))
+        each.append(out[0]), dh.append(out[1]), beach.append(out[3]), bh.append(out[4])
+        dw, bw = dw + out[2], bw + out[5]
+    return torch.cat(each), torch.cat(dh), dw, torch.cat(beach), torch.cat(bh), bw
+
+
+# more than one chunk of 4 GiB: fp32 of 131072 ids takes 3072 rows at a time, of 2^20 ids 256, bf16 of 2^20 1792. In one
+# the last chunk's rows are all left out.
+@pytest.mark.parametrize("dtype,T,V,top,kw", [
+    ("fp32", 3400, [130072, 1000], 0, {}), ("fp32", 6500, [130072, 1000], 3, dict(weights=True)),
+    ("fp32", 4500, [130072, 1000], 8, dict(weights=True, temperature=1.5)),
+    ("fp32", 600, [1 << 19, 1 << 19], 6, dict(reduction="none")), ("fp32", 1100, [1 << 20], 2, dict(reduction="sum", left_out=0.6)),
+    ("bf16", 2300, [1 << 20], 9, dict(reduction="none", left_out=0.05)), ("bf16", 2000, [1 << 19, 1 << 19], 4, dict(weights=True, left_out=0.02))])
+def test_lists_weights_and_means_in_chunks(dtype, T, V, top, kw):
+    torch = torch_mod()
+    c = Case(T, 20, V, dtype, top, seed=47, **kw)
+    loss, dh, dw = c.run()
+    alone = c.run(False)
+    count = int((c.ids.reshape(T, -1) >= 0).any(1).sum())
+    # a chunk's sums have no more terms than the oracle's blocks, but for bf16, whose 1792 roundings of |D| |h| are
+    # 1792 * 2^-24 * 2^8 of what D's own rounding gives
+    each, want_h, want_w, beach, bh, bw = by_rows(c, 3072 if sum(V) < 1 << 20 else 512, count)
+    if dtype == "bf16":
+        bw = 1.03 * bw
+    if c.kw.get("reduction", "mean") == "none":
+        within(loss, each, beach, "loss")
+        assert torch.equal(loss, alone)
+    else:
+        within(loss, each.sum(), beach.sum() + 4 * ov.U * each.sum().abs(), "loss")
+        within(alone, each.sum(), beach.sum() + 4 * ov.U * each.sum().abs(), "loss alone")
+    within(dh, want_h, bh, "d_hidden")
+    within(torch.cat(dw), want_w, bw, "d_weight")

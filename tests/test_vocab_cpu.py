@@ -241,3 +241,27 @@ def test_what_of_the_workspace_grows_with_the_tokens(top, dtype, rows, grad):
     terms = rows * 64 * 6 if dtype == "fp32" else 0
     for T in (1 << 16, 1 << 21, 1 << 24):
         assert need(T) <= (4 << 30) + T * per + terms + (512 << 20) + (rows + 255) * 64 * 4 + (1 << 20)
+
+
+@pytest.mark.parametrize("lost", [None, 0, 1, 2, 3, 4, 5])
+def test_a_lost_product_of_terms_shows(lost):
+    """fp32 operands as three bf16 terms, and the six products that a call sums, smallest first: within 8 U of the value,
+    and past it (and past what the GPU tests allow two of them, 10 U of both) where one is left out."""
+    g = torch.Generator().manual_seed(2)
+    x, y = [1 + torch.rand(2000, generator=g) for _ in range(2)]
+
+    def terms(v):
+        out = []
+        for _ in range(3):
+            out.append(v.bfloat16().float())
+            v = v - out[-1]
+        assert not bool(v.any())
+        return out
+    a, b = terms(x), terms(y)
+    total = torch.zeros(2000)
+    for i, (p, q) in enumerate([(2, 0), (0, 2), (1, 1), (1, 0), (0, 1), (0, 0)]):
+        if i != lost:
+            total += a[p] * b[q]
+    exact = x.double() * y.double()
+    off = ((total.double() - exact).abs() / exact).max()
+    assert float(off) <= 8 * ov.U if lost is None else float(off) > 20 * ov.U
