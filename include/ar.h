@@ -421,10 +421,10 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
  *    bf16 operands are exact and their sums fp32; d is rounded to bf16 once before the gradients' products (p before
  *    that to 2^-11 of it, or 2^-39 of the row's largest p), whose fp32 sums are rounded to bf16. fp32: operands are
  *    split into three bf16 terms (which hold all their bits down to 2^-133) and six products of them summed, 2^-24
- *    or so of a product. Logits, the teacher's too, are divided by the temperature after the row's largest has been
- *    subtracted (a difference past the largest fp32 value counts as infinite). Values below 2^-126 on the way may be
- *    lost. The order of every sum is fixed by the sizes, the alignment and the number of rows that take part, so a
- *    call gives the same bits on every run.
+ *    or so of a product; an infinite operand, whose other terms are 0, makes its products NaN. Logits, the teacher's
+ *    too, are divided by the temperature after the row's largest has been subtracted (a difference past the largest
+ *    fp32 value counts as infinite). Values below 2^-126 on the way may be lost. The order of every sum is fixed by
+ *    the sizes, the alignment and the number of rows that take part, so a call gives the same bits on every run.
  *  - Stream, errors, capture: as for the gradient calls. The tables of pieces travel as kernel arguments.
  *  - Workspace: device scratch of ar_vocab_workspace_bytes() bytes, 16-byte aligned, contents unprepared; the library
  *    keeps none of its own for these calls: NULL is too small. The loss alone keeps no logits. With gradients a call
