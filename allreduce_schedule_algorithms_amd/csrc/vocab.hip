@@ -11,6 +11,9 @@
 //                   the call's loss over the temperature
 //   dh = D W,  dW = D^T h
 //
+// (In bf16 D is rounded. 1 / N of a mean over N rows, the same in every D, would be rounded the same way in all of
+// them, which no sum over rows or ids evens out: of c, D takes on a power of two, and the results the rest.)
+//
 // Rows that the targets leave out take no part: the rows that count are gathered in order
 // (k_vocab_prepare, k_vocab_pack), and every product runs over as many as there are. The products are
 // matrix products of bf16 operands with fp32 sums; fp32 operands are split exactly into
@@ -64,10 +67,12 @@ struct PieceTab {
   int32_t count, at;
 };
 
-struct Counts {
+struct alignas(16) Counts {
   int32_t active;  // rows that take part
   int32_t mean;    // rows that are not left out (those of weight 0 among them)
   int32_t bad;     // rows with an id outside the vocabulary
+  float factor;    // what a mean and the temperature make of the gradients is share times factor: a power of two, which D
+  double share;    // takes on, and a value in [1, 2), which the results are multiplied by in fp32
 };
 
 enum Flag : uint8_t { F_OUT = 0, F_ACTIVE = 1, F_BAD = 2, F_ZERO = 3 };
@@ -177,7 +182,7 @@ __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_teacher(Targets t, int
 
 // Rows that take part, in order, at rows[0..active); the others behind them. One workgroup; returns active.
 constexpr int kScanThreads = 1024, kScanEach = 4;
-__device__ __forceinline__ int scan_rows(const Targets& t, int64_t T, int32_t* rows, uint8_t* flags, Counts* counts) {
+__device__ __forceinline__ int scan_rows(const Targets& t, int64_t T, bool mean_of, int32_t* rows, uint8_t* flags, Counts* counts) {
   __shared__ int wave_n[kScanThreads / 64][kScanEach], tally[2], round;
   const int tid = threadIdx.x, wave = tid / 64, lane = tid & 63;
   if (tid < 2) tally[tid] = 0;
@@ -232,7 +237,11 @@ __device__ __forceinline__ int scan_rows(const Targets& t, int64_t T, int32_t* r
   if (mean) atomicAdd(&tally[0], mean);  // whole numbers in LDS: the order does not matter
   if (bad) atomicAdd(&tally[1], bad);
   __syncthreads();
-  if (tid == 0) *counts = Counts{done, tally[0], tally[1]};
+  if (tid == 0) {
+    int e;
+    const double m = frexp(1 / (double(t.temperature) * (mean_of && tally[0] ? tally[0] : 1)), &e);
+    *counts = Counts{done, tally[0], tally[1], float(2 * m), ldexp(1., e - 1)};
+  }
   __syncthreads();
   return done;
 }
@@ -385,7 +394,7 @@ struct PrepareArgs {
   PieceTab tab;
   Piece* pieces;
   char* wp;  // null: read in place
-  int32_t scan, pack, H, Hp;
+  int32_t scan, pack, mean, H, Hp;
   int64_t T;
   int32_t* rows;
   uint8_t* flags;
@@ -405,7 +414,7 @@ template <int DT> __global__ __launch_bounds__(kScanThreads) void k_vocab_prepar
       p.pieces[p.tab.at + i] = q;
     }
     if (p.scan) {
-      const int active = scan_rows(t, p.T, p.rows, p.flags, p.counts);
+      const int active = scan_rows(t, p.T, p.mean, p.rows, p.flags, p.counts);
       if (p.pack) pack_rows<DT>(a, t, p.tab.p, active, wave, kScanThreads / 64);
     }
   }
@@ -449,8 +458,7 @@ using TileS = Tile<128, 64, 4, 1, 2, 5>;
 template <int DT> using TileF = std::conditional_t<DT == D_FP32, Tile<64, 64, 4, 1, 2, 5>, TileS>;
 
 struct Product {
-  const Piece* pieces;
-  const Counts* counts;
+  const Piece* pieces;  // the call's Counts lie before them: one address, for registers are short where this is used
   int32_t P, H, Hp, Vp, mtiles, planes;
   int32_t splits, bn, resident;  // at most so many shares of the depth; columns of a tile; workgroups that stay resident
   int32_t chunk, chunk_rows;  // this call's rows: [chunk, chunk + chunk_rows) of those that take part
@@ -752,7 +760,8 @@ __device__ __forceinline__ int splits_of(const Product& a, int nlen) {
   return tiles ? min(max(a.resident / tiles, 1), a.splits) : 1;
 }
 
-__device__ __forceinline__ int chunk_active(const Product& a) { return min(max(a.counts->active - a.chunk, 0), a.chunk_rows); }
+__device__ __forceinline__ const Counts& counts_of(const Product& a) { return reinterpret_cast<const Counts*>(a.pieces)[-1]; }
+__device__ __forceinline__ int chunk_active(const Product& a) { return min(max(counts_of(a).active - a.chunk, 0), a.chunk_rows); }
 
 // Where a workgroup's tile t lies, and which slices of the depth it takes.
 struct Place {
@@ -904,6 +913,14 @@ template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradie
   static_assert(KEEP != D_BF16 || C::FM % 2 == 0, "bf16 is written by pairs of products");
   const int lane = wave.lane, wn0 = at.n0 + wave.n * C::NW, wm0 = at.m0 + wave.m * C::MW;
   constexpr int kBytes = KEEP == D_BF16 ? 2 : 4;
+  float factor = 1;
+  if (!a.part) {
+    // A scalar load (nothing writes there meanwhile), whose wait is not one for the next tile's slices; and waited for
+    // here, for otherwise the compiler has the products' loop wait for it, and with it for all loads: 6% of d_hidden.
+    typedef const __attribute__((address_space(4))) float* Constant;
+    factor = *(Constant)(uintptr_t)&counts_of(a).factor;
+    __builtin_amdgcn_s_waitcnt(kLdsDone);
+  }
   // a tile of the vocabulary lies in one piece
   const Piece* p = nullptr;
   if constexpr (DIR == S_WEIGHT) p = a.pieces + __builtin_amdgcn_readfirstlane(piece_of<true>(a.pieces, a.P, at.n0));
@@ -931,11 +948,11 @@ template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradie
       } else if constexpr (KEEP == D_BF16) {
         if (i & 1) {
           const int m8 = wm0 + (i - 1) * 16 + lane / 16 * 8;
-          const bf16x8 v = eight_of<bf16x8, bf16x4>(acc[i - 1][j], acc[i][j]);
+          const bf16x8 v = eight_of<bf16x8, bf16x4>(acc[i - 1][j] * factor, acc[i][j] * factor);
           if (there && m8 < a.H) put(reinterpret_cast<__bf16*>(row) + m8, v, a.H - m8);
         }
       } else {
-        if (there && m < a.H) put(reinterpret_cast<float*>(row) + m, acc[i][j], a.H - m);
+        if (there && m < a.H) put(reinterpret_cast<float*>(row) + m, acc[i][j] * factor, a.H - m);
       }
     }
   }
@@ -1222,10 +1239,10 @@ struct Soft {
   int32_t blocks, chunk, chunk_rows, reduction;
   int32_t planes, block;  // block: columns a statistic covers
   int64_t Vp;
-  float temperature, scale;  // scale: log2(e) / temperature
+  float scale;  // log2(e) / temperature
   float2* lse;   // [chunk rows] in two parts: the largest product, the log of the sum around it (their sum would round
                  // p by 2^-24 of the logit)
-  float* coef;   // [chunk rows]: the row's weight in the loss over the temperature; 0 behind the rows
+  float* coef;   // [chunk rows]: the row's weight times Counts::share; 0 behind the rows
   float* exps;   // fp32: exp(z - m)
   char* d;
 };
@@ -1302,8 +1319,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
       if (r < active) {
         lse = float2{m, log2f(s)};
         // in 64 bits: a weight over a small temperature may pass the largest fp32 value where its share of the mean does not
-        const double w = a.weights ? a.weights[a.rows[a.chunk + r]] : 1.f, n = a.reduction == R_MEAN ? a.counts->mean : 1;
-        coef = float(w / (double(a.temperature) * n));
+        coef = float((a.weights ? double(a.weights[a.rows[a.chunk + r]]) : 1.) * a.counts->share);
       }
       if (lane < 16) {
         a.lse[r] = row_lse[row] = lse;
@@ -1375,7 +1391,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
   }
 }
 
-// exp(z - m) -> c p, in place for bf16, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
+// exp(z - m) -> c p (c but for Counts::factor), in place for bf16, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
 // Bound by memory: 8192 x 128000 in bf16, 2.1 GB each way, take 767 us, 5.6 TB/s.
 constexpr int kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
@@ -1492,6 +1508,7 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
       for (int q = 0; q < 8; ++q) s += v[q];
     }
     for (; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(from + k * a.part_stride);
+    s *= counts_of(a).factor;
     if constexpr (DT == D_BF16) put(reinterpret_cast<__bf16*>(row) + m, __builtin_convertvector(s, bf16x4), a.H - m);
     else put(reinterpret_cast<float*>(row) + m, s, a.H - m);
   }
@@ -1574,8 +1591,9 @@ Plan plan_of(const Vocab& v, bool grad) {
   p.tile_rows = p.logits == Z_L ? 256 : p.logits == Z_M ? 128 : 64;
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += up(bytes); return o; };
-  p.counts = take(sizeof(Counts));
-  p.pieces = take(sizeof(Piece) * v.pieces.size());
+  static_assert(sizeof(Counts) % alignof(Piece) == 0, "the pieces follow");
+  p.counts = take(sizeof(Counts) + sizeof(Piece) * v.pieces.size());
+  p.pieces = p.counts + sizeof(Counts);
   p.rows = take(size_t(p.Tpad) * 4);
   p.flags = take(size_t(p.Tpad));
   p.teacher = take(v.top ? size_t(p.Tpad) * 8 : 0);
@@ -1652,6 +1670,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     pr.wp = p.packed ? ws + p.wp : nullptr;
     pr.scan = i0 == 0;
     pr.pack = pack_first;
+    pr.mean = v.reduction == R_MEAN;
     pr.H = int32_t(v.H);
     pr.Hp = p.Hp;
     pr.T = v.T;
@@ -1668,7 +1687,6 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   }
   Product a{};
   a.pieces = pieces;
-  a.counts = counts;
   a.P = int32_t(P);
   a.H = int32_t(v.H);
   a.Hp = p.Hp;
@@ -1690,7 +1708,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.dh = v.dh;
   a.dh_ld = v.dh_ld;
   Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
-         v.temperature, a.scale, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
+         a.scale, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
   const auto rows_of = [&](int64_t c) { return std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)); };
   const auto join_blocks = [&](int64_t n) { return blocks_of(int64_t(up(size_t(n), kUnit)) / kJoinRows); };
   Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, nullptr};

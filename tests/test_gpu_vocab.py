@@ -832,3 +832,19 @@ def test_lists_weights_and_means_in_chunks(dtype, T, V, top, kw):
         within(alone, each.sum(), beach.sum() + 4 * ov.U * each.sum().abs(), "loss alone")
     within(dh, want_h, bh, "d_hidden")
     within(torch.cat(dw), want_w, bw, "d_weight")
+
+
+@pytest.mark.parametrize("T,H,V", [(13, 40, 300), (48, 64, 1000), (48, 61, 1000), (100, 200, 5000), (700, 72, 30000)])
+@pytest.mark.parametrize("top", [0, 6])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_a_means_factor_is_not_rounded_into_d(T, H, V, top, dtype):
+    """N times a mean's gradients are the sum's, but for the rounding of each result (in fp32 the factor's own and its
+    product's as well): 1 / N, the same in every row, may not be rounded into what the products multiply."""
+    c = Case(T, H, [V], dtype, top, seed=50)
+    _, dh, dw = c.run()
+    _, sh, sw = c.run(reduction="sum")
+    n = int((c.ids.reshape(T, -1) >= 0).any(1).sum())
+    assert n & (n - 1)
+    u = {"bf16": 2 * ov.U_BF16 + 4 * ov.U, "fp32": 6 * ov.U}[dtype] * 1.01
+    for mean, total in ((dh, sh), (dw[0], sw[0])):
+        within(mean * 1.0, total.double() / n, u * total.double().abs() / n + 2.0 ** -120, "a mean's gradient")
