@@ -11,7 +11,7 @@
 //                   the call's loss over the temperature
 //   dh = D W,  dW = D^T h
 //
-// (In bf16 D is rounded. 1 / N of a mean over N rows, the same in every D, would be rounded the same way in all of
+// (In bf16 D is rounded, of few rows to two bf16 terms. 1 / N of a mean over N rows, the same in every D, would be rounded the same way in all of
 // them, which no sum over rows or ids evens out: of c, D takes on a power of two, and the results the rest.)
 //
 // Rows that the targets leave out take no part: the rows that count are gathered in order
@@ -259,6 +259,7 @@ struct PackArgs {
   char* hp;
   int32_t* idt;  // [Tpad][Kp], -1 behind a row's ids
   int32_t Kp;
+  int32_t lo;    // as in Product: the rows are there once more from this one on
   void* dh;      // null: no gradient
   int64_t dh_ld;
   float* each;   // every row's loss, or null
@@ -305,13 +306,15 @@ template <int DT> __device__ __forceinline__ void pack_rows(const PackArgs& a, c
   constexpr int PL = DT == D_FP32 ? 3 : 1;
   const int lane = threadIdx.x & 63;
   // the products go 2 kBK rows deep at a time, and tiles look up the ids of up to kUnit rows
-  const int zeros = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK, end = (active + kUnit - 1) / kUnit * kUnit;
+  const int lo = DT == D_BF16 ? a.lo : 0, zeros = lo ? 2 * lo : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK, end = (active + kUnit - 1) / kUnit * kUnit;
   const int K = t.K ? t.K : 1;
   for (int64_t i = first; i < a.Tpad; i += step) {
     const int64_t r = i < a.T ? a.rows[i] : -1;
     __bf16* dst = reinterpret_cast<__bf16*>(a.hp) + i * PL * a.Hp;
-    if (i < active) {
-      pack_row<DT>(a.hidden, r * a.ld, a.H, a.Hp, dst, lane);
+    int64_t from = i < active ? r : -1;
+    if (lo && i >= lo && i < lo + active) from = a.rows[i - lo];
+    if (from >= 0) {
+      pack_row<DT>(a.hidden, from * a.ld, a.H, a.Hp, dst, lane);
     } else if (i < zeros) {
       for (int c = lane * 8; c < PL * a.Hp; c += 512) *reinterpret_cast<bf16x8*>(dst + c) = bf16x8{};
     }
@@ -462,6 +465,7 @@ struct Product {
   int32_t P, H, Hp, Vp, mtiles, planes;
   int32_t splits, bn, resident;  // at most so many shares of the depth; columns of a tile; workgroups that stay resident
   int32_t chunk, chunk_rows;  // this call's rows: [chunk, chunk + chunk_rows) of those that take part
+  int32_t lo;                 // few rows of bf16: what D's rounding leaves, rounded too, is its rows from this one on; or 0
   int32_t kend;               // elements of a row along H that exist
   const char* hp;             // gathered hidden rows
   char* d;                    // [rows][planes * Vp]: (bf16) exp(z - m) in fp16, then D
@@ -762,6 +766,8 @@ __device__ __forceinline__ int splits_of(const Product& a, int nlen) {
 
 __device__ __forceinline__ const Counts& counts_of(const Product& a) { return reinterpret_cast<const Counts*>(a.pieces)[-1]; }
 __device__ __forceinline__ int chunk_active(const Product& a) { return min(max(counts_of(a).active - a.chunk, 0), a.chunk_rows); }
+// Rows of D, its second terms' among them.
+__device__ __forceinline__ int d_rows(const Product& a, int active) { return active ? a.lo + active : 0; }
 
 // Where a workgroup's tile t lies, and which slices of the depth it takes.
 struct Place {
@@ -972,7 +978,7 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
   constexpr int kLoads = St::kLoads;
   AR_LDS char *lds = (AR_LDS char*)shared, *last = lds + (C::kStages - 1) * C::kStage;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64), wm = wave % C::WM, wn = wave / C::WM;
-  const int active = chunk_active(a);
+  const int active = DIR == S_LOGITS ? chunk_active(a) : d_rows(a, chunk_active(a));
   const int nlen = DIR == S_WEIGHT ? a.Vp : active;
   const uint32_t ntiles = (nlen + C::BN - 1) / C::BN, mtiles = a.mtiles, tiles = ntiles * mtiles, splits = splits_of(a, nlen), places = tiles * splits;
   const int depth = DIR == S_LOGITS ? a.Hp : DIR == S_HIDDEN ? a.Vp : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK;
@@ -1085,9 +1091,10 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
   using C = TileF<DT>;
   static_assert(C::WN == 1 && C::BN == 64 && C::kThreads == 256, "the loads below");
   constexpr bool kAlong = DIR == S_LOGITS;
-  constexpr int PL = DT == D_FP32 ? 3 : 1, kPer = DT == D_FP32 ? 4 : 8;  // kPer: elements of a 16-byte load
+  // terms of X and of Y; elements of a 16-byte load
+  constexpr int PL = DT == D_FP32 ? 3 : 1, PY = DT == D_BF16 && !kAlong ? 2 : PL, kPer = DT == D_FP32 ? 4 : 8;
   constexpr int kLoads = C::BM * kBK / kPer / C::kThreads, kRow = (kAlong ? kBK : C::BM) / kPer;
-  constexpr int kSlice = PL * C::kStage;
+  constexpr int kSlice = PL * C::kX + PY * C::kY;
   using E = std::conditional_t<DT == D_FP32, float, uint16_t>;
   typedef E V __attribute__((ext_vector_type(kPer)));
   // (in global memory: a load that may be of LDS would be waited for with it)
@@ -1102,7 +1109,7 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
   const int ntiles = (active + C::BN - 1) / C::BN, tiles = ntiles * a.mtiles;
   struct Slice {
     V x[kLoads];
-    bf16x8 y[PL];
+    bf16x8 y[PY];
   };
   const int splits = splits_of(a, active);
   for (int t = blockIdx.x; t < tiles * splits; t += gridDim.x) {
@@ -1139,8 +1146,8 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
       const int64_t n = min(at.n0 + tid / 4, active - 1);
       const char* p = (DIR == S_LOGITS ? a.hp + (a.chunk + n) * PL * a.Hp * 2 : a.d + n * PL * a.Vp * 2) + (k + tid % 4 * 8) * 2;
 #pragma unroll
-      for (int i = 0; i < PL; ++i)
-        r.y[i] = *reinterpret_cast<const __attribute__((address_space(1))) bf16x8*>(reinterpret_cast<uintptr_t>(p) + int64_t(i) * (DIR == S_LOGITS ? a.Hp : a.Vp) * 2);
+      for (int i = 0; i < PY; ++i)
+        r.y[i] = *reinterpret_cast<const __attribute__((address_space(1))) bf16x8*>(reinterpret_cast<uintptr_t>(p) + int64_t(i) * (kAlong ? a.Hp : PY == 2 ? a.lo * int64_t(a.Vp) : a.Vp) * 2);
     };
     const auto store = [&](Slice& r, int s, AR_LDS char* to) {
       const int col0 = kAlong ? s * kBK : at.m0;
@@ -1171,7 +1178,7 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
         }
       }
 #pragma unroll
-      for (int i = 0; i < PL; ++i) {
+      for (int i = 0; i < PY; ++i) {
         const uint32_t row = tid / 4;
         *reinterpret_cast<AR_LDS bf16x8*>(to + PL * C::kX + i * C::kY + row * 64 + ((tid % 4) ^ along_swizzle(row)) * 16) = r.y[i];
       }
@@ -1195,9 +1202,9 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
         store(r[i], s + i, here);
         load(r[i], s + i + kDeep);
         lds_barrier();  // the slice is there, and the one before the last has been multiplied
-        bf16x8 y[PL][PARTS];
+        bf16x8 y[PY][PARTS];
 #pragma unroll
-        for (int l = 0; l < PL; ++l)
+        for (int l = 0; l < PY; ++l)
 #pragma unroll
           for (int j = 0; j < PARTS; ++j) y[l][j] = read_along(here + PL * C::kX + l * C::kY, j * 16, lane);
 #pragma unroll
@@ -1209,10 +1216,10 @@ template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(Til
             else x[l] = read_across<C::BM>(here + l * C::kX, wm * C::MW + f * 16, lane);
           }
 #pragma unroll
-          for (int pass = 0; pass < (PL == 3 ? 6 : 1); ++pass)
+          for (int pass = 0; pass < (PL == 3 ? 6 : PY); ++pass)
 #pragma unroll
             for (int j = 0; j < PARTS; ++j)
-              acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
+              acc[f][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[plane_x(pass, PL)], y[PY == 2 ? 1 - pass : plane_y(pass, PL)][j], acc[f][j], 0, 0, 0);
         }
       }
     }
@@ -1245,6 +1252,7 @@ struct Soft {
   float* coef;   // [chunk rows]: the row's weight times Counts::share; 0 behind the rows
   float* exps;   // fp32: exp(z - m)
   char* d;
+  int32_t lo;    // as in Product
 };
 
 // What the rows' own ids are for.
@@ -1383,6 +1391,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
   __bf16* row = reinterpret_cast<__bf16*>(a.d) + int64_t(i) * (DT == D_BF16 ? 1 : 3) * a.Vp;
   if constexpr (DT == D_BF16) {
     row[id] = __bf16(d);
+    if (a.lo) row[a.lo * a.Vp + id] = __bf16(d - float(__bf16(d)));
   } else {
     __bf16 b[3];
     split3(d, b);
@@ -1398,7 +1407,8 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
   if (e.total && blockIdx.x + 1 == gridDim.x) put_total(a, e);
   constexpr int kBlocks = kNormCols / 64;  // no statistic covers fewer columns
   __shared__ float factor[kNormRows][kBlocks];
-  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows), end = (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK / kNormRows;
+  const int active = min(max(a.counts->active - a.chunk, 0), a.chunk_rows);
+  const int end = (a.lo && active ? a.lo : (active + 2 * kBK - 1) / (2 * kBK) * 2 * kBK) / kNormRows;
   const int64_t cols = (a.Vp + kNormCols - 1) / kNormCols, tiles = cols * end;
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const int r0 = int(tile / cols) * kNormRows;
@@ -1434,10 +1444,16 @@ template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normal
           const int r = r4 + q * kNormThreads / kLanes;
           const float f = factor[r][c8 / 64];
           if constexpr (DT == D_BF16) {
-            bf16x8 o;
+            bf16x8 o, o2;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __bf16(float(v[q][j]) * f);
-            *reinterpret_cast<bf16x8*>(reinterpret_cast<__bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8) = o;
+            for (int j = 0; j < 8; ++j) {
+              const float d = float(v[q][j]) * f;  // (a second term only few rows keep)
+              o[j] = __bf16(d);
+              o2[j] = __bf16(d - float(o[j]));
+            }
+            __bf16* to = reinterpret_cast<__bf16*>(a.d) + int64_t(r0 + r) * a.Vp + c0 + c8;
+            *reinterpret_cast<bf16x8*>(to) = o;
+            if (a.lo) *reinterpret_cast<bf16x8*>(to + a.lo * a.Vp) = o2;
           } else {
             bf16x8 o[3];
             split3_of<8>(v[q] * f, o);
@@ -1482,9 +1498,9 @@ template <int DT> __global__ __launch_bounds__(256) void k_vocab_own(Soft a, End
 
 // Partial gradients [splits][n][Hp] joined in order, into the outputs. Bound by memory: 67 MB into 8 in 14 us, 5.3 TB/s.
 template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Product a) {
-  const int n_end = DIR == S_WEIGHT ? a.Vp : chunk_active(a), per = a.Hp / 4;
+  const int n_end = DIR == S_WEIGHT ? a.Vp : chunk_active(a), per = a.Hp / 4, lo = DIR == S_HIDDEN ? a.lo : 0;
   const int64_t all = int64_t(n_end) * per;
-  const int splits = splits_of(a, n_end);
+  const int splits = splits_of(a, DIR == S_WEIGHT ? n_end : d_rows(a, n_end));
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 256) {
     const int n = int(i / per), m = int(i % per) * 4;
     if (m >= a.H) continue;
@@ -1498,16 +1514,19 @@ template <int DIR, int DT> __global__ __launch_bounds__(256) void k_vocab_sum(Pr
       row = p.dw + int64_t(n - p.start) * p.dld * e;
     }
     f32x4 s = {0, 0, 0, 0};
-    const float* from = a.part + int64_t(n) * a.Hp + m;
-    int k = 0;
-    for (; k + 8 <= splits; k += 8) {  // eight on their way together, added in order
-      f32x4 v[8];
+    const auto add = [&](const float* from) {
+      int k = 0;
+      for (; k + 8 <= splits; k += 8) {  // eight on their way together, added in order
+        f32x4 v[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const f32x4*>(from + (k + q) * a.part_stride);
+        for (int q = 0; q < 8; ++q) v[q] = *reinterpret_cast<const f32x4*>(from + (k + q) * a.part_stride);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) s += v[q];
-    }
-    for (; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(from + k * a.part_stride);
+        for (int q = 0; q < 8; ++q) s += v[q];
+      }
+      for (; k < splits; ++k) s += *reinterpret_cast<const f32x4*>(from + k * a.part_stride);
+    };
+    if (lo) add(a.part + int64_t(lo + n) * a.Hp + m);
+    add(a.part + int64_t(n) * a.Hp + m);
     s *= counts_of(a).factor;
     if constexpr (DT == D_BF16) put(reinterpret_cast<__bf16*>(row) + m, __builtin_convertvector(s, bf16x4), a.H - m);
     else put(reinterpret_cast<float*>(row) + m, s, a.H - m);
@@ -1535,8 +1554,10 @@ struct Plan {
   int64_t V = 0, Vp = 0, Tpad, Tc, chunks;
   bool packed;  // the output matrix is copied as bf16 terms
   bool few;     // or split on its way into few rows' products
+  int lo;       // D is two bf16 terms, the second ones from this row on; or 0
   Size logits, hidden, weight;
   int hidden_splits = 1, weight_splits = 1;
+  bool hidden_part = false;  // d_hidden's products leave partial sums
   int block;  // columns a statistic covers: a logits tile's
   int tile_rows;  // rows of a logits tile
   // offsets in the workspace
@@ -1577,6 +1598,12 @@ Plan plan_of(const Vocab& v, bool grad) {
   }
   p.few = p.packed && v.T <= kFewRows && v.H >= 8;  // (a whole vector in every row)
   if (p.few) p.packed = false;
+  // Few rows of bf16 keep D as two terms: a result has few terms there, whose roundings do not even out. As one bf16 value
+  // D left bf16 gradients of up to 128 rows as much as 2.2 times as far from 64 bits as an fp32 D does, of 129 and more 1.1
+  // to 1.6 times; as two, 1.00 times. The second terms are more rows of D (and the hidden rows are there twice), so that
+  // W is read once: us a call with gradients, so and with one term, 8 x 2048 x 32000 119 and 115, 48 x 256 x 1000 46.4
+  // and 43.7, 64 x 2048 x 32000 145 and 120. (100 x 2048 x 32000 took 195 and 147: more rows keep one.)
+  p.lo = grad && v.dtype == D_BF16 && v.T <= kFewRows ? (v.T <= 32 ? 32 : 64) : 0;
   p.Tpad = int64_t(up(size_t(std::max<int64_t>(v.T, 1)), kUnit));
   // a chunk's scratch: statistics at their finest, the own ids' logits, log-sum-exp and weight, and with gradients the
   // exponentials and D
@@ -1612,11 +1639,13 @@ Plan plan_of(const Vocab& v, bool grad) {
     p.exps = take(v.dtype == D_FP32 ? size_t(p.Tc) * size_t(p.Vp) * 4 : 0);
     p.d = take(size_t(p.Tc) * size_t(p.Vp) * size_t(p.planes) * 2);
     const int64_t hidden_steps = p.Vp / kBK * (p.few ? 1 : passes);
-    p.hidden = p.few ? few : size_for(v.H, n, hidden_steps / 8);
-    p.hidden_splits = splits_for(tiles_of(p.hidden, v.H, n), hidden_steps, n * p.Hp * 4);
+    const int64_t nd = p.lo && !p.few ? 2 * p.lo : n;
+    p.hidden = p.few ? few : size_for(v.H, nd, hidden_steps / 8);
+    p.hidden_splits = splits_for(tiles_of(p.hidden, v.H, nd), hidden_steps, nd * p.Hp * 4);
+    p.hidden_part = p.hidden_splits > 1 || (p.lo && !p.few);
     p.weight = size_for(v.H, p.Vp, 1);
-    if (p.chunks == 1) p.weight_splits = splits_for(tiles_of(p.weight, v.H, p.Vp), (n + kBK - 1) / kBK * passes, p.Vp * p.Hp * 4);
-    const size_t dh = p.hidden_splits > 1 ? size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp) * 4 : 0;
+    if (p.chunks == 1) p.weight_splits = splits_for(tiles_of(p.weight, v.H, p.Vp), ((p.lo ? 2 * p.lo : n) + kBK - 1) / kBK * passes, p.Vp * p.Hp * 4);
+    const size_t dh = p.hidden_part ? size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp) * 4 : 0;
     const size_t dw = p.weight_splits > 1 || p.chunks > 1 ? size_t(p.weight_splits) * size_t(p.Vp) * size_t(p.Hp) * 4 : 0;
     p.part = take(p.chunks > 1 ? dh + dw : std::max(dh, dw));  // chunks add to dW's across dh's
   }
@@ -1643,7 +1672,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   const bool each = v.reduction == R_NONE;
   const int64_t batches = (P + kPieceTab - 1) / kPieceTab, row_blocks = (p.Tpad + kRowWaves - 1) / kRowWaves;
   const bool sorted = p.Kp > kFewIds, pack_first = batches == 1 && v.T * p.Hp * p.planes <= kFewElements;
-  const int64_t per_chunk = 2 + (grad ? 3 + sorted + (p.hidden_splits > 1) + (p.chunks == 1 && p.weight_splits > 1) : 0);
+  const int64_t per_chunk = 2 + (grad ? 3 + sorted + p.hidden_part + (p.chunks == 1 && p.weight_splits > 1) : 0);
   s.left = batches + (v.top ? 1 : 0) + !pack_first + sorted + p.chunks * per_chunk + (grad ? p.chunks > 1 : !each);
   Piece* pieces = reinterpret_cast<Piece*>(ws + p.pieces);
   Counts* counts = reinterpret_cast<Counts*>(ws + p.counts);
@@ -1652,7 +1681,7 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   float2* teacher = reinterpret_cast<float2*>(ws + p.teacher);
   const Targets t{v.ids, v.logits, v.token_weights, v.ids_ld, v.logits_ld, v.ignore, p.V, v.top, v.logits_dtype, v.wide_ids, v.temperature};
   const PackArgs pa{v.hidden, v.ld, v.T, p.Tpad, int32_t(v.H), p.Hp, int32_t(P), pieces, rows, flags, counts, ws + p.hp,
-                    reinterpret_cast<int32_t*>(ws + p.idt), p.Kp, grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
+                    reinterpret_cast<int32_t*>(ws + p.idt), p.Kp, p.lo, grad ? v.dh : nullptr, v.dh_ld, each ? v.loss : nullptr};
   if (v.top) s.launch(k_vocab_teacher, blocks_of(row_blocks), kRowWaves * 64, t, v.T, teacher, flags);
   int64_t first = 0, start = 0;
   for (int64_t i0 = 0; i0 < P; i0 += kPieceTab) {
@@ -1708,13 +1737,13 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
   a.dh = v.dh;
   a.dh_ld = v.dh_ld;
   Soft f{counts, rows, v.token_weights, a.stats, p.Tc, int32_t(p.Vp / p.block), 0, 0, v.reduction, p.planes, p.block, p.Vp,
-         a.scale, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d};
+         a.scale, reinterpret_cast<float2*>(ws + p.lse), reinterpret_cast<float*>(ws + p.coef), reinterpret_cast<float*>(ws + p.exps), ws + p.d, p.lo};
   const auto rows_of = [&](int64_t c) { return std::min(p.Tc, std::max<int64_t>(v.T - c * p.Tc, 0)); };
   const auto join_blocks = [&](int64_t n) { return blocks_of(int64_t(up(size_t(n), kUnit)) / kJoinRows); };
   Ends ends{teacher, pa.idt, p.Kp, a.zt, reinterpret_cast<float*>(ws + p.row_loss), each ? v.loss : nullptr, nullptr};
   float* dh_part = reinterpret_cast<float*>(ws + p.part);
   float* dw_part = dh_part;
-  if (p.chunks > 1 && p.hidden_splits > 1) dw_part += size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp);
+  if (p.chunks > 1 && p.hidden_part) dw_part += size_t(p.hidden_splits) * size_t(p.Tc) * size_t(p.Hp);
   for (int64_t c = 0; c < p.chunks; ++c) {
     a.chunk = f.chunk = int32_t(c * p.Tc);
     a.chunk_rows = f.chunk_rows = int32_t(rows_of(c));
@@ -1743,17 +1772,20 @@ template <int DT> RunResult run_typed(const Vocab& v, bool grad, const Plan& p, 
     tile(p.hidden);
     a.mtiles = mtiles(p.hidden);
     a.splits = p.hidden_splits;
-    a.part = a.splits > 1 ? dh_part : nullptr;
+    a.part = p.hidden_part ? dh_part : nullptr;
+    a.lo = p.lo;
     a.part_stride = p.Tc * p.Hp;
     a.accumulate = 0;
-    launch_product<DT, S_HIDDEN, DT>(s, p, p.hidden, tiles_of(p.hidden, v.H, n), a);
-    if (a.splits > 1) s.launch(k_vocab_sum<S_HIDDEN, DT>, blocks_of((n * p.Hp / 4 + 255) / 256), 256, a);
+    launch_product<DT, S_HIDDEN, DT>(s, p, p.hidden, tiles_of(p.hidden, v.H, p.lo ? 2 * p.lo : n), a);
+    if (p.few) a.lo = 0;  // (its products are of both terms)
+    if (a.part) s.launch(k_vocab_sum<S_HIDDEN, DT>, blocks_of((n * p.Hp / 4 + 255) / 256), 256, a);
     tile(p.weight);
     a.mtiles = mtiles(p.weight);
     a.splits = p.weight_splits;
     a.part = a.splits > 1 || p.chunks > 1 ? dw_part : nullptr;
     a.part_stride = p.Vp * p.Hp;
     a.accumulate = c > 0;
+    a.lo = p.lo;
     launch_product<DT, S_WEIGHT, DT>(s, p, p.weight, tiles_of(p.weight, v.H, p.Vp), a);
     if (a.part && c + 1 == p.chunks) s.launch(k_vocab_sum<S_WEIGHT, DT>, blocks_of((p.Vp * p.Hp / 4 + 255) / 256), 256, a);
   }

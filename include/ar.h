@@ -418,9 +418,10 @@ ar_status ar_allreduce_clip_workspace_bytes(const int64_t* n, int32_t buckets, i
  *    (>= V; for cross entropy also a negative one that is not `ignore`) makes its row's loss, and so the
  *    call's, NaN, and gives no gradient.
  *  - Precision: logits, softmax and losses are fp32 (a call's loss is summed in 64 bits). bf16: products of the
- *    bf16 operands are exact and their sums fp32; d is rounded to bf16 once before the gradients' products (p before
- *    that to 2^-11 of it, or 2^-39 of the row's largest p), whose fp32 sums are rounded to bf16. fp32: operands are
- *    split into three bf16 terms (which hold all their bits down to 2^-133) and six products of them summed, 2^-24
+ *    bf16 operands are exact and their sums fp32; d is rounded to bf16 before the gradients' products (where T <= 64 to
+ *    two bf16 terms, 2^-16 of it; p before that to 2^-11 of it, or 2^-39 of the row's largest p; a mean's 1 / N and the
+ *    temperature are not rounded with it), whose fp32 sums are rounded to bf16. fp32: operands are split into three
+ *    bf16 terms (which hold all their bits down to 2^-133) and six products of them summed, 2^-24
  *    or so of a product; an infinite operand, whose other terms are 0, makes its products NaN. Logits, the teacher's
  *    too, are divided by the temperature after the row's largest has been subtracted (a difference past the largest
  *    fp32 value counts as infinite). Values below 2^-126 on the way may be lost. The order of every sum is fixed by

@@ -28,8 +28,9 @@ def teacher(logits, ids, temperature):
 
 
 def loss_and_gradients(hidden, weight, ids, logits=None, reduction="mean", temperature=1.0, token_weights=None,
-                       ignore_index=-100, dtype=None):
+                       ignore_index=-100, dtype=None, d_terms=1):
     """(loss, d_hidden, d_weight), and with dtype ("fp32" or "bf16", what a call computes in) their bounds behind them.
+    d_terms: of how many bf16 values, each the rounding of what the ones before leave, a bf16 call's D is the sum.
 
     The bounds, all in absolute terms, with A = |h| |W|^T / temperature:
     * logits: H products and sums in fp32, and a rounding of the scale: (H + 8) U A; fp32 operands are three bf16
@@ -37,7 +38,7 @@ def loss_and_gradients(hidden, weight, ids, logits=None, reduction="mean", tempe
     * statistics: a shift of all logits by at most dz changes log-sum-exp by at most that; exponentials are off by 4 U
       and what rounds their argument, U (|z| + |lse|) log2(e), sums by U for each of at most 192 levels;
     * losses: both, the target's own logit, and a rounding of every operation (16 U of every term);
-    * D = c (p - q): p's relative error is that of its exponent; in bf16 D is rounded, U_BF16, and exp(z - m) to fp16
+    * D = c (p - q): p's relative error is that of its exponent; in bf16 D is rounded, U_BF16 to the power of d_terms, and exp(z - m) to fp16
       times 2^14, 2^-11 of it or, below the smallest normal value, 2^-25, which is 2^-39 of the largest; in fp32 a
       few U;
     * products of D: its error times the other operand, a sum of fp32 terms in any order (n U of the terms'
@@ -104,10 +105,10 @@ def loss_and_gradients(hidden, weight, ids, logits=None, reduction="mean", tempe
     dD = c.abs() * dp + 8 * U * (c.abs() * p)
     if dtype == "bf16":
         most_p = p.max(1, keepdim=True)[0] if len(take) else p.new_zeros(0, 1)
-        dD = dD + 1.01 * (U_BF16 + 2.0 ** -11) * (c.abs() * p) + 2.0 ** -39 * (c.abs() * most_p)
+        dD = dD + 1.01 * (U_BF16 ** d_terms + 2.0 ** -11) * (c.abs() * p) + 2.0 ** -39 * (c.abs() * most_p)
     own_q = torch.zeros_like(p).scatter_add_(1, at, q)
     dq = own_q * (K + 64) * U * (1 + (float(log_q.abs().max()) if log_q.numel() else 0.0))
-    dD = dD + c.abs() * (dq + 4 * U * own_q) + (U_BF16 if dtype == "bf16" else U) * 1.01 * torch.where(own_q > 0, D.abs(), torch.zeros_like(D))
+    dD = dD + c.abs() * (dq + 4 * U * own_q) + (U_BF16 ** d_terms + 2 * U if dtype == "bf16" else U) * 1.01 * torch.where(own_q > 0, D.abs(), torch.zeros_like(D))
     tiny = 2.0 ** -126
     dD = dD + tiny * (2 * c.abs() + 2)
     last = U_BF16 if dtype == "bf16" else 2 * U

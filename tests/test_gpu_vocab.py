@@ -848,3 +848,18 @@ def test_a_means_factor_is_not_rounded_into_d(T, H, V, top, dtype):
     u = {"bf16": 2 * ov.U_BF16 + 4 * ov.U, "fp32": 6 * ov.U}[dtype] * 1.01
     for mean, total in ((dh, sh), (dw[0], sw[0])):
         within(mean * 1.0, total.double() / n, u * total.double().abs() / n + 2.0 ** -120, "a mean's gradient")
+
+
+@pytest.mark.parametrize("T,H,V", [(1, 64, [300]), (3, 256, [5000, 37]), (16, 61, [1000]), (17, 128, [20000]), (48, 64, [700, 300]),
+                                   (64, 200, [3000]), (64, 33, [257]), (50, 2048, [9000])])
+@pytest.mark.parametrize("top", [0, 3, 8])
+def test_few_rows_gradients_in_bf16_keep_two_terms_of_d(T, H, V, top):
+    """Up to 64 rows D is the sum of two bf16 values: off by 2^-16 of it where one would be by 2^-8, which few terms of a
+    result do not even out."""
+    torch = torch_mod()
+    c = Case(T, H, V, "bf16", top, seed=51, weights=T > 3, left_out=0.1 if T > 3 else 0.0, temperature=0.7)
+    loss, dh, dw = c.run()
+    want = c.want(d_terms=2)
+    within(loss, want[0], want[3], "loss")
+    within(dh, want[1], want[4], "d_hidden")
+    within(torch.cat(dw), want[2], want[5], "d_weight")
