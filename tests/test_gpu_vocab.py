@@ -863,3 +863,16 @@ def test_few_rows_gradients_in_bf16_keep_two_terms_of_d(T, H, V, top):
     within(loss, want[0], want[3], "loss")
     within(dh, want[1], want[4], "d_hidden")
     within(torch.cat(dw), want[2], want[5], "d_weight")
+
+
+@pytest.mark.parametrize("limit", [1, 3])
+def test_launch_limit_of_few_rows(limit):
+    """Two terms of D, in the tiles that load W as it is and in those that bring it in order."""
+    A = lib()
+    cases = [Case(T, H, [300, 30], "bf16", top=top, seed=52, left_out=0.2) for T, H, top in ((20, 64, 0), (50, 64, 6), (50, 61, 3), (9, 33, 0))]
+    prev = A.ar_set_launch_blocks(limit)
+    try:
+        for c in cases:
+            c.check()
+    finally:
+        A.ar_set_launch_blocks(prev)
