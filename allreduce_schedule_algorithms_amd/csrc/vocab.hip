@@ -25,8 +25,8 @@
 // a row's lse is known, one pass turns them into D. Nothing is added atomically: the
 // same sizes give the same bits on every run.
 //
-// 8192 tokens x 4096 x 128000 in bf16, 8 pieces, with gradients: 21.1 ms, of which products 6.85 + 6.38 + 6.95
-// (1254, 1346 and 1235 TFLOP/s), D 0.77, the rest 0.08.
+// 8192 tokens x 4096 x 128000 in bf16, 8 pieces, with gradients: 21.1 ms, of which products 6.88 + 6.51 + 6.91
+// (1249, 1321 and 1244 TFLOP/s), D 0.74, the rest 0.07. (Cards differ by some 3%.)
 #include "vocab.h"
 
 #include <hip/hip_ext.h>
@@ -346,7 +346,7 @@ template <int DT> __global__ __launch_bounds__(kRowWaves * 64) void k_vocab_pack
 
 // More ids a row than kFewIds are sorted by the tile of logits that they lie in, so that a tile finds its own: one
 // workgroup for the rows of a tile counts them, adds the counts up and deals the entries out. (Where an entry lies
-// among its tile's does not show in any result.) 3687 rows x 64 ids: 22 us, after which the logits of 50000 took 887;
+// among its tile's does not show in any result.) 3687 rows x 64 ids: 22 us, after which the logits of 50000 took 886;
 // with tiles that compare all of their rows' ids, 1176.
 constexpr int kFewIds = 4, kSortThreads = 1024;
 __global__ __launch_bounds__(kSortThreads) void k_vocab_sort(const int32_t* idt, int ld_idt, int bn, int bm, int mtiles, int64_t row_tiles, const Counts* counts, int32_t* starts, uint32_t* entries) {
@@ -966,11 +966,12 @@ template <class C, int DIR, int KEEP> __device__ __forceinline__ void put_gradie
 
 // KEEP: what a logits tile leaves behind: 0 only its sums, D_BF16 or D_FP32 the exponentials. The other directions:
 // the outputs' type.
-// Bound by power where tiles are many: at 8192 x 4096 x 128000 the matrix pipes are busy for 64-72% of the time, the
-// clock at 1.8-1.9 GHz, 1235-1346 TFLOP/s (on zeros, 2.3 GHz at the same share). 256 x 256 outputs for 8 waves are
+// Where tiles are many the matrix pipes are busy for 64-71% of the time at 8192 x 4096 x 128000, at the 1.8-1.9 GHz that
+// power leaves, 1244-1321 TFLOP/s (on zeros, 2.3 GHz at the same share): the other third is what a SIMD's two waves
+// wait for together, at the barrier of every slice. 256 x 256 outputs for 8 waves are
 // what the accumulators hold: each slice's 32 KB are read into LDS for 4.2 MFLOP. With 64 deep double buffers the three
 // took 7.8, 9.2 and 9.3 ms in place of 6.8, 6.4 and 7.0; in 32 x 32 x 16 products 2-8% more than in 16 x 16 x 32.
-// Of up to 64 rows the reading of the output matrix bounds it: 8 x 2048 x 32000 in 25 us, 5.3 TB/s.
+// Of up to 64 rows the reading of the output matrix bounds it: 8 x 2048 x 32000 in 25 us, 5.4 TB/s.
 template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, C::kWaves) void k_vocab_product(Product a) {
   __shared__ __attribute__((aligned(512))) char shared[C::kStages * C::kStage];
   using St = Stager<C, DIR>;
@@ -1083,8 +1084,8 @@ template <class C, int DIR, int KEEP> __global__ __launch_bounds__(C::kThreads, 
 // Few rows against an output matrix that loads into LDS cannot bring as bf16 (fp32, or rows at odd addresses): the
 // products read it as it is, split it into terms on the way to LDS and multiply all terms of a slice at once, where
 // many rows are better served by a copy (which reads, writes and reads again what is read once here). S_LOGITS and
-// S_HIDDEN only: the output matrix is X. (us a loss of 2048 x 32000, so and with a copy: fp32 of 8 rows 74 and 297, of 64
-// 98 and 297; bf16 of 64 rows of odd width 52 and 86.) kDeep slices are on their way in registers. PARTS: sixteen rows
+// S_HIDDEN only: the output matrix is X. (us a loss of 2048 x 32000, so and with a copy: fp32 of 8 rows 77 and 292, of 64
+// 92 and 294; bf16 of 64 rows of odd width 49 and 86.) kDeep slices are on their way in registers. PARTS: sixteen rows
 // each, of which products are formed.
 constexpr int kFewRows = 64, kDeep = 3;
 template <int DT, int DIR, int KEEP, int PARTS> __global__ __launch_bounds__(TileF<DT>::kThreads, TileF<DT>::kWaves) void k_vocab_few(Product a) {
@@ -1282,8 +1283,8 @@ struct Teacher {
 __device__ __forceinline__ Teacher teacher_of(const Targets& t, const Ends& e, int64_t row) { return Teacher{t, row, t.K ? e.teacher[row] : float2{0, 1}}; }
 
 // The rows' softmax statistics, weights and losses, 16 rows a workgroup: first a wave's lanes are 16 rows x 4
-// statistics, and its 16 waves share the statistics; then each wave takes a row's ids. 8192 rows x 500 statistics: 34
-// us; few rows take 6, a chain of waits for memory.
+// statistics, and its 16 waves share the statistics; then each wave takes a row's ids. 8192 rows x 500 statistics: 25
+// us; few rows take 4, a chain of waits for memory.
 constexpr int kJoinThreads = 1024, kJoinRows = 16;
 __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Targets t) {
   __shared__ float2 part[kJoinThreads / 64][kJoinRows];
@@ -1359,7 +1360,8 @@ __global__ __launch_bounds__(kJoinThreads) void k_vocab_join(Soft a, Ends e, Tar
 }
 
 // The call's loss from its rows' (of launches before): one workgroup adds them up, in 64 bits and in an order that their
-// number fixes.
+// number fixes: beside the normalizing pass, or in 2 to 5 us behind the join (whose last workgroup, known by a counter, took a
+// call no less time).
 constexpr int kNormThreads = 256;
 __device__ __forceinline__ void put_total(const Soft& a, const Ends& e) {
   __shared__ double wave_sum[kNormThreads / 64];
@@ -1401,7 +1403,7 @@ template <int DT> __device__ __forceinline__ void put_own(const Soft& a, const E
 }
 
 // exp(z - m) -> c p (c but for Counts::factor), in place for bf16, 16 rows x 512 columns a workgroup: every statistic's factor once, then 16 bytes a lane.
-// Bound by memory: 8192 x 128000 in bf16, 2.1 GB each way, take 767 us, 5.6 TB/s.
+// Bound by memory: 8192 x 128000 in bf16, 2.1 GB each way, take 744 us, 5.7 TB/s.
 constexpr int kNormRows = 16, kNormCols = 512, kBatch = 4;
 template <int DT> __global__ __launch_bounds__(kNormThreads) void k_vocab_normalize(Soft a, Ends e, Targets t) {
   if (e.total && blockIdx.x + 1 == gridDim.x) put_total(a, e);
@@ -1546,7 +1548,7 @@ enum Size { Z_S = 0, Z_M = 1, Z_L = 2, Z_F = 3 };
 constexpr int64_t kChunkBytes = int64_t(4) << 30;
 constexpr int kUnits = 256;  // compute units
 // Hidden elements that the first launch's one workgroup packs itself rather than leaving them to another launch.
-// (us a loss, so and with the launch: 16 x 64 fp32 27.2 and 28.2, 8 x 2048 bf16 46.6 and 42.6, 48 x 256 31.6 and 27.0.)
+// (us a loss, so and with the launch: 16 x 64 fp32 26.7 and 26.6, 8 x 2048 bf16 45.7 and 41.8, 48 x 256 31.6 and 26.8.)
 constexpr int64_t kFewElements = 4096;
 
 struct Plan {
@@ -1579,7 +1581,7 @@ Size size_for(int64_t m, int64_t n, int64_t splits) {
 }
 
 // How often a product's depth is split so that its tiles fill the device (us a call with gradients, so and unsplit:
-// 8 x 2048 x 32000 122 and 276, 1024 x 1024 x 32000 288 and 804, 48 x 256 x 1000 50 and 53).
+// 8 x 2048 x 32000 117 and 287, 1024 x 1024 x 32000 271 and 796, 48 x 256 x 1000 47 and 54).
 int splits_for(int64_t tiles, int64_t steps, int64_t part_bytes) {
   const int64_t want = (2 * kUnits) / std::max<int64_t>(tiles, 1), most = std::min<int64_t>(steps / 4, (int64_t(256) << 20) / std::max<int64_t>(part_bytes, 1));
   return int(std::max<int64_t>(1, std::min(want, most)));
